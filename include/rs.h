@@ -22,6 +22,9 @@
  *   rs_block_dequant    the inverse of rs_block_quant
  *   rs_unpack_dequant   gathered codes + scales -> the quantised full tensors
  *   rs_adam8_step       one AdamW step on block-quantised int8 / uint8 state
+ *   rs_orthogonalize    Newton-Schulz orthogonalisation of the WHOLE matrices
+ *   rs_muon_step        one Muon step on the WHOLE matrices
+ *   rs_muon_workspace   bytes of workspace the two need
  *   rs_last_error       text of the calling thread's last error
  *
  * Conventions
@@ -166,7 +169,8 @@ int rs_plan_build(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t ali
  * integer E4M3 encoder instead of gfx950's conversion instruction;
  * RS_TM_KERNEL=direct runs the tile-major reorder of unpack / pack with
  * direct per-lane kernels instead of staging it through LDS. Both give
- * identical results.
+ * identical results. RS_MUON_TILE=128|256 forces the output tile of the
+ * matrix products (rs_orthogonalize, rs_muon_step).
  * On success *out owns host memory and one device allocation, released by
  * rs_plan_free. Errors: the above, RS_ENOMEM, RS_EHIP. */
 int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,
@@ -329,6 +333,70 @@ typedef struct rs_adam_hparams {
  * lr / wd), RS_EALIGN, RS_EHIP. */
 int rs_adam8_step(rs_plan* plan, float* param, const float* grad, void* q_m, float* s_m,
                   void* q_v, float* s_v, const rs_adam_hparams* hp, void* stream);
+
+/* Orthogonalisation of every matrix of the plan by Newton-Schulz products
+ * (feynmanwiki walkthrough, Muon paragraphs: the rank that holds a matrix
+ * whole runs Newton-Schulz on it, which is what RS_WHOLE blocks are for). A
+ * matrix is a WHOLE tensor of more than one row and one column; other tensors
+ * and padding are neither read nor written. For each matrix G (X is G, or its
+ * transpose where rows > cols):
+ *   X = G / (|G|_F + eps);
+ *   for t in 0 .. steps-1:  A = X X^T,  X = (a_t I + b_t A + c_t A^2) X,
+ * and out gets X (transposed back) rounded once to the nearest bf16.
+ * Products take fp16 operands with fp32 sums; X is carried as a high and a
+ * low fp16 part and the diagonals of A and of the polynomial in fp32, which
+ * keeps the result within about 1e-3 of the exact one (Frobenius norm), ahead
+ * of the bf16 rounding. The polynomials must keep every singular value below
+ * 7 (A is held to 2^16 / 2^10) and the off-diagonal entries of b A + c A^2
+ * below 60. The norm is summed in fp64. The sums have a fixed order: the same
+ * call gives the same bits. A zero matrix gives zeros; a NaN or an infinity
+ * makes its own matrix's result NaN and leaves the others alone.
+ * src: device, R_mat*S elements of src_dt (RS_F32 or RS_BF16). out: device
+ * bf16, R_mat*S elements, not overlapping src. coeffs: HOST array of 3*steps
+ * floats a_t, b_t, c_t (finite). steps: 1 to 32. eps >= 0 (with eps = 0 a
+ * zero matrix gives NaN). work: device memory of rs_muon_workspace bytes,
+ * whose contents need not be kept between calls; calls that may overlap (on
+ * other streams, or in graphs that may) need a workspace each. All 16-byte
+ * aligned. A matrix needs both sides at most 2^20 and one at most 2^16.
+ * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
+int rs_orthogonalize(rs_plan* plan, const void* src, int32_t src_dt, void* out, const float* coeffs,
+                     int32_t steps, float eps, void* work, int64_t work_bytes, void* stream);
+
+/* Factor on an update's rate: 1; sqrt(max(1, rows/cols)); or
+ * 0.2 * sqrt(max(rows, cols)), which gives an orthogonal matrix the root mean
+ * square of a usual AdamW update. */
+enum { RS_MUON_SCALE_NONE = 0, RS_MUON_SCALE_SPECTRAL = 1, RS_MUON_SCALE_RMS = 2 };
+
+typedef struct rs_muon_hparams {
+  float lr;
+  float momentum;      /* mu, in [0, 1) */
+  float weight_decay;  /* decoupled */
+  float eps;           /* >= 0, added to the norm */
+  int32_t steps;       /* Newton-Schulz steps, 1 to 32 */
+  int32_t nesterov;    /* 0 or 1 */
+  int32_t scale_mode;  /* RS_MUON_SCALE_* */
+} rs_muon_hparams;
+
+/* One Muon step on every matrix of the plan (see rs_orthogonalize), in place;
+ * per matrix, f its factor from scale_mode, all in fp32:
+ *   momentum = mu * momentum + grad
+ *   U = nesterov ? grad + mu * momentum : momentum
+ *   param = param * (1 - lr * weight_decay) - lr * f * orthogonalise(U)
+ * The other tensors of the group and the padding are left as they are (they
+ * take another optimiser, e.g. rs_adam8_step on their quantisation blocks).
+ * A NaN or an infinity in U makes that matrix's parameters NaN.
+ * param, momentum: device fp32 R_mat*S, in place. grad: device R_mat*S of
+ * grad_dt (RS_F32 or RS_BF16), e.g. from rs_pack_scatter. The three do not
+ * overlap. coeffs: HOST array of 3*hp->steps floats. work, work_bytes: as in
+ * rs_orthogonalize. Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE,
+ * RS_EHIP. */
+int rs_muon_step(rs_plan* plan, float* param, const void* grad, int32_t grad_dt, float* momentum,
+                 const rs_muon_hparams* hp, const float* coeffs, void* work, int64_t work_bytes, void* stream);
+
+/* Bytes of workspace that rs_orthogonalize and rs_muon_step need for this
+ * plan (about 8 per element of its matrices and 4 per element of their smaller
+ * Gram matrices; half as much again for sides of at most 64). Errors: RS_EINVAL. */
+int rs_muon_workspace(const rs_plan* plan, int64_t* bytes);
 
 /* Message for the calling thread's last failed call ("" if none). The
  * pointer stays valid until the thread's next rs_* call. */

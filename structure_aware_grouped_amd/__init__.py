@@ -4,6 +4,7 @@ The work runs in librs_hip.so (hand-written HIP kernels behind a C ABI, see
 include/rs.h); ``binding`` exposes its calls under the same names.
 """
 from .binding import (  # noqa: F401
+    MUON_COEFFS,
     Plan,
     PlanSpec,
     plan_from_json,
@@ -14,6 +15,9 @@ from .binding import (  # noqa: F401
     rs_block_dequant,
     rs_block_quant,
     rs_block_quant_noalloc,
+    rs_muon_step,
+    rs_muon_workspace,
+    rs_orthogonalize,
     rs_pack_scatter,
     rs_plan_build,
     rs_plan_load,

@@ -27,7 +27,7 @@ RS_F32, RS_BF16, RS_E4M3, RS_I8, RS_U8 = 0, 1, 2, 3, 4
 CODE_FORMATS = {"e4m3": RS_E4M3, "i8": RS_I8, "u8": RS_U8}
 EXPORTS = ("rs_plan_build", "rs_plan_load", "rs_plan_info", "rs_plan_free", "rs_unpack_gathered",
            "rs_pack_scatter", "rs_block_quant", "rs_block_dequant", "rs_unpack_dequant", "rs_adam8_step",
-           "rs_last_error", "rs_block_quant_noalloc")
+           "rs_last_error", "rs_block_quant_noalloc", "rs_orthogonalize", "rs_muon_step", "rs_muon_workspace")
 
 
 class RsError(RuntimeError):
@@ -40,6 +40,12 @@ class AdamHParamsC(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("step", ctypes.c_int64)]
+
+
+class MuonHParamsC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("eps", ctypes.c_float), ("steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
+                ("scale_mode", ctypes.c_int32)]
 
 
 class TensorSpecC(ctypes.Structure):
@@ -76,6 +82,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rs_adam8_step.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(AdamHParamsC), P]
     lib.rs_block_quant_noalloc.argtypes = [ctypes.POINTER(TensorSpecC), I64, I64, I64, PI64, I64, P, I32, P, I32,
                                            P, I64, P]
+    PF = ctypes.POINTER(ctypes.c_float)
+    lib.rs_orthogonalize.argtypes = [P, P, I32, P, PF, I32, F, P, I64, P]
+    lib.rs_muon_step.argtypes = [P, P, P, I32, P, ctypes.POINTER(MuonHParamsC), PF, P, I64, P]
+    lib.rs_muon_workspace.argtypes = [P, PI64]
     lib.rs_last_error.argtypes = []
     lib.rs_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -361,6 +371,93 @@ def rs_adam8_step(plan: Plan, param: torch.Tensor, grad: torch.Tensor, q_m: torc
     hp = AdamHParamsC(lr, beta1, beta2, eps, weight_decay, 0, int(step))
     _check(load().rs_adam8_step(plan.handle, param.data_ptr(), grad.data_ptr(), q_m.data_ptr(), s_m.data_ptr(),
                                 q_v.data_ptr(), s_v.data_ptr(), ctypes.byref(hp), _stream(plan.device)))
+
+
+# ---------------------------------------------------------------- whole matrices
+
+# a, b, c of the quintic of the published Muon optimiser: singular values in (0, 1] go to
+# about [0.7, 1.2] in five steps
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+UPDATE_SCALES = {"none": 0, "spectral": 1, "rms": 2}
+
+
+def _coeffs(coeffs, steps: int) -> ctypes.Array:
+    """3 * steps floats: one (a, b, c) for every step, or a sequence of one per step."""
+    rows = list(coeffs)
+    if rows and not hasattr(rows[0], "__len__"):
+        rows = [rows] * int(steps)
+    if len(rows) != int(steps) or any(len(r) != 3 for r in rows):
+        raise ValueError("coeffs: (a, b, c), or one (a, b, c) per step")
+    flat = [float(v) for r in rows for v in r]
+    return (ctypes.c_float * max(len(flat), 1))(*flat)
+
+
+def _flat_check(plan: Plan, t: torch.Tensor, dtypes, what: str):
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    if t.numel() < plan.R_mat * plan.S:
+        raise ValueError(f"{what} shorter than R_mat * S")
+
+
+def _apart_check(**tensors: torch.Tensor):
+    """The named buffers share no byte: the kernels read some while they write others."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), k) for k, t in tensors.items())
+    for (_, end, a), (start, stop, b) in zip(spans, spans[1:]):
+        if start < end and start < stop:
+            raise ValueError(f"{a} and {b} overlap")
+
+
+def _work_check(work: torch.Tensor, need: int):
+    if work.dtype != torch.uint8 or work.numel() < need:
+        raise ValueError(f"work: uint8 with at least {need} entries")
+
+
+def _muon_bytes(plan: Plan) -> int:
+    n = ctypes.c_int64()
+    _check(load().rs_muon_workspace(plan.handle, ctypes.byref(n)))
+    return n.value
+
+
+def rs_muon_workspace(plan: Plan) -> torch.Tensor:
+    """Workspace for rs_orthogonalize and rs_muon_step on this plan (uint8, on the plan's
+    device). Calls that may overlap need a workspace each."""
+    return torch.empty(max(_muon_bytes(plan), 1), dtype=torch.uint8, device=f"cuda:{plan.device}")
+
+
+def rs_orthogonalize(plan: Plan, src: torch.Tensor, out: torch.Tensor, work: torch.Tensor,
+                     coeffs=MUON_COEFFS, steps: int = 5, eps: float = 1e-7):
+    """out <- the Newton-Schulz orthogonalisation of every WHOLE matrix of the flat buffer src
+    (fp32 or bf16), in bf16; the rest of out is left as it is."""
+    _dev_check(plan, src, out, work)
+    _flat_check(plan, src, (torch.float32, torch.bfloat16), "src")
+    _flat_check(plan, out, (torch.bfloat16,), "out")
+    _work_check(work, _muon_bytes(plan))
+    _apart_check(src=src, out=out, work=work)
+    _check(load().rs_orthogonalize(plan.handle, src.data_ptr(), RS_F32 if src.dtype == torch.float32 else RS_BF16,
+                                   out.data_ptr(), _coeffs(coeffs, steps), int(steps), float(eps), work.data_ptr(),
+                                   work.numel(), _stream(plan.device)))
+
+
+def rs_muon_step(plan: Plan, param: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, work: torch.Tensor,
+                 lr: float, momentum_decay: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True,
+                 update_scale: str = "rms", coeffs=MUON_COEFFS, steps: int = 5, eps: float = 1e-7):
+    """One Muon step on every WHOLE matrix, in place: param and momentum (fp32 flat) with the
+    packed gradient (fp32 or bf16). update_scale: "none", "spectral" (sqrt(max(1, rows/cols)))
+    or "rms" (0.2 sqrt(max(rows, cols)))."""
+    _dev_check(plan, param, grad, momentum, work)
+    _flat_check(plan, param, (torch.float32,), "param")
+    _flat_check(plan, momentum, (torch.float32,), "momentum")
+    _flat_check(plan, grad, (torch.float32, torch.bfloat16), "grad")
+    _work_check(work, _muon_bytes(plan))
+    _apart_check(param=param, grad=grad, momentum=momentum, work=work)
+    if update_scale not in UPDATE_SCALES:
+        raise ValueError(f"update_scale: one of {sorted(UPDATE_SCALES)}")
+    hp = MuonHParamsC(lr, momentum_decay, weight_decay, eps, int(steps), int(bool(nesterov)),
+                      UPDATE_SCALES[update_scale])
+    _check(load().rs_muon_step(plan.handle, param.data_ptr(), grad.data_ptr(),
+                               RS_F32 if grad.dtype == torch.float32 else RS_BF16, momentum.data_ptr(),
+                               ctypes.byref(hp), _coeffs(coeffs, steps), work.data_ptr(), work.numel(),
+                               _stream(plan.device)))
 
 
 def rs_block_quant_noalloc(specs, V: int, S: int, starts: Sequence[int], R_mat: int, src: torch.Tensor,

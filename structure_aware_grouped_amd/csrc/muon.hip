@@ -1,0 +1,725 @@
+// Orthogonalisation of whole matrices by Newton-Schulz products, and the Muon
+// step built on it, on gfx950: kernels and the rs_orthogonalize /
+// rs_muon_step / rs_muon_workspace entry points ("veScale-FSDP: flexible,
+// structure-aware sharding at 10K-GPU scale", feynmanwiki walkthrough, Muon
+// paragraphs: a rank that holds a whole matrix runs Newton-Schulz on it).
+//
+// Mathematics, for a matrix G (X is G or its transpose, m x n with m <= n):
+//   X <- G / (|G|_F + eps);  `steps` times:  X <- (a I + b A + c A^2) X,
+//   A = X X^T.
+// Every product has the form  C[i, j] = sum_k P[i, k] Q[j, k]  with k
+// contiguous in both operands: A from X and X; A^2 from A and A (symmetric);
+// the polynomial times X from the symmetric polynomial and X^T, which is kept
+// beside X. A and A^2 are symmetric, so only tiles on and below the diagonal
+// are computed and each is stored twice.
+//
+// Number formats. Products run on fp16 operands with fp32 sums
+// (v_mfma_f32_32x32x16_f16): at the same rate as bf16, fp16 rounds 8 times
+// finer, and every operand here has a known size, so fp16's range is no
+// limit: X is stored times 2^ex (about sqrt(n)), A and the polynomial times
+// 2^10. Three things that fp16 alone would spoil are kept apart:
+//   - X as a high and a low fp16 part. A gradient with few strong directions
+//     has its weak ones below the rounding error of the strong ones, and the
+//     steps raise them. With the polynomial as d_i on the diagonal (fp32)
+//     plus the rest (fp16), d_i acts on both parts and only the rest is
+//     multiplied with the high part alone. While a row of X is short (A_ii at
+//     most 1/2: early steps) d_i = a, so the rest spans the strong directions
+//     only and drops nothing from the weak ones; later d_i is the whole
+//     diagonal, so the rest is small where A is near the identity.
+//   - the diagonal of A in fp32, zeros in its place in the fp16 operand.
+// A matrix of few rows has few singular values, so its error is that of the
+// worst of them, and the published polynomial's slope reaches 1.6: for
+// m <= kMatTwoPart all operands have a high and a low part, and a product is
+// high * low + low * high + high * high.
+// On simulated matrices of 48 to 2048 rows with one part, with spectra flat, falling by 10^4
+// or of a few directions 100 times above the others, the relative error of
+// the result against 64 bits is 2e-4 to 1.4e-3; plain fp16 operands give 1e-3
+// to 4e-2, bf16 ones 1e-2 and more.
+#include "host_common.h"
+
+namespace rs {
+namespace {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+constexpr float kOpScale = 1024.0f;          // stored A and polynomial: value * 2^10
+constexpr float kLowScale = 2048.0f;         // stored low part of X: (x - high) * 2^11
+
+// What a call does to each matrix beside the products.
+struct MuonK {
+  float a, b, c;       // polynomial of this step
+  float mu;            // momentum decay
+  float lr, decay;     // decay = 1 - lr * weight_decay
+  int32_t nesterov, scale_mode;
+};
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, bool bf16) {
+  return bf16 ? In<true>::elem(p, i) : In<false>::elem(p, i);
+}
+
+// ------------------------------------------------------------------ momentum and norm
+
+// One chunk of one matrix: m <- mu m + g (fp32, in place) where there is a
+// momentum, and the chunk's sum of squares of the matrix to orthogonalise
+// (g, m, or g + mu m). Squares and sums are fp64: an fp32 square would
+// overflow from 1e19 and vanish below 1e-23.
+template <bool BF16, bool MUON>
+__global__ __launch_bounds__(kThreads) void mat_norm_kernel(const MuonMat* __restrict__ mats,
+                                                            const MatChunk* __restrict__ jobs, const void* grad,
+                                                            float* mom, char* work, MuonK k) {
+  __shared__ double red[kThreads / kWave];
+  const MatChunk job = jobs[blockIdx.x];
+  const MuonMat& q = mats[job.mat];
+  const int64_t n = static_cast<int64_t>(q.rows) * q.cols, off = static_cast<int64_t>(job.chunk) * kMatChunk;
+  const int64_t base = q.start + off;
+  const int len = static_cast<int>(n - off < kMatChunk ? n - off : kMatChunk);
+  double sum = 0.0;
+  auto one = [&](float g, float& m) {
+    if constexpr (MUON) {
+      m = __fadd_rn(__fmul_rn(k.mu, m), g);
+      g = k.nesterov ? __fadd_rn(g, __fmul_rn(k.mu, m)) : m;
+    }
+    sum += static_cast<double>(g) * static_cast<double>(g);
+  };
+  const int nv = len / 8;   // base is a multiple of 16 elements
+  for (int v = threadIdx.x; v < nv; v += kThreads) {
+    float x[8], m[8] = {};
+    if constexpr (BF16) {
+      In<true>::widen(*reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(grad) + base + v * 8), x);
+    } else {
+      const f32x4* gp = reinterpret_cast<const f32x4*>(static_cast<const float*>(grad) + base + v * 8);
+      const f32x4 g0 = gp[0], g1 = gp[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { x[e] = g0[e]; x[4 + e] = g1[e]; }
+    }
+    f32x4* mp = reinterpret_cast<f32x4*>(mom + base + v * 8);
+    if constexpr (MUON) {
+      const f32x4 m0 = mp[0], m1 = mp[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { m[e] = m0[e]; m[4 + e] = m1[e]; }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) one(x[e], m[e]);
+    if constexpr (MUON) {
+      mp[0] = f32x4{m[0], m[1], m[2], m[3]};
+      mp[1] = f32x4{m[4], m[5], m[6], m[7]};
+    }
+  }
+  for (int e = nv * 8 + threadIdx.x; e < len; e += kThreads) {
+    float m = 0.0f;
+    if constexpr (MUON) m = mom[base + e];
+    one(load_elem(grad, base + e, BF16), m);
+    if constexpr (MUON) mom[base + e] = m;
+  }
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / kWave; ++w) sum += red[w];
+    reinterpret_cast<double*>(work + q.part)[job.chunk] = sum;
+  }
+}
+
+// 2^ex / (norm + eps) of each matrix, one workgroup per matrix; the partial
+// sums are added in a fixed order.
+__global__ __launch_bounds__(kThreads) void mat_scale_kernel(const MuonMat* __restrict__ mats, char* work, double eps) {
+  __shared__ double red[kThreads / kWave];
+  const MuonMat& q = mats[blockIdx.x];
+  const double* part = reinterpret_cast<const double*>(work + q.part);
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < q.n_part; i += kThreads) sum += part[i];
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / kWave; ++w) sum += red[w];
+    *reinterpret_cast<double*>(work + q.inv) = static_cast<double>(1 << q.ex) / (sqrt(sum) + eps);
+  }
+}
+
+// x as a high and a low fp16 part.
+__device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
+  hi = static_cast<_Float16>(x);
+  lo = static_cast<_Float16>((x - static_cast<float>(hi)) * kLowScale);
+}
+
+__device__ __forceinline__ h8 low_parts(const float (&v)[8]) {
+  h8 h;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    _Float16 hi, lo;
+    split(v[t], hi, lo);
+    h[t] = lo;
+  }
+  return h;
+}
+
+// One 64 x 64 tile of X from the gradient (and momentum): scaled, split, and
+// written as X's high and low parts and the transposed high part (for
+// m <= kMatTwoPart the low one too), zeros in the padding of the contraction dimensions.
+template <bool BF16, bool MUON>
+__global__ __launch_bounds__(kThreads) void mat_spread_kernel(const MuonMat* __restrict__ mats,
+                                                              const MatJob* __restrict__ jobs, const void* grad,
+                                                              const float* mom, char* work, MuonK k) {
+  constexpr int T = kMatSpread;
+  __shared__ float tile[T][T + 1];   // [row of X][column of X]
+  const MatJob job = jobs[blockIdx.x];
+  const MuonMat& q = mats[job.mat];
+  const double inv = *reinterpret_cast<const double*>(work + q.inv);
+  const int i0 = job.i * T, j0 = job.j * T;
+  for (int e = threadIdx.x; e < T * T; e += kThreads) {
+    const int r = e / T, c = e % T;                       // in the matrix's own orientation
+    const int i = q.tall ? c : r, j = q.tall ? r : c;     // in X's
+    float x = 0.0f;
+    if (i0 + i < q.m && j0 + j < q.n) {
+      const int64_t at = q.start + (q.tall ? static_cast<int64_t>(j0 + j) * q.m + i0 + i
+                                           : static_cast<int64_t>(i0 + i) * q.n + j0 + j);
+      float g = load_elem(grad, at, BF16);
+      if constexpr (MUON) {
+        const float m = mom[at];
+        g = k.nesterov ? __fadd_rn(g, __fmul_rn(k.mu, m)) : m;
+      }
+      x = static_cast<float>(static_cast<double>(g) * inv);
+    }
+    tile[i][j] = x;
+  }
+  __syncthreads();
+  _Float16* xh = reinterpret_cast<_Float16*>(work + q.xh);
+  _Float16* xl = reinterpret_cast<_Float16*>(work + q.xl);
+  _Float16* xt0 = reinterpret_cast<_Float16*>(work + q.xt[0]);
+  for (int e = threadIdx.x; e < T * T / 8; e += kThreads) {
+    const int r = e / (T / 8), c = e % (T / 8) * 8;
+    if (i0 + r < q.m) {   // row r of X, 8 columns
+      h8 hi, lo;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        _Float16 h, l;
+        split(tile[r][c + t], h, l);
+        hi[t] = h;
+        lo[t] = l;
+      }
+      const int64_t at = static_cast<int64_t>(i0 + r) * q.np + j0 + c;
+      *reinterpret_cast<h8*>(xh + at) = hi;
+      *reinterpret_cast<h8*>(xl + at) = lo;
+    }
+    if (j0 + r < q.n) {   // column r of X, 8 rows
+      h8 hi, lo;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        _Float16 h, l;
+        split(tile[c + t][r], h, l);
+        hi[t] = h;
+        lo[t] = l;
+      }
+      const int64_t at = static_cast<int64_t>(j0 + r) * q.mp + i0 + c;
+      *reinterpret_cast<h8*>(xt0 + at) = hi;
+      if (q.two_part) *reinterpret_cast<h8*>(reinterpret_cast<_Float16*>(work + q.xtl[0]) + at) = lo;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ products
+
+enum Product {
+  P_GRAM,    // A = X X^T: off-diagonal part and diagonal
+  P_POLY,    // a I + b A + c A^2: off-diagonal part and diagonal
+  P_APPLY,   // polynomial times X: the next X
+  P_OUT,     // the same, last step: the result in bf16
+  P_STEP     // the same, last step: the parameters' update
+};
+
+// C = P Q^T on one BM x BM output tile, BM * 2 threads: a 2 x BM/64 grid of
+// waves, each 64 * (BM / 128) rows x 64 columns in 32 x 32 accumulators.
+// Operands go straight from memory to LDS, kMatK wide, in two stages: while
+// one stage is multiplied the next is on its way. In LDS a row is 128 bytes,
+// eight 16-byte pieces, piece c of row r at place c ^ (r & 7), so that the 32
+// rows a fragment takes spread over all banks; the loads permute the pieces
+// within each row's 128-byte line in memory. The fragment of the next 16
+// columns is read while the current one is multiplied; the stage turns over
+// (wait, barrier, new loads) before the last multiplication of a stage.
+template <int BM>
+struct Tile {
+  static constexpr int kNT = BM * 2;
+  static constexpr int kWaves = kNT / kWave;
+  static constexpr int WC = BM / 64;             // wave columns
+  static constexpr int NI = BM / 64;             // 32-row blocks per wave (2 wave rows)
+  static constexpr int NJ = 2;                   // 32-column blocks per wave
+  static constexpr int kStage = 2 * BM * kMatK * 2;   // bytes of both operands
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLoads = kStage / 1024 / kWaves;   // 1 KiB loads per wave and stage
+  static constexpr int kPasses = NI / 2;         // the epilogue stages 2 blocks of rows per wave at a time
+  static_assert(128 * BM * 4 <= kLds, "an epilogue pass fits the operand stages");
+};
+
+template <int BM>
+struct Acc {
+  f32x16 v[Tile<BM>::NI][2];
+};
+
+template <int BM>
+struct Multiply {
+__device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q, int ld, int p0, int p_rows, int q0,
+                                         int q_rows, int ksteps, char* lds, Acc<BM>& c) {
+  using T = Tile<BM>;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wr = wave / T::WC, wc = wave % T::WC;
+  // rows past an operand's end repeat its last row: their results are not stored
+  const int64_t row_bytes = static_cast<int64_t>(ld) * 2;
+  const int pr = min(p_rows - p0, BM), qr = min(q_rows - q0, BM);
+  const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(reinterpret_cast<const char*>(P) + p0 * row_bytes), 0, static_cast<int>(pr * row_bytes),
+      kRawBufferWord3);
+  const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(reinterpret_cast<const char*>(Q) + q0 * row_bytes), 0, static_cast<int>(qr * row_bytes),
+      kRawBufferWord3);
+  constexpr int kHalf = T::kLoads / 2;   // the first half of the loads fetch P, the others Q
+  int off[T::kLoads];
+#pragma unroll
+  for (int t = 0; t < T::kLoads; ++t) {
+    const int seg = (t % kHalf) * T::kWaves + wave;
+    const int row = min(seg * 8 + lane / 8, (t < kHalf ? pr : qr) - 1);
+    off[t] = static_cast<int>(row * row_bytes) + ((lane % 8) ^ (lane / 8)) * 16;
+  }
+  auto load = [&](int s) {
+    lds_char* dst = (lds_char*)(lds + (s & 1) * T::kStage) + wave * 1024;
+    const int k = s * static_cast<int>(kMatK) * 2;
+#pragma unroll
+    for (int t = 0; t < T::kLoads; ++t)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(t < kHalf ? rp : rq, dst + t * T::kWaves * 1024, 16, off[t], k, 0, 0);
+  };
+  // fragment addresses: row lane % 32 of a block, columns kk*16 + lane/32*8 ..+7
+  const int frow = lane % 32;
+  int fp[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) fp[kk] = frow * 128 + (((kk * 2 + lane / 32) ^ (frow & 7)) * 16);
+  const int pbase = wr * T::NI * 32 * 128, qbase = BM * 128 + wc * 64 * 128;
+  h8 fa[2][T::NI], fb[2][2];
+  auto fetch = [&](int s, int kk, int to) {
+    const char* b = lds + (s & 1) * T::kStage + fp[kk];
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i) fa[to][i] = *reinterpret_cast<const h8*>(b + pbase + i * 4096);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb[to][j] = *reinterpret_cast<const h8*>(b + qbase + j * 4096);
+  };
+  auto mma = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[from][i], fb[from][j], c.v[i][j], 0, 0, 0);
+  };
+  load(0);
+  if (ksteps > 1) {
+    load(1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(T::kLoads) : "memory");
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  fetch(0, 0, 0);
+  for (int s = 0; s < ksteps; ++s) {
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      fetch(s, kk + 1, (kk + 1) & 1);
+      mma(kk & 1);
+    }
+    // every wave has read this stage and the next one has arrived
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + 2 < ksteps) load(s + 2);
+    if (s + 1 < ksteps) fetch(s + 1, 0, 0);
+    mma(1);
+  }
+}
+};
+
+// sqrt(max(1, rows / cols)), 0.2 sqrt(max(rows, cols)) or 1.
+__device__ __forceinline__ float update_scale(int mode, int rows, int cols) {
+  if (mode == RS_MUON_SCALE_SPECTRAL) return rows > cols ? sqrtf(static_cast<float>(rows) / cols) : 1.0f;
+  if (mode == RS_MUON_SCALE_RMS) return 0.2f * sqrtf(static_cast<float>(max(rows, cols)));
+  return 1.0f;
+}
+
+// One output tile of one product. The accumulators go through LDS, 128 rows a
+// pass: a row-wise phase computes the result and stores it along its rows, a
+// column-wise phase stores its transpose. In LDS element (i, j) of a pass
+// lies at i * BM + (j ^ 4 * (i / 8 % 16)): 16-byte pieces along a row stay
+// whole, and the eight rows that a lane of the column-wise phase reads fall
+// into banks of their own.
+template <int BM, Product WHAT>
+__global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __restrict__ mats,
+                                                             const MatJob* __restrict__ jobs, char* work, int turn,
+                                                             MuonK k, void* out) {
+  using T = Tile<BM>;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const MatJob job = jobs[piece_index<32>(blockIdx.x, gridDim.x)];
+  const MuonMat& q = mats[job.mat];
+  const int i0 = job.i * BM, j0 = job.j * BM;
+  constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY;
+  const int m = q.m, n = q.n, mp = q.mp, np = q.np;
+  const bool two = q.two_part;
+  const int jn = kSym ? m : n;                   // columns of this product
+  const char* p_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.b);
+  const char* q_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.xt[turn]);
+  const char* p_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.bl);
+  const char* q_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.xtl[turn]);
+  const int ld = WHAT == P_GRAM ? np : mp;
+  Acc<BM> acc = {};
+  for (int part = two ? 0 : 2; part < 3; ++part) {   // high * low, low * high, high * high
+    if (two && part == 2) {
+#pragma unroll
+      for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc.v[i][j] *= 1.0f / kLowScale;
+    }
+    Multiply<BM>::run(reinterpret_cast<const _Float16*>(part == 1 ? p_lo : p_hi),
+                      reinterpret_cast<const _Float16*>(part == 0 ? q_lo : q_hi), ld, i0, m, j0, jn,
+                      ld / static_cast<int>(kMatK), lds, acc);
+  }
+
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int wr = wave / T::WC, wc = wave % T::WC;
+  float* stage = reinterpret_cast<float*>(lds);
+  float* da = reinterpret_cast<float*>(work + q.da);
+  float* db = reinterpret_cast<float*>(work + q.db);
+  _Float16* pa = reinterpret_cast<_Float16*>(work + q.a);
+  _Float16* pb = reinterpret_cast<_Float16*>(work + q.b);
+  _Float16* xh = reinterpret_cast<_Float16*>(work + q.xh);
+  _Float16* xl = reinterpret_cast<_Float16*>(work + q.xl);
+  _Float16* xt = reinterpret_cast<_Float16*>(work + q.xt[turn ^ 1]);
+  _Float16* pal = reinterpret_cast<_Float16*>(work + q.al);     // used where `two` only
+  _Float16* pbl = reinterpret_cast<_Float16*>(work + q.bl);
+  _Float16* xtl = reinterpret_cast<_Float16*>(work + q.xtl[turn ^ 1]);
+  const float ex = static_cast<float>(1 << q.ex);
+  const bool tall = q.tall;
+  const float step = WHAT == P_STEP ? k.lr * update_scale(k.scale_mode, q.rows, q.cols) / ex : 0.0f;
+  // the pass's row r is the tile's row (r / 64) * NI * 32 + pass * 64 + r % 64
+  for (int pass = 0; pass < T::kPasses; ++pass) {
+    if (pass) __syncthreads();
+#pragma unroll
+    for (int p = 0; p < T::kPasses; ++p) {
+      if (p != pass) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int row = wr * 64 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+            const int col = wc * 64 + j * 32 + lane % 32;
+            stage[row * BM + (col ^ (4 * (row / 8 % 16)))] = acc.v[2 * p + i][j][r];
+          }
+    }
+    __syncthreads();
+    // row-wise: 8 columns per thread
+    for (int e = threadIdx.x; e < 128 * (BM / 8); e += T::kNT) {
+      const int r = e / (BM / 8), c = e % (BM / 8) * 8;
+      const int i = i0 + (r / 64) * (T::NI * 32) + pass * 64 + r % 64, j = j0 + c;
+      const int sw = 4 * (r / 8 % 16);
+      f32x4* s0 = reinterpret_cast<f32x4*>(stage + r * BM + (c ^ sw));
+      f32x4* s1 = reinterpret_cast<f32x4*>(stage + r * BM + ((c + 4) ^ sw));
+      float v[8];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) { v[t] = (*s0)[t]; v[4 + t] = (*s1)[t]; }
+      const bool in = i < m && j < jn;
+      if constexpr (WHAT == P_GRAM) {
+        const float f = kOpScale / (ex * ex);
+        h8 h;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          v[t] = in && j + t < jn ? v[t] * f : 0.0f;
+          if (in && i == j + t) {
+            da[i] = v[t] / kOpScale;
+            v[t] = 0.0f;
+          }
+          h[t] = static_cast<_Float16>(v[t]);
+        }
+        if (i < m && j < mp) {
+          *reinterpret_cast<h8*>(pa + static_cast<int64_t>(i) * mp + j) = h;
+          if (two) *reinterpret_cast<h8*>(pal + static_cast<int64_t>(i) * mp + j) = low_parts(v);
+        }
+      } else if constexpr (WHAT == P_POLY) {
+        h8 h = {};
+        if (in) {
+          const h8 o = *reinterpret_cast<const h8*>(pa + static_cast<int64_t>(i) * mp + j);
+          const float di = da[i];
+          h8 ol = {};
+          if (two) ol = *reinterpret_cast<const h8*>(pal + static_cast<int64_t>(i) * mp + j);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            if (j + t >= jn) {
+              v[t] = 0.0f;
+            } else if (i == j + t) {
+              const float rest = k.b * di + k.c * (v[t] / (kOpScale * kOpScale) + di * di);
+              const bool whole = di > 0.5f;
+              db[i] = whole ? k.a + rest : k.a;
+              v[t] = whole ? 0.0f : rest * kOpScale;
+            } else {
+              const float x = static_cast<float>(o[t]) + static_cast<float>(ol[t]) * (1.0f / kLowScale);
+              v[t] = k.b * x + k.c * (v[t] / kOpScale + (di + da[j + t]) * x);
+            }
+            h[t] = static_cast<_Float16>(v[t]);
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[t] = 0.0f;
+        }
+        if (i < m && j < mp) {
+          *reinterpret_cast<h8*>(pb + static_cast<int64_t>(i) * mp + j) = h;
+          if (two) *reinterpret_cast<h8*>(pbl + static_cast<int64_t>(i) * mp + j) = low_parts(v);
+        }
+      } else {
+        if (in) {
+          const int64_t at = static_cast<int64_t>(i) * np + j;
+          const h8 hi = *reinterpret_cast<const h8*>(xh + at), lo = *reinterpret_cast<const h8*>(xl + at);
+          const float d = db[i];
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            v[t] = j + t < n ? v[t] * (1.0f / kOpScale) +
+                                   d * (static_cast<float>(hi[t]) + static_cast<float>(lo[t]) * (1.0f / kLowScale))
+                             : 0.0f;
+          if constexpr (WHAT == P_APPLY) {
+            h8 nh, nl;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              _Float16 a, b;
+              split(v[t], a, b);
+              nh[t] = a;
+              nl[t] = b;
+            }
+            *reinterpret_cast<h8*>(xh + at) = nh;
+            *reinterpret_cast<h8*>(xl + at) = nl;
+          } else if (!tall) {
+            const int64_t o = q.start + static_cast<int64_t>(i) * n + j;
+            if constexpr (WHAT == P_OUT) {
+              uint16_t* dst = static_cast<uint16_t*>(out) + o;
+              uint32_t w[8];
+#pragma unroll
+              for (int t = 0; t < 8; ++t) w[t] = bf16_rne(v[t] / ex);
+              if (n % 8 == 0) {
+                *reinterpret_cast<u32x4*>(dst) = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
+                                                       w[6] | w[7] << 16};
+              } else {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                  if (j + t < n) dst[t] = static_cast<uint16_t>(w[t]);
+              }
+            } else {
+              float* dst = static_cast<float*>(out) + o;
+              if (n % 4 == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (j + 4 * h < n) {
+                    f32x4 p = *reinterpret_cast<f32x4*>(dst + 4 * h);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) p[t] = __fsub_rn(__fmul_rn(p[t], k.decay), __fmul_rn(step, v[4 * h + t]));
+                    *reinterpret_cast<f32x4*>(dst + 4 * h) = p;
+                  }
+              } else {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                  if (j + t < n) dst[t] = __fsub_rn(__fmul_rn(dst[t], k.decay), __fmul_rn(step, v[t]));
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[t] = 0.0f;
+          if constexpr (WHAT == P_APPLY) {
+            if (i < m && j < np) {
+              const int64_t at = static_cast<int64_t>(i) * np + j;
+              *reinterpret_cast<h8*>(xh + at) = h8{};
+              *reinterpret_cast<h8*>(xl + at) = h8{};
+            }
+          }
+        }
+      }
+      *s0 = f32x4{v[0], v[1], v[2], v[3]};
+      *s1 = f32x4{v[4], v[5], v[6], v[7]};
+    }
+    // column-wise: 8 rows per thread, 16 threads along a column of the pass
+    const bool mirror = kSym ? job.i != job.j : WHAT == P_APPLY || tall;
+    if (!mirror) continue;
+    __syncthreads();
+    for (int e = threadIdx.x; e < BM * 16; e += T::kNT) {
+      const int r = e % 16 * 8, c = e / 16;
+      const int i = i0 + (r / 64) * (T::NI * 32) + pass * 64 + r % 64, j = j0 + c;
+      const int sw = 4 * (r / 8 % 16);
+      float v[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) v[t] = stage[(r + t) * BM + (c ^ sw)];
+      if (j >= jn) continue;
+      if constexpr (kSym || WHAT == P_APPLY) {
+        if (i < mp) {
+          h8 h;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) h[t] = static_cast<_Float16>(v[t]);
+          const int64_t at = static_cast<int64_t>(j) * mp + i;
+          *reinterpret_cast<h8*>((WHAT == P_GRAM ? pa : WHAT == P_POLY ? pb : xt) + at) = h;
+          if (two) *reinterpret_cast<h8*>((WHAT == P_GRAM ? pal : WHAT == P_POLY ? pbl : xtl) + at) = low_parts(v);
+        }
+      } else if (i < m) {
+        const int64_t o = q.start + static_cast<int64_t>(j) * m + i;
+        if constexpr (WHAT == P_OUT) {
+          uint16_t* dst = static_cast<uint16_t*>(out) + o;
+          uint32_t w[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) w[t] = bf16_rne(v[t] / ex);
+          if (m % 8 == 0) {
+            *reinterpret_cast<u32x4*>(dst) = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
+                                                   w[6] | w[7] << 16};
+          } else {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              if (i + t < m) dst[t] = static_cast<uint16_t>(w[t]);
+          }
+        } else {
+          float* dst = static_cast<float*>(out) + o;
+          if (m % 4 == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (i + 4 * h < m) {
+                f32x4 p = *reinterpret_cast<f32x4*>(dst + 4 * h);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) p[t] = __fsub_rn(__fmul_rn(p[t], k.decay), __fmul_rn(step, v[4 * h + t]));
+                *reinterpret_cast<f32x4*>(dst + 4 * h) = p;
+              }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              if (i + t < m) dst[t] = __fsub_rn(__fmul_rn(dst[t], k.decay), __fmul_rn(step, v[t]));
+          }
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+
+template <Product WHAT>
+void launch_product(const rs_plan* p, int side, const MatJob* jobs, int64_t n_jobs, char* work, int turn,
+                    const MuonK& k, void* out, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(n_jobs));
+  if (side == 256)
+    hipLaunchKernelGGL((mat_product_kernel<256, WHAT>), grid, dim3(512), 0, s, p->mats, jobs, work, turn, k, out);
+  else
+    hipLaunchKernelGGL((mat_product_kernel<128, WHAT>), grid, dim3(256), 0, s, p->mats, jobs, work, turn, k, out);
+}
+
+// Momentum (MUON), norm and Newton-Schulz on every matrix of the plan; the
+// last product writes `out` (bf16 values, or fp32 parameters in place).
+template <bool MUON>
+int run_matrices(rs_plan* p, const void* grad, int32_t grad_dt, float* mom, const float* coeffs, int32_t steps,
+                 float eps, MuonK k, void* out, char* work, hipStream_t s, const char* who) {
+  const dim3 chunks(static_cast<unsigned>(p->n_mat_chunks)), spread(static_cast<unsigned>(p->n_mat_spread));
+  if (grad_dt == RS_BF16) {
+    hipLaunchKernelGGL((mat_norm_kernel<true, MUON>), chunks, dim3(kThreads), 0, s, p->mats, p->mat_chunks, grad, mom,
+                       work, k);
+  } else {
+    hipLaunchKernelGGL((mat_norm_kernel<false, MUON>), chunks, dim3(kThreads), 0, s, p->mats, p->mat_chunks, grad, mom,
+                       work, k);
+  }
+  hipLaunchKernelGGL(mat_scale_kernel, dim3(static_cast<unsigned>(p->n_mats)), dim3(kThreads), 0, s, p->mats, work,
+                     static_cast<double>(eps));
+  if (grad_dt == RS_BF16) {
+    hipLaunchKernelGGL((mat_spread_kernel<true, MUON>), spread, dim3(kThreads), 0, s, p->mats, p->mat_spread, grad,
+                       mom, work, k);
+  } else {
+    hipLaunchKernelGGL((mat_spread_kernel<false, MUON>), spread, dim3(kThreads), 0, s, p->mats, p->mat_spread, grad,
+                       mom, work, k);
+  }
+  for (int t = 0; t < steps; ++t) {
+    k.a = coeffs[3 * t];
+    k.b = coeffs[3 * t + 1];
+    k.c = coeffs[3 * t + 2];
+    launch_product<P_GRAM>(p, p->mat_tile_sym, p->mat_sym, p->n_mat_sym, work, t & 1, k, nullptr, s);
+    launch_product<P_POLY>(p, p->mat_tile_sym, p->mat_sym, p->n_mat_sym, work, t & 1, k, nullptr, s);
+    if (t + 1 < steps)
+      launch_product<P_APPLY>(p, p->mat_tile_full, p->mat_full, p->n_mat_full, work, t & 1, k, nullptr, s);
+    else
+      launch_product<MUON ? P_STEP : P_OUT>(p, p->mat_tile_full, p->mat_full, p->n_mat_full, work, t & 1, k, out, s);
+  }
+  return launched(who);
+}
+
+int check_matrices(const rs_plan* p, const float* coeffs, int32_t steps, float eps, const void* work,
+                   int64_t work_bytes, const char* who) {
+  if (p->mat_too_large)
+    return fail(RS_ERANGE, std::string(who) + ": a WHOLE matrix has a side over " + std::to_string(kMatMaxSide) +
+                               " or both over " + std::to_string(kMatMaxMin));
+  if (!coeffs || steps < 1 || steps > kMuonMaxSteps)
+    return fail(RS_EINVAL, std::string(who) + ": 1 to " + std::to_string(kMuonMaxSteps) + " steps of three coefficients");
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(coeffs[i])) return fail(RS_EINVAL, std::string(who) + ": coefficients must be finite");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(RS_EINVAL, std::string(who) + ": eps must be finite and >= 0");
+  if (p->n_mats && !work) return fail(RS_EINVAL, std::string(who) + ": null workspace");
+  if (!aligned16(work)) return fail(RS_EALIGN, std::string(who) + ": workspace must be 16-byte aligned");
+  if (work_bytes < p->mat_work_bytes)
+    return fail(RS_EINVAL, std::string(who) + ": workspace of " + std::to_string(work_bytes) + " bytes, " +
+                               std::to_string(p->mat_work_bytes) + " needed");
+  return RS_OK;
+}
+
+}  // namespace
+}  // namespace rs
+
+using namespace rs;
+
+extern "C" int rs_muon_workspace(const rs_plan* p, int64_t* bytes) {
+  clear_error();
+  if (!p || !bytes) return fail(RS_EINVAL, "rs_muon_workspace: null argument");
+  *bytes = p->mat_work_bytes;
+  return RS_OK;
+}
+
+extern "C" int rs_orthogonalize(rs_plan* p, const void* src, int32_t src_dt, void* out, const float* coeffs,
+                                int32_t steps, float eps, void* work, int64_t work_bytes, void* stream) {
+  const char* who = "rs_orthogonalize";
+  clear_error();
+  int st = check_call(p, who);
+  if (st != RS_OK) return st;
+  if (!src || !out) return fail(RS_EINVAL, std::string(who) + ": null argument");
+  if (src_dt != RS_F32 && src_dt != RS_BF16) return fail(RS_EDTYPE, std::string(who) + ": src is fp32 or bf16");
+  st = check_matrices(p, coeffs, steps, eps, work, work_bytes, who);
+  if (st != RS_OK) return st;
+  if (!aligned16(src) || !aligned16(out)) return fail(RS_EALIGN, std::string(who) + ": buffers must be 16-byte aligned");
+  if (p->n_mats == 0) return RS_OK;
+  return run_matrices<false>(p, src, src_dt, nullptr, coeffs, steps, eps, MuonK{}, out, static_cast<char*>(work),
+                             static_cast<hipStream_t>(stream), who);
+}
+
+extern "C" int rs_muon_step(rs_plan* p, float* param, const void* grad, int32_t grad_dt, float* momentum,
+                            const rs_muon_hparams* hp, const float* coeffs, void* work, int64_t work_bytes,
+                            void* stream) {
+  const char* who = "rs_muon_step";
+  clear_error();
+  int st = check_call(p, who);
+  if (st != RS_OK) return st;
+  if (!param || !grad || !momentum || !hp) return fail(RS_EINVAL, std::string(who) + ": null argument");
+  if (grad_dt != RS_F32 && grad_dt != RS_BF16) return fail(RS_EDTYPE, std::string(who) + ": grad is fp32 or bf16");
+  if (!std::isfinite(hp->lr) || !(hp->momentum >= 0.0f && hp->momentum < 1.0f) || !std::isfinite(hp->weight_decay) ||
+      (hp->nesterov != 0 && hp->nesterov != 1) || hp->scale_mode < RS_MUON_SCALE_NONE ||
+      hp->scale_mode > RS_MUON_SCALE_RMS)
+    return fail(RS_EINVAL, std::string(who) + ": bad hyper-parameters");
+  st = check_matrices(p, coeffs, hp->steps, hp->eps, work, work_bytes, who);
+  if (st != RS_OK) return st;
+  if (!aligned16(param) || !aligned16(grad) || !aligned16(momentum))
+    return fail(RS_EALIGN, std::string(who) + ": buffers must be 16-byte aligned");
+  if (p->n_mats == 0) return RS_OK;
+  MuonK k{};
+  k.mu = hp->momentum;
+  k.lr = hp->lr;
+  k.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * static_cast<double>(hp->weight_decay));
+  k.nesterov = hp->nesterov;
+  k.scale_mode = hp->scale_mode;
+  return run_matrices<true>(p, grad, grad_dt, momentum, coeffs, hp->steps, hp->eps, k, param, static_cast<char*>(work),
+                            static_cast<hipStream_t>(stream), who);
+}

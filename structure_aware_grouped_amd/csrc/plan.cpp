@@ -289,6 +289,11 @@ void lower(const std::vector<Tensor>& t, int64_t S, int64_t R_mat, Tables* tb) {
 }
 
 template <typename T>
+bool upload(T* dev, const std::vector<T>& host) {
+  return host.empty() || hipMemcpy(dev, host.data(), sizeof(T) * host.size(), hipMemcpyHostToDevice) == hipSuccess;
+}
+
+template <typename T>
 T* carve(char*& p, int64_t count) {
   T* out = reinterpret_cast<T*>(p);
   p += align_up(static_cast<int64_t>(sizeof(T)) * std::max<int64_t>(count, 1), 256);
@@ -477,6 +482,96 @@ void lower_quant(const std::vector<Tensor>& t, int64_t top, QuantList* ql) {
   }
 }
 
+// The whole matrices of a plan: where their operands lie in the workspace and
+// the work lists of the passes over them (rs_orthogonalize, rs_muon_step).
+void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
+  std::vector<const Tensor*> ms;
+  for (const Tensor& x : t) {
+    if (x.kind != RS_WHOLE || x.rows < 2 || x.cols < 2) continue;
+    if (std::max(x.rows, x.cols) > kMatMaxSide || std::min(x.rows, x.cols) > kMatMaxMin) {
+      mt->too_large = true;
+      continue;
+    }
+    ms.push_back(&x);
+  }
+  // longest products first, so that the last ones to start are short
+  std::stable_sort(ms.begin(), ms.end(), [](const Tensor* a, const Tensor* b) {
+    const int64_t na = std::max(a->rows, a->cols), nb = std::max(b->rows, b->cols);
+    return na != nb ? na > nb : std::min(a->rows, a->cols) > std::min(b->rows, b->cols);
+  });
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  for (const Tensor* x : ms) {
+    MuonMat q{};
+    q.start = x->start;
+    q.rows = static_cast<int32_t>(x->rows);
+    q.cols = static_cast<int32_t>(x->cols);
+    q.tall = x->rows > x->cols;
+    q.m = std::min(q.rows, q.cols);
+    q.n = std::max(q.rows, q.cols);
+    q.mp = static_cast<int32_t>(align_up(q.m, kMatK));
+    q.np = static_cast<int32_t>(align_up(q.n, kMatK));
+    // 2^ex is within sqrt(2) of sqrt(n): entries of an orthogonal X are about 1 then
+    while ((int64_t(1) << (2 * q.ex + 1)) <= q.n) ++q.ex;
+    q.n_part = static_cast<int32_t>(ceil_div(x->n, kMatChunk));
+    q.xh = take(int64_t(2) * q.m * q.np);
+    q.xl = take(int64_t(2) * q.m * q.np);
+    for (int64_t& o : q.xt) o = take(int64_t(2) * q.n * q.mp);
+    q.a = take(int64_t(2) * q.m * q.mp);
+    q.b = take(int64_t(2) * q.m * q.mp);
+    q.two_part = q.m <= kMatTwoPart;
+    if (q.two_part) {
+      for (int64_t& o : q.xtl) o = take(int64_t(2) * q.n * q.mp);
+      q.al = take(int64_t(2) * q.m * q.mp);
+      q.bl = take(int64_t(2) * q.m * q.mp);
+    }
+    q.da = take(int64_t(4) * q.m);
+    q.db = take(int64_t(4) * q.m);
+    q.part = take(int64_t(8) * q.n_part);
+    q.inv = take(8);
+    mt->mats.push_back(q);
+  }
+  mt->work_bytes = at;
+  auto tiles = [&](int64_t side, bool sym) {
+    int64_t c = 0;
+    for (const MuonMat& q : mt->mats) {
+      const int64_t a = ceil_div(q.m, side), b = ceil_div(q.n, side);
+      c += sym ? a * (a + 1) / 2 : a * b;
+    }
+    return c;
+  };
+  mt->tile_sym = tiles(256, true) >= kMatMinTiles ? 256 : 128;
+  mt->tile_full = tiles(256, false) >= kMatMinTiles ? 256 : 128;
+  // RS_MUON_TILE=128|256 forces one size
+  if (const char* e = std::getenv("RS_MUON_TILE")) {
+    const int side = std::atoi(e);
+    if (side == 128 || side == 256) mt->tile_sym = mt->tile_full = side;
+  }
+  // Tiles in blocks of kBlock x kBlock: the workgroups that run together on
+  // one XCD share their operands' rows in its L2.
+  constexpr int64_t kBlock = 6;
+  for (int32_t k = 0; k < static_cast<int32_t>(mt->mats.size()); ++k) {
+    const MuonMat& q = mt->mats[k];
+    for (int32_t c = 0; c < q.n_part; ++c) mt->chunks.push_back({k, c});
+    for (int64_t i = 0; i < ceil_div(q.m, kMatSpread); ++i)
+      for (int64_t j = 0; j < ceil_div(q.n, kMatSpread); ++j)
+        mt->spread.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j)});
+    for (const bool sym : {true, false}) {
+      const int64_t side = sym ? mt->tile_sym : mt->tile_full;
+      const int64_t ti = ceil_div(q.m, side), tj = sym ? ti : ceil_div(q.n, side);
+      std::vector<MatJob>& out = sym ? mt->sym : mt->full;
+      for (int64_t i0 = 0; i0 < ti; i0 += kBlock)
+        for (int64_t j0 = 0; j0 < tj; j0 += kBlock)
+          for (int64_t i = i0; i < std::min(ti, i0 + kBlock); ++i)
+            for (int64_t j = j0; j < std::min(tj, j0 + kBlock); ++j)
+              if (!sym || j <= i) out.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j)});
+    }
+  }
+}
 
 }  // namespace rs
 
@@ -521,6 +616,8 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
 
     Tables tb;
     lower(t, S, R_mat, &tb);
+    MuonTables mt;
+    lower_muon(t, &mt);
     // Every launch loops over its work items beyond kMaxGrid workgroups; item
     // and piece indices are 32-bit. Under the 2^39-element limit this holds
     // for any plan but one made of tiny tiles.
@@ -565,6 +662,15 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->gather_vec = tb.gather_vec;
     p->gather_split8 = tb.gather_split8;
     p->gather_split4 = tb.gather_split4;
+    p->n_mats = static_cast<int64_t>(mt.mats.size());
+    p->n_mat_chunks = static_cast<int64_t>(mt.chunks.size());
+    p->n_mat_spread = static_cast<int64_t>(mt.spread.size());
+    p->n_mat_sym = static_cast<int64_t>(mt.sym.size());
+    p->n_mat_full = static_cast<int64_t>(mt.full.size());
+    p->mat_tile_sym = mt.tile_sym;
+    p->mat_tile_full = mt.tile_full;
+    p->mat_work_bytes = mt.work_bytes;
+    p->mat_too_large = mt.too_large;
     // gfx950's FP8 conversion (OCP E4M3, round to nearest even) by default;
     // RS_E4M3_ENCODER=sw selects the integer encoder, which gives the same codes.
     const char* enc = std::getenv("RS_E4M3_ENCODER");
@@ -593,6 +699,11 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
                           align_up(sizeof(QJob) * std::max<int64_t>(p->n_qjobs, 1), 256) +
                           align_up(sizeof(GatherChunk) * std::max<int64_t>(p->n_gchunks, 1), 256) +
                           align_up(sizeof(QJob) * std::max<int64_t>(p->n_gtile + p->n_gflat, 1), 256) +
+                          align_up(sizeof(MuonMat) * std::max<int64_t>(p->n_mats, 1), 256) +
+                          align_up(sizeof(MatChunk) * std::max<int64_t>(p->n_mat_chunks, 1), 256) +
+                          align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_spread, 1), 256) +
+                          align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_sym, 1), 256) +
+                          align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_full, 1), 256) +
                           3 * align_up(sizeof(void*) * n, 256);
     if (hipMalloc(&p->dmem, bytes) != hipSuccess) {
       p->dmem = nullptr;
@@ -607,6 +718,11 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->qjobs = carve<QJob>(cur, p->n_qjobs);
     p->gchunks = carve<GatherChunk>(cur, p->n_gchunks);
     p->gjobs = carve<QJob>(cur, p->n_gtile + p->n_gflat);
+    p->mats = carve<MuonMat>(cur, p->n_mats);
+    p->mat_chunks = carve<MatChunk>(cur, p->n_mat_chunks);
+    p->mat_spread = carve<MatJob>(cur, p->n_mat_spread);
+    p->mat_sym = carve<MatJob>(cur, p->n_mat_sym);
+    p->mat_full = carve<MatJob>(cur, p->n_mat_full);
     void** dst_dev = carve<void*>(cur, n);
     void** src_dev = carve<void*>(cur, n);
     void** gdst_dev = carve<void*>(cur, n);
@@ -616,7 +732,9 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
               (p->n_pack == 0 || hipMemcpy(p->pack, tb.pack.data(), sizeof(PackChunk) * p->n_pack, hipMemcpyHostToDevice) == hipSuccess) &&
               (p->n_qjobs == 0 || hipMemcpy(p->qjobs, tb.qjobs.data(), sizeof(QJob) * p->n_qjobs, hipMemcpyHostToDevice) == hipSuccess) &&
               (p->n_gchunks == 0 || hipMemcpy(p->gchunks, tb.gchunks.data(), sizeof(GatherChunk) * p->n_gchunks, hipMemcpyHostToDevice) == hipSuccess) &&
-              (tb.gjobs.empty() || hipMemcpy(p->gjobs, tb.gjobs.data(), sizeof(QJob) * tb.gjobs.size(), hipMemcpyHostToDevice) == hipSuccess);
+              (tb.gjobs.empty() || hipMemcpy(p->gjobs, tb.gjobs.data(), sizeof(QJob) * tb.gjobs.size(), hipMemcpyHostToDevice) == hipSuccess) &&
+              upload(p->mats, mt.mats) && upload(p->mat_chunks, mt.chunks) && upload(p->mat_spread, mt.spread) &&
+              upload(p->mat_sym, mt.sym) && upload(p->mat_full, mt.full);
     if (!ok) {
       release(p);
       (void)hipSetDevice(prev);

@@ -298,6 +298,70 @@ constexpr int64_t kGatherMaxRun =
 static_assert(kGatherMaxRun / 4 < 65536, "a run of several rows keeps its vector indices under 2^16");
 
 
+// ---- whole matrices (rs_orthogonalize, rs_muon_step) ----
+//
+// A WHOLE tensor of more than one row and one column is a matrix. The
+// Newton-Schulz products run on X, the matrix or its transpose, whichever has
+// m = min(rows, cols) rows and n = max(rows, cols) columns. Every operand of a
+// product is stored with its contraction dimension contiguous and padded with
+// zeros to kMatK elements, so a product's inner loop has no tail.
+constexpr int64_t kMatK = 64;
+// Matrices of at most this many rows of X have high and low parts throughout.
+constexpr int64_t kMatTwoPart = 64;
+// Largest side and smallest-side limits of a matrix: byte offsets inside one
+// 256-row panel of an operand stay under 2^31, tile numbers fit 16 bits.
+constexpr int64_t kMatMaxSide = int64_t(1) << 20;
+constexpr int64_t kMatMaxMin = int64_t(1) << 16;
+// A product takes 256 x 256 output tiles where the plan's matrices give at
+// least kMatMinTiles of them, else 128 x 128.
+constexpr int64_t kMatMinTiles = 200;
+// Elements per work item of the pass that updates momentum and sums squares.
+constexpr int64_t kMatChunk = 8192;
+// Tile of the pass that splits the scaled matrix into its operands.
+constexpr int64_t kMatSpread = 64;
+constexpr int kMuonMaxSteps = 32;
+
+// One matrix of a plan; offsets xh .. part are bytes in the caller's workspace.
+struct MuonMat {
+  int64_t start;      // flat position of its first element
+  int64_t xh, xl;     // m x np: high and low fp16 parts of X
+  int64_t xt[2];      // n x mp: the transposed high part, read and written in turn
+  int64_t a, b;       // m x mp: X X^T and the polynomial without (part of) their diagonals
+  int64_t xtl[2], al, bl;   // low parts of xt, a and b (two_part only)
+  int64_t da, db;     // m fp32: their diagonals
+  int64_t part;       // doubles: partial sums of squares
+  int64_t inv;        // one double: 2^ex / (norm + eps)
+  int32_t rows, cols, m, n, mp, np;
+  int32_t tall;       // rows > cols: X is the transpose
+  int32_t ex;         // X is stored times 2^ex
+  int32_t n_part;
+  int32_t two_part;   // m <= kMatTwoPart: every operand has a low part
+};
+
+// Work items of the matrix passes: a chunk of kMatChunk elements (i = chunk),
+// a spread tile or a product's output tile (i, j = tile row and column of X).
+struct MatJob {
+  int32_t mat;
+  uint16_t i, j;
+};
+struct MatChunk {
+  int32_t mat;
+  int32_t chunk;
+};
+
+// The matrices of a plan and the work lists of their passes, on the host.
+struct MuonTables {
+  std::vector<MuonMat> mats;         // longest contraction first
+  std::vector<MatChunk> chunks;
+  std::vector<MatJob> spread;
+  std::vector<MatJob> sym;           // tiles on and below the diagonal of an m x m product
+  std::vector<MatJob> full;          // tiles of an m x n product
+  int tile_sym = 0, tile_full = 0;   // tile sides
+  int64_t work_bytes = 0;
+  bool too_large = false;            // a matrix beyond kMatMaxSide / kMatMaxMin
+};
+void lower_muon(const std::vector<Tensor>& t, MuonTables* mt);
+
 // Device copy of a per-tensor pointer table plus the host state that decides
 // when it must be uploaded again.
 struct PtrTable {
@@ -366,6 +430,16 @@ struct rs_plan {
   int64_t n_gchunks = 0;
   rs::QJob* gjobs = nullptr;           // gather side, other tensors: tile jobs, then flat groups
   int64_t n_gtile = 0, n_gflat = 0;
+
+  rs::MuonMat* mats = nullptr;         // whole matrices and their work lists
+  rs::MatChunk* mat_chunks = nullptr;
+  rs::MatJob* mat_spread = nullptr;
+  rs::MatJob* mat_sym = nullptr;
+  rs::MatJob* mat_full = nullptr;
+  int64_t n_mats = 0, n_mat_chunks = 0, n_mat_spread = 0, n_mat_sym = 0, n_mat_full = 0;
+  int mat_tile_sym = 0, mat_tile_full = 0;
+  int64_t mat_work_bytes = 0;
+  bool mat_too_large = false;
 
   rs::PtrTable dst;   // unpack destinations
   rs::PtrTable src;   // pack sources
