@@ -22,6 +22,9 @@
  *   rs_block_dequant    the inverse of rs_block_quant
  *   rs_unpack_dequant   gathered codes + scales -> the quantised full tensors
  *   rs_adam8_step       one AdamW step on block-quantised int8 / uint8 state
+ *   rs_embed_rows       embedding lookup straight from the gathered buffer
+ *   rs_embed_grad       its gradient straight into the packed buffer
+ *   rs_embed_workspace  bytes of workspace rs_embed_grad needs
  *   rs_orthogonalize    Newton-Schulz orthogonalisation of the WHOLE matrices
  *   rs_muon_step        one Muon step on the WHOLE matrices
  *   rs_muon_workspace   bytes of workspace the two need
@@ -333,6 +336,52 @@ typedef struct rs_adam_hparams {
  * lr / wd), RS_EALIGN, RS_EHIP. */
 int rs_adam8_step(rs_plan* plan, float* param, const float* grad, void* q_m, float* s_m,
                   void* q_v, float* s_v, const rs_adam_hparams* hp, void* stream);
+
+/* Embedding lookup straight from the gathered buffer: what rs_unpack_gathered
+ * would copy of one tensor, for the rows that a batch of tokens names
+ * (feynmanwiki walkthrough, DBuffer paragraphs: a tensor is its planned
+ * slice). With T = tensor `tensor` of the plan, rows x cols:
+ *   out[t, c] = fl32(T[ids[t], c] * scale)   for 0 <= t < n_ids,
+ * rounded once more to bf16 (nearest, ties to even) when out_dt is RS_BF16.
+ * An id outside [0, rows) (padding tokens, e.g. -1) names no row: its output
+ * row is +0.0. Any block kind but RS_TILEMAJOR (whose rows are not
+ * contiguous).
+ * gathered: device, R_mat*S elements of dt (RS_F32 or RS_BF16). ids: device,
+ * n_ids signed integers of id_bytes (4 or 8) bytes. scale: finite. out:
+ * device, n_ids x cols row-major of out_dt (RS_F32 or RS_BF16), overlapping
+ * neither input. gathered and out 16-byte aligned. n_ids may be 0. rows, cols
+ * and n_ids under 2^31, n_ids * cols at most 2^39.
+ * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
+int rs_embed_rows(rs_plan* plan, int64_t tensor, const void* gathered, int32_t dt, const void* ids,
+                  int32_t id_bytes, int64_t n_ids, float scale, void* out, int32_t out_dt, void* stream);
+
+/* Gradient of the lookup straight into the packed buffer: what
+ * rs_pack_scatter would write of one tensor, without the dense gradient.
+ *   y[r, c] = fl32(sigma * sum of dy[t, c] over the t with ids[t] = r)
+ *   packed[r, c] = prev ? fl32(prev[r, c] + y[r, c]) : y[r, c]
+ * on the tensor's interval of the flat buffers (r, c there), with sigma =
+ * scale (RS_SCALE_GIVEN) or fl32(scale / V) (RS_SCALE_INV_V); a bf16 packed
+ * buffer gets the result rounded once to nearest even. Sums are fp32, in an
+ * order that depends on the ids alone: the same call gives the same bits.
+ * Ids outside [0, rows) contribute nothing and their dy is not read.
+ * prev = packed (fp32 only) adds in place: rows that no token names are
+ * neither read nor written, e.g. a tied table whose dense gradient is packed
+ * already. Otherwise every row of the tensor is written (+0.0, or prev + 0.0,
+ * where no token names it), and prev must not overlap packed. Positions
+ * outside the tensor's interval are left alone in any case.
+ * dy: device, n_ids x cols row-major of dy_dt (RS_F32 or RS_BF16). prev:
+ * device fp32 R_mat*S or NULL. packed: device R_mat*S of packed_dt (RS_F32 or
+ * RS_BF16). work: device memory of rs_embed_workspace bytes, contents not
+ * kept between calls; calls that may overlap need a workspace each. All
+ * 16-byte aligned; ids as in rs_embed_rows.
+ * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
+int rs_embed_grad(rs_plan* plan, int64_t tensor, const void* ids, int32_t id_bytes, int64_t n_ids,
+                  const void* dy, int32_t dy_dt, const float* prev, void* packed, int32_t packed_dt,
+                  int32_t scale_mode, float scale, void* work, int64_t work_bytes, void* stream);
+
+/* Bytes of workspace for rs_embed_grad on this tensor with n_ids tokens; it
+ * grows with n_ids. Errors: RS_EINVAL, RS_ERANGE. */
+int rs_embed_workspace(const rs_plan* plan, int64_t tensor, int64_t n_ids, int64_t* bytes);
 
 /* Orthogonalisation of every matrix of the plan by Newton-Schulz products
  * (feynmanwiki walkthrough, Muon paragraphs: the rank that holds a matrix

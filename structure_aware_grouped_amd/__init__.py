@@ -15,6 +15,9 @@ from .binding import (  # noqa: F401
     rs_block_dequant,
     rs_block_quant,
     rs_block_quant_noalloc,
+    rs_embed_grad,
+    rs_embed_rows,
+    rs_embed_workspace,
     rs_muon_step,
     rs_muon_workspace,
     rs_orthogonalize,

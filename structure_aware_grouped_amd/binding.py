@@ -27,7 +27,8 @@ RS_F32, RS_BF16, RS_E4M3, RS_I8, RS_U8 = 0, 1, 2, 3, 4
 CODE_FORMATS = {"e4m3": RS_E4M3, "i8": RS_I8, "u8": RS_U8}
 EXPORTS = ("rs_plan_build", "rs_plan_load", "rs_plan_info", "rs_plan_free", "rs_unpack_gathered",
            "rs_pack_scatter", "rs_block_quant", "rs_block_dequant", "rs_unpack_dequant", "rs_adam8_step",
-           "rs_last_error", "rs_block_quant_noalloc", "rs_orthogonalize", "rs_muon_step", "rs_muon_workspace")
+           "rs_last_error", "rs_block_quant_noalloc", "rs_orthogonalize", "rs_muon_step", "rs_muon_workspace",
+           "rs_embed_rows", "rs_embed_grad", "rs_embed_workspace")
 
 
 class RsError(RuntimeError):
@@ -86,6 +87,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rs_orthogonalize.argtypes = [P, P, I32, P, PF, I32, F, P, I64, P]
     lib.rs_muon_step.argtypes = [P, P, P, I32, P, ctypes.POINTER(MuonHParamsC), PF, P, I64, P]
     lib.rs_muon_workspace.argtypes = [P, PI64]
+    lib.rs_embed_rows.argtypes = [P, I64, P, I32, P, I32, I64, F, P, I32, P]
+    lib.rs_embed_grad.argtypes = [P, I64, P, I32, I64, P, I32, P, P, I32, I32, F, P, I64, P]
+    lib.rs_embed_workspace.argtypes = [P, I64, I64, PI64]
     lib.rs_last_error.argtypes = []
     lib.rs_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -371,6 +375,70 @@ def rs_adam8_step(plan: Plan, param: torch.Tensor, grad: torch.Tensor, q_m: torc
     hp = AdamHParamsC(lr, beta1, beta2, eps, weight_decay, 0, int(step))
     _check(load().rs_adam8_step(plan.handle, param.data_ptr(), grad.data_ptr(), q_m.data_ptr(), s_m.data_ptr(),
                                 q_v.data_ptr(), s_v.data_ptr(), ctypes.byref(hp), _stream(plan.device)))
+
+
+# ---------------------------------------------------------------- embeddings
+
+def _table(plan: Plan, tensor: int, ids: torch.Tensor, rows: torch.Tensor, what: str):
+    """(tokens) of an embedding call: ids are int32 or int64, `rows` holds one row per id."""
+    if not 0 <= int(tensor) < len(plan.specs):
+        raise ValueError(f"no tensor {tensor} in a plan of {len(plan.specs)}")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids: int32 or int64")
+    if rows.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{what}: fp32 or bf16")
+    if rows.numel() != ids.numel() * int(plan.specs[tensor].cols):
+        raise ValueError(f"{what}: one row of {plan.specs[tensor].cols} columns per id")
+    return ids.numel()
+
+
+def _code(t: torch.Tensor) -> int:
+    return RS_F32 if t.dtype == torch.float32 else RS_BF16
+
+
+def _embed_bytes(plan: Plan, tensor: int, n_ids: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().rs_embed_workspace(plan.handle, int(tensor), int(n_ids), ctypes.byref(n)))
+    return n.value
+
+
+def rs_embed_workspace(plan: Plan, tensor: int, n_ids: int) -> torch.Tensor:
+    """Workspace for rs_embed_grad with up to n_ids tokens (uint8, on the plan's device). Calls
+    that may overlap need a workspace each."""
+    return torch.empty(max(_embed_bytes(plan, tensor, n_ids), 1), dtype=torch.uint8, device=f"cuda:{plan.device}")
+
+
+def rs_embed_rows(plan: Plan, tensor: int, gathered: torch.Tensor, ids: torch.Tensor, out: torch.Tensor,
+                  scale: float = 1.0):
+    """out[t] <- scale * row ids[t] of tensor number `tensor` of the gathered flat buffer (fp32 or
+    bf16); ids outside [0, rows) give rows of +0.0."""
+    n = _table(plan, tensor, ids, out, "out")
+    _dev_check(plan, gathered, ids, out)
+    _flat_check(plan, gathered, (torch.float32, torch.bfloat16), "gathered")
+    _apart_check(gathered=gathered, out=out, ids=ids)
+    _check(load().rs_embed_rows(plan.handle, int(tensor), gathered.data_ptr(), _code(gathered), ids.data_ptr(),
+                                ids.element_size(), n, float(scale), out.data_ptr(), _code(out),
+                                _stream(plan.device)))
+
+
+def rs_embed_grad(plan: Plan, tensor: int, ids: torch.Tensor, dy: torch.Tensor, packed: torch.Tensor,
+                  work: torch.Tensor, prev: Optional[torch.Tensor] = None, scale: float = 1.0, inv_v: bool = False):
+    """Tensor number `tensor`'s interval of packed <- [prev +] sigma * the sum of dy's rows by id,
+    sigma = scale, or scale / V with inv_v. prev=packed (fp32) adds in place to the named rows."""
+    n = _table(plan, tensor, ids, dy, "dy")
+    _dev_check(plan, ids, dy, packed, work, prev)
+    _flat_check(plan, packed, (torch.float32, torch.bfloat16), "packed")
+    _work_check(work, _embed_bytes(plan, tensor, n))
+    apart = {"ids": ids, "dy": dy, "packed": packed, "work": work}
+    if prev is not None:
+        _flat_check(plan, prev, (torch.float32,), "prev")
+        if prev.data_ptr() != packed.data_ptr() or packed.dtype != torch.float32:
+            apart["prev"] = prev
+    _apart_check(**apart)
+    _check(load().rs_embed_grad(plan.handle, int(tensor), ids.data_ptr(), ids.element_size(), n, dy.data_ptr(),
+                                _code(dy), prev.data_ptr() if prev is not None else None, packed.data_ptr(),
+                                _code(packed), 0 if inv_v else 1, float(scale), work.data_ptr(), work.numel(),
+                                _stream(plan.device)))
 
 
 # ---------------------------------------------------------------- whole matrices

@@ -16,7 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librs_hip.so")
-SOURCES = ["planner.cpp", "plan.cpp", "transform.hip", "quant.hip", "gather.hip", "adam.hip", "muon.hip"]
+SOURCES = ["planner.cpp", "plan.cpp", "transform.hip", "quant.hip", "gather.hip", "adam.hip", "muon.hip", "embed.hip"]
 BENCH_LIB = os.path.join(HERE, "librs_bench.so")
 BENCH_SOURCES = ["stream_copy.hip", "selftest.hip"]
 
