@@ -236,9 +236,10 @@ enum Product {
 // waves, each 64 * (BM / 128) rows x 64 columns in 32 x 32 accumulators.
 // Operands go straight from memory to LDS, kMatK wide, in two stages: while
 // one stage is multiplied the next is on its way. In LDS a row is 128 bytes,
-// eight 16-byte pieces, piece c of row r at place c ^ (r & 7), so that the 32
-// rows a fragment takes spread over all banks; the loads permute the pieces
-// within each row's 128-byte line in memory. The fragment of the next 16
+// eight 16-byte pieces, piece c of row r at place c ^ (r / 2 % 8): two rows
+// fill the 64 banks once, and any 16 neighbouring rows of a fragment spread
+// over all of them; the loads permute the pieces within each row's 128-byte
+// line in memory. The fragment of the next 16
 // columns is read while the current one is multiplied; the stage turns over
 // (wait, barrier, new loads) before the last multiplication of a stage.
 template <int BM>
@@ -254,6 +255,22 @@ struct Tile {
   static constexpr int kPasses = NI / 2;         // the epilogue stages 2 blocks of rows per wave at a time
   static_assert(128 * BM * 4 <= kLds, "an epilogue pass fits the operand stages");
 };
+
+// Waits for all but VM of the wave's loads (and LDS reads, with LGKM). The
+// builtin, unlike assembly text, tells the compiler what has arrived.
+template <int VM, bool LGKM>
+__device__ __forceinline__ void wait() {
+  static_assert(VM < 16, "the low four bits of the counter");
+  __builtin_amdgcn_s_waitcnt(VM | 0x70 | (LGKM ? 0 : 0xf00));
+}
+
+// Workgroup barrier without a wait of its own; no memory access moves across.
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 template <int BM>
 struct Acc {
@@ -283,28 +300,35 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
   for (int t = 0; t < T::kLoads; ++t) {
     const int seg = (t % kHalf) * T::kWaves + wave;
     const int row = min(seg * 8 + lane / 8, (t < kHalf ? pr : qr) - 1);
-    off[t] = static_cast<int>(row * row_bytes) + ((lane % 8) ^ (lane / 8)) * 16;
+    off[t] = static_cast<int>(row * row_bytes) + ((lane % 8) ^ ((seg * 8 + lane / 8) / 2 % 8)) * 16;
   }
+  // LDS: P's two stages, then Q's two stages, so that a stage and a block are
+  // immediate offsets of a fragment read
+  constexpr int kHalfStage = T::kStage / 2;
   auto load = [&](int s) {
-    lds_char* dst = (lds_char*)(lds + (s & 1) * T::kStage) + wave * 1024;
     const int k = s * static_cast<int>(kMatK) * 2;
 #pragma unroll
-    for (int t = 0; t < T::kLoads; ++t)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(t < kHalf ? rp : rq, dst + t * T::kWaves * 1024, 16, off[t], k, 0, 0);
+    for (int t = 0; t < T::kLoads; ++t) {
+      lds_char* dst = (lds_char*)lds + (t < kHalf ? 0 : T::kStage) + (s & 1) * kHalfStage + wave * 1024 +
+                      (t % kHalf) * T::kWaves * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(t < kHalf ? rp : rq, dst, 16, off[t], k, 0, 0);
+    }
   };
   // fragment addresses: row lane % 32 of a block, columns kk*16 + lane/32*8 ..+7
   const int frow = lane % 32;
-  int fp[4];
+  const char *fp[4], *fq[4];
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) fp[kk] = frow * 128 + (((kk * 2 + lane / 32) ^ (frow & 7)) * 16);
-  const int pbase = wr * T::NI * 32 * 128, qbase = BM * 128 + wc * 64 * 128;
+  for (int kk = 0; kk < 4; ++kk) {
+    const int at = frow * 128 + (((kk * 2 + lane / 32) ^ (frow / 2 % 8)) * 16);
+    fp[kk] = lds + at + wr * T::NI * 32 * 128;
+    fq[kk] = lds + at + T::kStage + wc * 64 * 128;
+  }
   h8 fa[2][T::NI], fb[2][2];
-  auto fetch = [&](int s, int kk, int to) {
-    const char* b = lds + (s & 1) * T::kStage + fp[kk];
+  auto fetch = [&](int stage, int kk, int to) {
 #pragma unroll
-    for (int i = 0; i < T::NI; ++i) fa[to][i] = *reinterpret_cast<const h8*>(b + pbase + i * 4096);
+    for (int j = 0; j < 2; ++j) fb[to][j] = *reinterpret_cast<const h8*>(fq[kk] + stage * kHalfStage + j * 4096);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) fb[to][j] = *reinterpret_cast<const h8*>(b + qbase + j * 4096);
+    for (int i = 0; i < T::NI; ++i) fa[to][i] = *reinterpret_cast<const h8*>(fp[kk] + stage * kHalfStage + i * 4096);
   };
   auto mma = [&](int from) {
 #pragma unroll
@@ -313,30 +337,49 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
       for (int j = 0; j < 2; ++j)
         c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[from][i], fb[from][j], c.v[i][j], 0, 0, 0);
   };
+  // one fragment read between multiplications, so that none of them waits
+  auto interleave = [&]() {
+#pragma unroll
+    for (int i = 0; i < T::NI + 2; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one multiplication
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, T::NI * 2 - (T::NI + 2), 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // One stage: three sixteen-column multiplications, each while the next
+  // fragment is read; then, with every wave done reading this stage and the
+  // next stage arrived, the loads of the stage after that and the next
+  // stage's first fragment, under the fourth.
+  auto step = [&](int s, int stage, bool more_loads, bool more) {
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      fetch(stage, kk + 1, (kk + 1) & 1);
+      mma(kk & 1);
+      interleave();
+    }
+    wait<0, true>();
+    barrier();
+    if (more_loads) load(s + 2);
+    if (more) fetch(stage ^ 1, 0, 0);
+    mma(1);
+    __builtin_amdgcn_sched_barrier(0);
+  };
   load(0);
   if (ksteps > 1) {
     load(1);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(T::kLoads) : "memory");
+    wait<T::kLoads, false>();
   } else {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    wait<0, false>();
   }
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  barrier();
   fetch(0, 0, 0);
-  for (int s = 0; s < ksteps; ++s) {
-#pragma unroll
-    for (int kk = 0; kk < 3; ++kk) {
-      fetch(s, kk + 1, (kk + 1) & 1);
-      mma(kk & 1);
-    }
-    // every wave has read this stage and the next one has arrived
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (s + 2 < ksteps) load(s + 2);
-    if (s + 1 < ksteps) fetch(s + 1, 0, 0);
-    mma(1);
+  int s = 0;
+  for (; s + 3 < ksteps; s += 2) {
+    step(s, 0, true, true);
+    step(s + 1, 1, true, true);
   }
+  for (; s < ksteps; ++s) step(s, s & 1, s + 2 < ksteps, s + 1 < ksteps);
 }
 };
 
