@@ -253,7 +253,7 @@ struct Tile {
   static constexpr int kLds = 2 * kStage;
   static constexpr int kLoads = kStage / 1024 / kWaves;   // 1 KiB loads per wave and stage
   static constexpr int kPasses = NI / 2;         // the epilogue stages 2 blocks of rows per wave at a time
-  static_assert(128 * BM * 4 <= kLds, "an epilogue pass fits the operand stages");
+  static_assert(NI % 2 == 0 && 128 * BM * 4 <= kLds, "an epilogue pass fits the operand stages");
 };
 
 // Waits for all but VM of the wave's loads (and LDS reads, with LGKM). The
@@ -272,6 +272,15 @@ __device__ __forceinline__ void barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The thread's number, as a value that the compiler cannot see through: what
+// is computed from it is computed anew for each tile instead of being kept in
+// registers through the multiplication, which needs all of them.
+__device__ __forceinline__ int fresh_thread() {
+  int t = static_cast<int>(threadIdx.x);
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 template <int BM>
 struct Acc {
   f32x16 v[Tile<BM>::NI][2];
@@ -280,10 +289,12 @@ struct Acc {
 template <int BM>
 struct Multiply {
 __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q, int ld, int p0, int p_rows, int q0,
-                                         int q_rows, int ksteps, char* lds, Acc<BM>& c) {
+                                         int q_rows, int k0, int k1, char* lds, Acc<BM>& c) {
   using T = Tile<BM>;
-  const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int ksteps = k1 - k0;
+  const int tid = fresh_thread();
+  const int lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wr = wave / T::WC, wc = wave % T::WC;
   // rows past an operand's end repeat its last row: their results are not stored
   const int64_t row_bytes = static_cast<int64_t>(ld) * 2;
@@ -306,7 +317,7 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
   // immediate offsets of a fragment read
   constexpr int kHalfStage = T::kStage / 2;
   auto load = [&](int s) {
-    const int k = s * static_cast<int>(kMatK) * 2;
+    const int k = (k0 + s) * static_cast<int>(kMatK) * 2;
 #pragma unroll
     for (int t = 0; t < T::kLoads; ++t) {
       lds_char* dst = (lds_char*)lds + (t < kHalf ? 0 : T::kStage) + (s & 1) * kHalfStage + wave * 1024 +
@@ -390,44 +401,72 @@ __device__ __forceinline__ float update_scale(int mode, int rows, int cols) {
   return 1.0f;
 }
 
-// One output tile of one product. The accumulators go through LDS, 128 rows a
-// pass: a row-wise phase computes the result and stores it along its rows, a
-// column-wise phase stores its transpose. In LDS element (i, j) of a pass
-// lies at i * BM + (j ^ 4 * (i / 8 % 16)): 16-byte pieces along a row stay
-// whole, and the eight rows that a lane of the column-wise phase reads fall
-// into banks of their own.
+// The sums of one part of a cut tile, stored or added up in the order of the
+// parts. Slab element order is that of the registers: 16 bytes per thread.
+template <int BM>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t slab_of(char* slabs, int slab) {
+  constexpr int kSlab = BM * BM * 4;
+  return __builtin_amdgcn_make_buffer_rsrc(slabs + static_cast<int64_t>(slab) * kSlab, 0, kSlab, kRawBufferWord3);
+}
+
+template <int BM>
+struct Slab {
+using T = Tile<BM>;
+__device__ static __forceinline__ void store(const Acc<BM>& acc, char* slabs, int slab) {
+  const int mine = fresh_thread() * 16;
+  const __amdgpu_buffer_rsrc_t r = slab_of<BM>(slabs, slab);
+#pragma unroll
+  for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 x = {acc.v[i][j][4 * e], acc.v[i][j][4 * e + 1], acc.v[i][j][4 * e + 2], acc.v[i][j][4 * e + 3]};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, mine, ((i * 2 + j) * 4 + e) * T::kNT * 16, 0);
+      }
+}
+
+// Rows of 32-row blocks 2 * pass and 2 * pass + 1 of every wave.
+__device__ static __forceinline__ void load(f32x16 (&v)[2][2], char* slabs, int slab, int parts, int pass) {
+  const int mine = fresh_thread() * 16;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[i][j] = f32x16{};
+  for (int p = 0; p < parts; ++p) {
+    const __amdgpu_buffer_rsrc_t r = slab_of<BM>(slabs, slab + p);
+    f32x4 x[2][2][4];
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      x[q / 8][q / 4 % 2][q % 4] = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, mine, (pass * 16 + q) * T::kNT * 16, 0));
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) v[q / 8][q / 4 % 2][4 * (q % 4) + t] += x[q / 8][q / 4 % 2][q % 4][t];
+  }
+}
+};
+
+// What is stored of one tile, 128 rows (a pass) at a time. The accumulators of
+// the pass (two 32-row blocks of each wave) go through LDS: a row-wise phase
+// computes the result and stores it along its rows, a column-wise phase stores
+// its transpose. In LDS element (i, j) of a pass lies at
+// i * BM + (j ^ 4 * (i / 8 % 16)): 16-byte pieces along a row stay whole, and
+// the eight rows that a lane of the column-wise phase reads fall into banks of
+// their own. The pass's row r is the tile's row
+// (r / 64) * NI * 32 + pass * 64 + r % 64.
 template <int BM, Product WHAT>
-__global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __restrict__ mats,
-                                                             const MatJob* __restrict__ jobs, char* work, int turn,
-                                                             MuonK k, void* out) {
-  using T = Tile<BM>;
-  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
-  const MatJob job = jobs[piece_index<32>(blockIdx.x, gridDim.x)];
-  const MuonMat& q = mats[job.mat];
-  const int i0 = job.i * BM, j0 = job.j * BM;
+struct Store {
+using T = Tile<BM>;
+__device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const ProductJob& job, const MuonMat& q, int pass,
+                                           char* work, char* lds, int turn, const MuonK& k, void* out) {
   constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY;
+  const int i0 = job.i * BM, j0 = job.j * BM;
   const int m = q.m, n = q.n, mp = q.mp, np = q.np;
   const bool two = q.two_part;
-  const int jn = kSym ? m : n;                   // columns of this product
-  const char* p_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.b);
-  const char* q_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.xt[turn]);
-  const char* p_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.bl);
-  const char* q_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.xtl[turn]);
-  const int ld = WHAT == P_GRAM ? np : mp;
-  Acc<BM> acc = {};
-  for (int part = two ? 0 : 2; part < 3; ++part) {   // high * low, low * high, high * high
-    if (two && part == 2) {
-#pragma unroll
-      for (int i = 0; i < T::NI; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc.v[i][j] *= 1.0f / kLowScale;
-    }
-    Multiply<BM>::run(reinterpret_cast<const _Float16*>(part == 1 ? p_lo : p_hi),
-                      reinterpret_cast<const _Float16*>(part == 0 ? q_lo : q_hi), ld, i0, m, j0, jn,
-                      ld / static_cast<int>(kMatK), lds, acc);
-  }
-
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int jn = kSym ? m : n;
+  const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
   const int wr = wave / T::WC, wc = wave % T::WC;
   float* stage = reinterpret_cast<float*>(lds);
   float* da = reinterpret_cast<float*>(work + q.da);
@@ -443,26 +482,19 @@ __global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __re
   const float ex = static_cast<float>(1 << q.ex);
   const bool tall = q.tall;
   const float step = WHAT == P_STEP ? k.lr * update_scale(k.scale_mode, q.rows, q.cols) / ex : 0.0f;
-  // the pass's row r is the tile's row (r / 64) * NI * 32 + pass * 64 + r % 64
-  for (int pass = 0; pass < T::kPasses; ++pass) {
-    if (pass) __syncthreads();
 #pragma unroll
-    for (int p = 0; p < T::kPasses; ++p) {
-      if (p != pass) continue;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int row = wr * 64 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-            const int col = wc * 64 + j * 32 + lane % 32;
-            stage[row * BM + (col ^ (4 * (row / 8 % 16)))] = acc.v[2 * p + i][j][r];
-          }
-    }
+        for (int r = 0; r < 16; ++r) {
+          const int row = wr * 64 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+          const int col = wc * 64 + j * 32 + lane % 32;
+          stage[row * BM + (col ^ (4 * (row / 8 % 16)))] = acc[i][j][r];
+        }
     __syncthreads();
     // row-wise: 8 columns per thread
-    for (int e = threadIdx.x; e < 128 * (BM / 8); e += T::kNT) {
+    for (int e = tid; e < 128 * (BM / 8); e += T::kNT) {
       const int r = e / (BM / 8), c = e % (BM / 8) * 8;
       const int i = i0 + (r / 64) * (T::NI * 32) + pass * 64 + r % 64, j = j0 + c;
       const int sw = 4 * (r / 8 % 16);
@@ -589,9 +621,9 @@ __global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __re
     }
     // column-wise: 8 rows per thread, 16 threads along a column of the pass
     const bool mirror = kSym ? job.i != job.j : WHAT == P_APPLY || tall;
-    if (!mirror) continue;
+    if (!mirror) return;
     __syncthreads();
-    for (int e = threadIdx.x; e < BM * 16; e += T::kNT) {
+    for (int e = tid; e < BM * 16; e += T::kNT) {
       const int r = e % 16 * 8, c = e / 16;
       const int i = i0 + (r / 64) * (T::NI * 32) + pass * 64 + r % 64, j = j0 + c;
       const int sw = 4 * (r / 8 % 16);
@@ -642,19 +674,79 @@ __global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __re
         }
       }
     }
+}
+};
+
+// One job of one product.
+template <int BM, Product WHAT>
+__global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __restrict__ mats,
+                                                             const ProductJob* __restrict__ jobs, char* work,
+                                                             int64_t slabs, int turn, MuonK k, void* out) {
+  using T = Tile<BM>;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const ProductJob job = jobs[blockIdx.x];
+  const MuonMat& q = mats[job.mat];
+  const int ld = WHAT == P_GRAM ? q.np : q.mp;
+  const char* p_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.b);
+  const char* q_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.xt[turn]);
+  const char* p_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.bl);
+  const char* q_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.xtl[turn]);
+  const bool two = q.two_part;
+  Acc<BM> acc = {};
+  for (int part = two ? 0 : 2; part < 3; ++part) {   // high * low, low * high, high * high
+    if (two && part == 2) {
+#pragma unroll
+      for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc.v[i][j] *= 1.0f / kLowScale;
+    }
+    Multiply<BM>::run(reinterpret_cast<const _Float16*>(part == 1 ? p_lo : p_hi),
+                      reinterpret_cast<const _Float16*>(part == 0 ? q_lo : q_hi), ld, job.i * BM, q.m, job.j * BM,
+                      WHAT == P_GRAM || WHAT == P_POLY ? q.m : q.n, job.k0, job.k1, lds, acc);
   }
+  if (job.parts > 1) {
+    Slab<BM>::store(acc, work + slabs, job.slab);
+    return;
+  }
+  f32x16 (&v)[T::NI][2] = acc.v;
+  Store<BM, WHAT>::run(reinterpret_cast<const f32x16 (&)[2][2]>(v[0]), job, q, 0, work, lds, turn, k, out);
+  if constexpr (T::kPasses == 2) {
+    __syncthreads();
+    Store<BM, WHAT>::run(reinterpret_cast<const f32x16 (&)[2][2]>(v[2]), job, q, 1, work, lds, turn, k, out);
+  }
+}
+
+// One pass of one cut tile: its parts' sums added up, then stored as above.
+template <int BM, Product WHAT>
+__global__ __launch_bounds__(BM * 2) void mat_join_kernel(const MuonMat* __restrict__ mats,
+                                                          const ProductJob* __restrict__ joins, char* work,
+                                                          int64_t slabs, int turn, MuonK k, void* out) {
+  using T = Tile<BM>;
+  __shared__ __attribute__((aligned(16))) char lds[128 * BM * 4];
+  const ProductJob job = joins[blockIdx.x / T::kPasses];
+  const int pass = blockIdx.x % T::kPasses;
+  f32x16 v[2][2];
+  Slab<BM>::load(v, work + slabs, job.slab, job.parts, pass);
+  Store<BM, WHAT>::run(v, job, mats[job.mat], pass, work, lds, turn, k, out);
 }
 
 // ------------------------------------------------------------------ launches
 
+template <int BM, Product WHAT>
+void launch_tiles(const rs_plan* p, int list, char* work, int turn, const MuonK& k, void* out, hipStream_t s) {
+  hipLaunchKernelGGL((mat_product_kernel<BM, WHAT>), dim3(static_cast<unsigned>(p->n_mat_jobs[list])), dim3(BM * 2), 0,
+                     s, p->mats, p->mat_jobs[list], work, p->mat_slabs, turn, k, out);
+  if (p->n_mat_joins[list])
+    hipLaunchKernelGGL((mat_join_kernel<BM, WHAT>),
+                       dim3(static_cast<unsigned>(p->n_mat_joins[list] * Tile<BM>::kPasses)), dim3(BM * 2), 0, s,
+                       p->mats, p->mat_joins[list], work, p->mat_slabs, turn, k, out);
+}
+
 template <Product WHAT>
-void launch_product(const rs_plan* p, int side, const MatJob* jobs, int64_t n_jobs, char* work, int turn,
-                    const MuonK& k, void* out, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(n_jobs));
-  if (side == 256)
-    hipLaunchKernelGGL((mat_product_kernel<256, WHAT>), grid, dim3(512), 0, s, p->mats, jobs, work, turn, k, out);
-  else
-    hipLaunchKernelGGL((mat_product_kernel<128, WHAT>), grid, dim3(256), 0, s, p->mats, jobs, work, turn, k, out);
+void launch_product(const rs_plan* p, char* work, int turn, const MuonK& k, void* out, hipStream_t s) {
+  constexpr int kList = WHAT == P_GRAM ? 0 : WHAT == P_POLY ? 1 : 2;
+  if (p->mat_side[kList] == 256) launch_tiles<256, WHAT>(p, kList, work, turn, k, out, s);
+  else launch_tiles<128, WHAT>(p, kList, work, turn, k, out, s);
 }
 
 // Momentum (MUON), norm and Newton-Schulz on every matrix of the plan; the
@@ -683,12 +775,10 @@ int run_matrices(rs_plan* p, const void* grad, int32_t grad_dt, float* mom, cons
     k.a = coeffs[3 * t];
     k.b = coeffs[3 * t + 1];
     k.c = coeffs[3 * t + 2];
-    launch_product<P_GRAM>(p, p->mat_tile_sym, p->mat_sym, p->n_mat_sym, work, t & 1, k, nullptr, s);
-    launch_product<P_POLY>(p, p->mat_tile_sym, p->mat_sym, p->n_mat_sym, work, t & 1, k, nullptr, s);
-    if (t + 1 < steps)
-      launch_product<P_APPLY>(p, p->mat_tile_full, p->mat_full, p->n_mat_full, work, t & 1, k, nullptr, s);
-    else
-      launch_product<MUON ? P_STEP : P_OUT>(p, p->mat_tile_full, p->mat_full, p->n_mat_full, work, t & 1, k, out, s);
+    launch_product<P_GRAM>(p, work, t & 1, k, nullptr, s);
+    launch_product<P_POLY>(p, work, t & 1, k, nullptr, s);
+    if (t + 1 < steps) launch_product<P_APPLY>(p, work, t & 1, k, nullptr, s);
+    else launch_product<MUON ? P_STEP : P_OUT>(p, work, t & 1, k, out, s);
   }
   return launched(who);
 }

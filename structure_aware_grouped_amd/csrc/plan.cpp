@@ -7,6 +7,7 @@
 #include <cassert>
 #include <cstdlib>
 #include <cstring>
+#include <functional>
 #include <string>
 #include <vector>
 
@@ -482,6 +483,143 @@ void lower_quant(const std::vector<Tensor>& t, int64_t top, QuantList* ql) {
   }
 }
 
+namespace {
+
+struct ProductTile {
+  int32_t mat;
+  uint16_t i, j;
+  int32_t steps;   // of kMatK
+  int32_t weight;  // multiplications per step (3 with high and low parts)
+};
+
+// The jobs of one product. Whole rounds of one tile per workgroup come first:
+// the workgroups of an XCD take neighbouring tiles and run in step, so that
+// they share operand rows in its L2 (out of step, with tiles cut at different
+// places ahead of them, an 8192 x 28672 product took 4.25 ms instead of 3.49).
+// The tiles left over (528 tiles of an 8192-row X X^T are 2.06 rounds) are laid
+// end to end into what room the workgroups have below a common end, and cut
+// where one workgroup's room ends and the next one's begins. A job starts
+// when a workgroup's place is free, so jobs are listed longest first within
+// the rounds' order.
+void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* out) {
+  struct Part {
+    int tile, k0, k1;
+  };
+  std::vector<Part> parts;
+  auto cost = [&](int t, int steps) { return int64_t(steps) * tiles[t].weight; };
+  const int n = static_cast<int>(tiles.size()), whole = n / groups * groups;
+  auto give = [&](int t) {
+    const ProductTile& x = tiles[t];
+    out->jobs.push_back({x.mat, x.i, x.j, 0, static_cast<uint16_t>(x.steps), 1, 0, -1});
+  };
+  // XCD x runs workgroups x, x + 8, ...: its run of each round
+  const int per = groups / kXcds;
+  for (int r = 0; r < whole; r += groups)
+    for (int q = 0; q < per; ++q)
+      for (int x = 0; x < kXcds; ++x) give(r + x * per + q);
+  if (whole == n) return;
+  // the workgroups' loads when each takes the next tile as it becomes free
+  std::vector<int64_t> load(groups, 0);
+  for (int t = 0; t < whole; ++t) {
+    std::pop_heap(load.begin(), load.end(), std::greater<int64_t>());
+    load.back() += cost(t, tiles[t].steps);
+    std::push_heap(load.begin(), load.end(), std::greater<int64_t>());
+  }
+  std::sort(load.begin(), load.end());
+  int64_t left = 0, longest = 0;
+  for (int t = whole; t < n; ++t) {
+    left += cost(t, tiles[t].steps);
+    longest = std::max(longest, cost(t, tiles[t].steps));
+  }
+  // the end at which the room below it holds what is left
+  int64_t end = 0, below = 0;
+  for (int c = 1; c <= groups; ++c) {
+    below += load[c - 1];
+    end = ceil_div(left + below, c);
+    if (c == groups || end <= load[c]) break;
+  }
+  const int64_t least = std::max<int64_t>(ceil_div(longest, kMatMaxParts - 1), kMatMinSteps);
+  // no cuts where they would save less than joining the parts costs
+  if (load[0] + longest - std::max(end, load[0] + least) <= kMatJoinSteps) {
+    for (int t = whole; t < n; ++t) give(t);
+    return;
+  }
+  int c = 0;
+  int64_t room = std::max(end - load[0], least);
+  for (int t = whole; t < n; ++t) {
+    for (int k = 0; k < tiles[t].steps;) {
+      const int rest = tiles[t].steps - k;
+      int take = static_cast<int>(std::min<int64_t>(rest, std::max<int64_t>(1, room / tiles[t].weight)));
+      if (rest - take < kMatMinSteps || c == groups - 1) take = rest;   // no short rest
+      parts.push_back({t, k, k + take});
+      k += take;
+      room -= cost(t, take);
+      if (room < kMatMinSteps * int64_t(tiles[t].weight) && c + 1 < groups) {
+        ++c;
+        room = std::max(end - load[c], least);
+      }
+    }
+  }
+  std::vector<int> count(n, 0), slab(n, -1);
+  for (const Part& p : parts) ++count[p.tile];
+  for (int t = whole; t < n; ++t) {
+    if (count[t] < 2) continue;
+    slab[t] = out->slabs;
+    out->slabs += count[t];
+    const ProductTile& x = tiles[t];
+    out->joins.push_back({x.mat, x.i, x.j, 0, static_cast<uint16_t>(x.steps), static_cast<uint16_t>(count[t]), 0, slab[t]});
+  }
+  std::vector<std::pair<int64_t, ProductJob>> jobs;
+  for (size_t p = 0; p < parts.size(); ++p) {
+    const Part& a = parts[p];
+    const ProductTile& x = tiles[a.tile];
+    const bool first = !p || parts[p - 1].tile != a.tile;
+    jobs.push_back({cost(a.tile, a.k1 - a.k0),
+                    {x.mat, x.i, x.j, static_cast<uint16_t>(a.k0), static_cast<uint16_t>(a.k1),
+                     static_cast<uint16_t>(count[a.tile]), 0,
+                     count[a.tile] < 2 ? -1 : first ? slab[a.tile] : jobs.back().second.slab + 1}});
+  }
+  std::stable_sort(jobs.begin(), jobs.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
+  for (const auto& j : jobs) out->jobs.push_back(j.second);
+}
+
+// The tiles of one product over all matrices and their schedule. sym: only
+// tiles on and below the diagonal of an m x m product; over_n: the
+// contraction runs over n (X X^T), else over m.
+void lower_product(const std::vector<MuonMat>& mats, bool sym, bool over_n, ProductList* out) {
+  auto count = [&](int64_t side) {
+    int64_t c = 0;
+    for (const MuonMat& q : mats) {
+      const int64_t a = ceil_div(q.m, side), b = ceil_div(q.n, side);
+      c += sym ? a * (a + 1) / 2 : a * b;
+    }
+    return c;
+  };
+  out->side = count(256) >= kMatMinTiles ? 256 : 128;
+  // RS_MUON_TILE=128|256 forces one size
+  if (const char* e = std::getenv("RS_MUON_TILE")) {
+    const int side = std::atoi(e);
+    if (side == 128 || side == 256) out->side = side;
+  }
+  // tiles in blocks of kBlock x kBlock: what runs together shares operand rows
+  constexpr int64_t kBlock = 6;
+  std::vector<ProductTile> tiles;
+  for (int32_t k = 0; k < static_cast<int32_t>(mats.size()); ++k) {
+    const MuonMat& q = mats[k];
+    const int64_t ti = ceil_div(q.m, out->side), tj = sym ? ti : ceil_div(q.n, out->side);
+    const int32_t steps = static_cast<int32_t>((over_n ? q.np : q.mp) / kMatK);
+    for (int64_t i0 = 0; i0 < ti; i0 += kBlock)
+      for (int64_t j0 = 0; j0 < tj; j0 += kBlock)
+        for (int64_t i = i0; i < std::min(ti, i0 + kBlock); ++i)
+          for (int64_t j = j0; j < std::min(tj, j0 + kBlock); ++j)
+            if (!sym || j <= i)
+              tiles.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j), steps, q.two_part ? 3 : 1});
+  }
+  schedule(tiles, out->side == 256 ? kMatGroups : 2 * kMatGroups, out);
+}
+
+}  // namespace
+
 // The whole matrices of a plan: where their operands lie in the workspace and
 // the work lists of the passes over them (rs_orthogonalize, rs_muon_step).
 void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
@@ -535,42 +673,21 @@ void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
     q.inv = take(8);
     mt->mats.push_back(q);
   }
-  mt->work_bytes = at;
-  auto tiles = [&](int64_t side, bool sym) {
-    int64_t c = 0;
-    for (const MuonMat& q : mt->mats) {
-      const int64_t a = ceil_div(q.m, side), b = ceil_div(q.n, side);
-      c += sym ? a * (a + 1) / 2 : a * b;
-    }
-    return c;
-  };
-  mt->tile_sym = tiles(256, true) >= kMatMinTiles ? 256 : 128;
-  mt->tile_full = tiles(256, false) >= kMatMinTiles ? 256 : 128;
-  // RS_MUON_TILE=128|256 forces one size
-  if (const char* e = std::getenv("RS_MUON_TILE")) {
-    const int side = std::atoi(e);
-    if (side == 128 || side == 256) mt->tile_sym = mt->tile_full = side;
-  }
-  // Tiles in blocks of kBlock x kBlock: the workgroups that run together on
-  // one XCD share their operands' rows in its L2.
-  constexpr int64_t kBlock = 6;
   for (int32_t k = 0; k < static_cast<int32_t>(mt->mats.size()); ++k) {
     const MuonMat& q = mt->mats[k];
     for (int32_t c = 0; c < q.n_part; ++c) mt->chunks.push_back({k, c});
     for (int64_t i = 0; i < ceil_div(q.m, kMatSpread); ++i)
       for (int64_t j = 0; j < ceil_div(q.n, kMatSpread); ++j)
         mt->spread.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j)});
-    for (const bool sym : {true, false}) {
-      const int64_t side = sym ? mt->tile_sym : mt->tile_full;
-      const int64_t ti = ceil_div(q.m, side), tj = sym ? ti : ceil_div(q.n, side);
-      std::vector<MatJob>& out = sym ? mt->sym : mt->full;
-      for (int64_t i0 = 0; i0 < ti; i0 += kBlock)
-        for (int64_t j0 = 0; j0 < tj; j0 += kBlock)
-          for (int64_t i = i0; i < std::min(ti, i0 + kBlock); ++i)
-            for (int64_t j = j0; j < std::min(tj, j0 + kBlock); ++j)
-              if (!sym || j <= i) out.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j)});
-    }
   }
+  int64_t slab_bytes = 0;
+  for (int w = 0; w < 3; ++w) {
+    lower_product(mt->mats, w != 2, w == 0, &mt->list[w]);
+    const ProductList& l = mt->list[w];
+    slab_bytes = std::max(slab_bytes, int64_t(4) * l.side * l.side * l.slabs);
+  }
+  mt->slabs = take(slab_bytes);
+  mt->work_bytes = at;
 }
 
 }  // namespace rs
@@ -665,11 +782,13 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->n_mats = static_cast<int64_t>(mt.mats.size());
     p->n_mat_chunks = static_cast<int64_t>(mt.chunks.size());
     p->n_mat_spread = static_cast<int64_t>(mt.spread.size());
-    p->n_mat_sym = static_cast<int64_t>(mt.sym.size());
-    p->n_mat_full = static_cast<int64_t>(mt.full.size());
-    p->mat_tile_sym = mt.tile_sym;
-    p->mat_tile_full = mt.tile_full;
+    for (int w = 0; w < 3; ++w) {
+      p->n_mat_jobs[w] = static_cast<int64_t>(mt.list[w].jobs.size());
+      p->n_mat_joins[w] = static_cast<int64_t>(mt.list[w].joins.size());
+      p->mat_side[w] = mt.list[w].side;
+    }
     p->mat_work_bytes = mt.work_bytes;
+    p->mat_slabs = mt.slabs;
     p->mat_too_large = mt.too_large;
     // gfx950's FP8 conversion (OCP E4M3, round to nearest even) by default;
     // RS_E4M3_ENCODER=sw selects the integer encoder, which gives the same codes.
@@ -693,6 +812,10 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
       p->max_grid = std::max<int64_t>(8, std::min<int64_t>(kMaxGrid, v) / 8 * 8);
     }
 
+    int64_t list_bytes = 0;
+    for (const ProductList& l : mt.list)
+      list_bytes += align_up(sizeof(ProductJob) * std::max<size_t>(l.jobs.size(), 1), 256) +
+                    align_up(sizeof(ProductJob) * std::max<size_t>(l.joins.size(), 1), 256);
     const int64_t bytes = align_up(sizeof(TmJob) * std::max<int64_t>(p->n_tm, 1), 256) +
                           align_up(sizeof(CopyChunk) * std::max<int64_t>(p->n_unpack, 1), 256) +
                           align_up(sizeof(PackChunk) * std::max<int64_t>(p->n_pack, 1), 256) +
@@ -702,8 +825,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
                           align_up(sizeof(MuonMat) * std::max<int64_t>(p->n_mats, 1), 256) +
                           align_up(sizeof(MatChunk) * std::max<int64_t>(p->n_mat_chunks, 1), 256) +
                           align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_spread, 1), 256) +
-                          align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_sym, 1), 256) +
-                          align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_full, 1), 256) +
+                          list_bytes +
                           3 * align_up(sizeof(void*) * n, 256);
     if (hipMalloc(&p->dmem, bytes) != hipSuccess) {
       p->dmem = nullptr;
@@ -721,8 +843,10 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->mats = carve<MuonMat>(cur, p->n_mats);
     p->mat_chunks = carve<MatChunk>(cur, p->n_mat_chunks);
     p->mat_spread = carve<MatJob>(cur, p->n_mat_spread);
-    p->mat_sym = carve<MatJob>(cur, p->n_mat_sym);
-    p->mat_full = carve<MatJob>(cur, p->n_mat_full);
+    for (int w = 0; w < 3; ++w) {
+      p->mat_jobs[w] = carve<ProductJob>(cur, p->n_mat_jobs[w]);
+      p->mat_joins[w] = carve<ProductJob>(cur, p->n_mat_joins[w]);
+    }
     void** dst_dev = carve<void*>(cur, n);
     void** src_dev = carve<void*>(cur, n);
     void** gdst_dev = carve<void*>(cur, n);
@@ -734,7 +858,9 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
               (p->n_gchunks == 0 || hipMemcpy(p->gchunks, tb.gchunks.data(), sizeof(GatherChunk) * p->n_gchunks, hipMemcpyHostToDevice) == hipSuccess) &&
               (tb.gjobs.empty() || hipMemcpy(p->gjobs, tb.gjobs.data(), sizeof(QJob) * tb.gjobs.size(), hipMemcpyHostToDevice) == hipSuccess) &&
               upload(p->mats, mt.mats) && upload(p->mat_chunks, mt.chunks) && upload(p->mat_spread, mt.spread) &&
-              upload(p->mat_sym, mt.sym) && upload(p->mat_full, mt.full);
+              upload(p->mat_jobs[0], mt.list[0].jobs) && upload(p->mat_joins[0], mt.list[0].joins) &&
+              upload(p->mat_jobs[1], mt.list[1].jobs) && upload(p->mat_joins[1], mt.list[1].joins) &&
+              upload(p->mat_jobs[2], mt.list[2].jobs) && upload(p->mat_joins[2], mt.list[2].joins);
     if (!ok) {
       release(p);
       (void)hipSetDevice(prev);

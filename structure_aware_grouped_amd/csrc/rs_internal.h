@@ -315,6 +315,13 @@ constexpr int64_t kMatMaxMin = int64_t(1) << 16;
 // A product takes 256 x 256 output tiles where the plan's matrices give at
 // least kMatMinTiles of them, else 128 x 128.
 constexpr int64_t kMatMinTiles = 200;
+// Workgroups of a product launch: one per CU with 256-wide tiles (128 KiB of
+// LDS each), two with 128-wide ones.
+constexpr int kMatGroups = 256;
+constexpr int kXcds = 8;
+constexpr int kMatMaxParts = 8;    // a tile's contraction is cut into at most this many parts
+constexpr int kMatMinSteps = 4;    // steps of kMatK in a part, at least
+constexpr int kMatJoinSteps = 10;  // joining parts costs about this many steps
 // Elements per work item of the pass that updates momentum and sums squares.
 constexpr int64_t kMatChunk = 8192;
 // Tile of the pass that splits the scaled matrix into its operands.
@@ -338,15 +345,34 @@ struct MuonMat {
   int32_t two_part;   // m <= kMatTwoPart: every operand has a low part
 };
 
-// Work items of the matrix passes: a chunk of kMatChunk elements (i = chunk),
-// a spread tile or a product's output tile (i, j = tile row and column of X).
+// Work items of the matrix passes: a chunk of kMatChunk elements; a spread
+// tile (i, j = its tile row and column of X).
+struct MatChunk {
+  int32_t mat;
+  int32_t chunk;
+};
 struct MatJob {
   int32_t mat;
   uint16_t i, j;
 };
-struct MatChunk {
+
+// Steps [k0, k1) of kMatK of one output tile of a product, one workgroup
+// each. A tile cut into `parts` jobs has one slab of fp32 sums per part
+// (slab .. slab + parts - 1) in the workspace; a second launch adds them up.
+struct ProductJob {
   int32_t mat;
-  int32_t chunk;
+  uint16_t i, j;
+  uint16_t k0, k1;
+  uint16_t parts, unused;
+  int32_t slab;        // this part's (in `joins`: the first part's)
+};
+
+// The jobs of one product launch, in the order in which they start.
+struct ProductList {
+  std::vector<ProductJob> jobs;
+  std::vector<ProductJob> joins;   // the cut tiles
+  int side = 0;                    // tile side
+  int32_t slabs = 0;
 };
 
 // The matrices of a plan and the work lists of their passes, on the host.
@@ -354,10 +380,9 @@ struct MuonTables {
   std::vector<MuonMat> mats;         // longest contraction first
   std::vector<MatChunk> chunks;
   std::vector<MatJob> spread;
-  std::vector<MatJob> sym;           // tiles on and below the diagonal of an m x m product
-  std::vector<MatJob> full;          // tiles of an m x n product
-  int tile_sym = 0, tile_full = 0;   // tile sides
+  ProductList list[3];               // X X^T, A A, polynomial times X
   int64_t work_bytes = 0;
+  int64_t slabs = 0;                 // in the workspace
   bool too_large = false;            // a matrix beyond kMatMaxSide / kMatMaxMin
 };
 void lower_muon(const std::vector<Tensor>& t, MuonTables* mt);
@@ -434,11 +459,12 @@ struct rs_plan {
   rs::MuonMat* mats = nullptr;         // whole matrices and their work lists
   rs::MatChunk* mat_chunks = nullptr;
   rs::MatJob* mat_spread = nullptr;
-  rs::MatJob* mat_sym = nullptr;
-  rs::MatJob* mat_full = nullptr;
-  int64_t n_mats = 0, n_mat_chunks = 0, n_mat_spread = 0, n_mat_sym = 0, n_mat_full = 0;
-  int mat_tile_sym = 0, mat_tile_full = 0;
-  int64_t mat_work_bytes = 0;
+  rs::ProductJob* mat_jobs[3] = {};    // X X^T, A A, polynomial times X
+  rs::ProductJob* mat_joins[3] = {};   // their cut tiles
+  int64_t n_mat_jobs[3] = {}, n_mat_joins[3] = {};
+  int mat_side[3] = {};
+  int64_t n_mats = 0, n_mat_chunks = 0, n_mat_spread = 0;
+  int64_t mat_work_bytes = 0, mat_slabs = 0;
   bool mat_too_large = false;
 
   rs::PtrTable dst;   // unpack destinations
