@@ -147,17 +147,6 @@ __device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
   lo = static_cast<_Float16>((x - static_cast<float>(hi)) * kLowScale);
 }
 
-__device__ __forceinline__ h8 low_parts(const float (&v)[8]) {
-  h8 h;
-#pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    _Float16 hi, lo;
-    split(v[t], hi, lo);
-    h[t] = lo;
-  }
-  return h;
-}
-
 // One 64 x 64 tile of X from the gradient (and momentum): scaled, split, and
 // written as X's high and low parts and the transposed high part (for
 // m <= kMatTwoPart the low one too), zeros in the padding of the contraction dimensions.
@@ -456,224 +445,234 @@ __device__ static __forceinline__ void load(f32x16 (&v)[2][2], char* slabs, int 
 // the eight rows that a lane of the column-wise phase reads fall into banks of
 // their own. The pass's row r is the tile's row
 // (r / 64) * NI * 32 + pass * 64 + r % 64.
+//   In the row-wise phase a thread has eight columns of eight rows. What it
+// reads of them from memory is fetched kAhead rows at a time, the first ones
+// before the accumulators go to LDS: one row at a time the loads of a row
+// waited for the stores of the one before (20 us for one 128-wide tile).
 template <int BM, Product WHAT>
 struct Store {
 using T = Tile<BM>;
+static constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY;
+static constexpr bool kLast = WHAT == P_OUT || WHAT == P_STEP;
+static constexpr int kRows = 8;
+static constexpr int kAhead = WHAT == P_STEP ? 2 : 4;
+static_assert(128 * (BM / 8) == kRows * T::kNT, "eight rows of eight columns per thread");
+
+struct In8 {   // of one row: A (POLY) or X, high and low; parameters (STEP)
+  h8 hi, lo;
+  float d;
+  f32x4 p[2];
+};
+
+// Rounded to bf16, or subtracted from the parameters; e elements from dst on
+// lie inside the matrix, whole: 16-byte aligned and all eight inside.
+__device__ static __forceinline__ void finish(void* out, int64_t at, const float (&v)[8], int e, bool whole, float f,
+                                              float decay, const f32x4 (&p)[2]) {
+  if constexpr (WHAT == P_OUT) {
+    uint16_t* dst = static_cast<uint16_t*>(out) + at;
+    uint32_t w[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) w[t] = bf16_rne(v[t] * f);
+    if (whole) {
+      *reinterpret_cast<u32x4*>(dst) = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (t < e) dst[t] = static_cast<uint16_t>(w[t]);
+    }
+  } else {
+    float* dst = static_cast<float*>(out) + at;
+    if (whole) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4 x;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = __fsub_rn(__fmul_rn(p[h][t], decay), __fmul_rn(f, v[4 * h + t]));
+        reinterpret_cast<f32x4*>(dst)[h] = x;
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (t < e) dst[t] = __fsub_rn(__fmul_rn(dst[t], decay), __fmul_rn(f, v[t]));
+    }
+  }
+}
+
 __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const ProductJob& job, const MuonMat& q, int pass,
                                            char* work, char* lds, int turn, const MuonK& k, void* out) {
-  constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY;
   const int i0 = job.i * BM, j0 = job.j * BM;
   const int m = q.m, n = q.n, mp = q.mp, np = q.np;
-  const bool two = q.two_part;
-  const int jn = kSym ? m : n;
+  const bool two = q.two_part, tall = q.tall;
+  const int jn = kSym ? m : n, jp = kSym ? mp : np;   // columns of this product, and padded
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
   const int wr = wave / T::WC, wc = wave % T::WC;
   float* stage = reinterpret_cast<float*>(lds);
-  float* da = reinterpret_cast<float*>(work + q.da);
-  float* db = reinterpret_cast<float*>(work + q.db);
-  _Float16* pa = reinterpret_cast<_Float16*>(work + q.a);
-  _Float16* pb = reinterpret_cast<_Float16*>(work + q.b);
-  _Float16* xh = reinterpret_cast<_Float16*>(work + q.xh);
-  _Float16* xl = reinterpret_cast<_Float16*>(work + q.xl);
-  _Float16* xt = reinterpret_cast<_Float16*>(work + q.xt[turn ^ 1]);
-  _Float16* pal = reinterpret_cast<_Float16*>(work + q.al);     // used where `two` only
-  _Float16* pbl = reinterpret_cast<_Float16*>(work + q.bl);
-  _Float16* xtl = reinterpret_cast<_Float16*>(work + q.xtl[turn ^ 1]);
   const float ex = static_cast<float>(1 << q.ex);
-  const bool tall = q.tall;
-  const float step = WHAT == P_STEP ? k.lr * update_scale(k.scale_mode, q.rows, q.cols) / ex : 0.0f;
+  // factor of the stored X in the result
+  const float f = WHAT == P_STEP ? k.lr * update_scale(k.scale_mode, q.rows, q.cols) / ex : 1.0f / ex;
+  float* diag = reinterpret_cast<float*>(work + (WHAT == P_GRAM || WHAT == P_POLY ? q.da : q.db));
+
+  // row-wise: rows i0 + row(it), columns j .. j + 7
+  const int r0 = tid / (BM / 8), c = tid % (BM / 8) * 8, j = j0 + c;
+  auto row = [&](int it) { return i0 + (it / 4) * (T::NI * 32) + pass * 64 + r0 + 16 * (it % 4); };
+  const char* in_hi = work + (WHAT == P_POLY ? q.a : q.xh);
+  const char* in_lo = work + (WHAT == P_POLY ? q.al : q.xl);
+  const bool read_lo = WHAT != P_POLY || two;
+  const bool step_rows = WHAT == P_STEP && !tall, whole_row = j + 8 <= n && n % 8 == 0;
+  In8 in[2][kAhead];
+  auto fetch = [&](int group) {
+    if constexpr (WHAT != P_GRAM) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int row = wr * 64 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-          const int col = wc * 64 + j * 32 + lane % 32;
-          stage[row * BM + (col ^ (4 * (row / 8 % 16)))] = acc[i][j][r];
-        }
-    __syncthreads();
-    // row-wise: 8 columns per thread
-    for (int e = tid; e < 128 * (BM / 8); e += T::kNT) {
-      const int r = e / (BM / 8), c = e % (BM / 8) * 8;
-      const int i = i0 + (r / 64) * (T::NI * 32) + pass * 64 + r % 64, j = j0 + c;
-      const int sw = 4 * (r / 8 % 16);
-      f32x4* s0 = reinterpret_cast<f32x4*>(stage + r * BM + (c ^ sw));
-      f32x4* s1 = reinterpret_cast<f32x4*>(stage + r * BM + ((c + 4) ^ sw));
-      float v[8];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) { v[t] = (*s0)[t]; v[4 + t] = (*s1)[t]; }
-      const bool in = i < m && j < jn;
-      if constexpr (WHAT == P_GRAM) {
-        const float f = kOpScale / (ex * ex);
-        h8 h;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          v[t] = in && j + t < jn ? v[t] * f : 0.0f;
-          if (in && i == j + t) {
-            da[i] = v[t] / kOpScale;
-            v[t] = 0.0f;
-          }
-          h[t] = static_cast<_Float16>(v[t]);
-        }
-        if (i < m && j < mp) {
-          *reinterpret_cast<h8*>(pa + static_cast<int64_t>(i) * mp + j) = h;
-          if (two) *reinterpret_cast<h8*>(pal + static_cast<int64_t>(i) * mp + j) = low_parts(v);
-        }
-      } else if constexpr (WHAT == P_POLY) {
-        h8 h = {};
-        if (in) {
-          const h8 o = *reinterpret_cast<const h8*>(pa + static_cast<int64_t>(i) * mp + j);
-          const float di = da[i];
-          h8 ol = {};
-          if (two) ol = *reinterpret_cast<const h8*>(pal + static_cast<int64_t>(i) * mp + j);
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            if (j + t >= jn) {
-              v[t] = 0.0f;
-            } else if (i == j + t) {
-              const float rest = k.b * di + k.c * (v[t] / (kOpScale * kOpScale) + di * di);
-              const bool whole = di > 0.5f;
-              db[i] = whole ? k.a + rest : k.a;
-              v[t] = whole ? 0.0f : rest * kOpScale;
-            } else {
-              const float x = static_cast<float>(o[t]) + static_cast<float>(ol[t]) * (1.0f / kLowScale);
-              v[t] = k.b * x + k.c * (v[t] / kOpScale + (di + da[j + t]) * x);
-            }
-            h[t] = static_cast<_Float16>(v[t]);
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) v[t] = 0.0f;
-        }
-        if (i < m && j < mp) {
-          *reinterpret_cast<h8*>(pb + static_cast<int64_t>(i) * mp + j) = h;
-          if (two) *reinterpret_cast<h8*>(pbl + static_cast<int64_t>(i) * mp + j) = low_parts(v);
-        }
-      } else {
-        if (in) {
-          const int64_t at = static_cast<int64_t>(i) * np + j;
-          const h8 hi = *reinterpret_cast<const h8*>(xh + at), lo = *reinterpret_cast<const h8*>(xl + at);
-          const float d = db[i];
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            v[t] = j + t < n ? v[t] * (1.0f / kOpScale) +
-                                   d * (static_cast<float>(hi[t]) + static_cast<float>(lo[t]) * (1.0f / kLowScale))
-                             : 0.0f;
-          if constexpr (WHAT == P_APPLY) {
-            h8 nh, nl;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-              _Float16 a, b;
-              split(v[t], a, b);
-              nh[t] = a;
-              nl[t] = b;
-            }
-            *reinterpret_cast<h8*>(xh + at) = nh;
-            *reinterpret_cast<h8*>(xl + at) = nl;
-          } else if (!tall) {
-            const int64_t o = q.start + static_cast<int64_t>(i) * n + j;
-            if constexpr (WHAT == P_OUT) {
-              uint16_t* dst = static_cast<uint16_t*>(out) + o;
-              uint32_t w[8];
-#pragma unroll
-              for (int t = 0; t < 8; ++t) w[t] = bf16_rne(v[t] / ex);
-              if (n % 8 == 0) {
-                *reinterpret_cast<u32x4*>(dst) = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
-                                                       w[6] | w[7] << 16};
-              } else {
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                  if (j + t < n) dst[t] = static_cast<uint16_t>(w[t]);
-              }
-            } else {
-              float* dst = static_cast<float*>(out) + o;
-              if (n % 4 == 0) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (j + 4 * h < n) {
-                    f32x4 p = *reinterpret_cast<f32x4*>(dst + 4 * h);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) p[t] = __fsub_rn(__fmul_rn(p[t], k.decay), __fmul_rn(step, v[4 * h + t]));
-                    *reinterpret_cast<f32x4*>(dst + 4 * h) = p;
-                  }
-              } else {
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                  if (j + t < n) dst[t] = __fsub_rn(__fmul_rn(dst[t], k.decay), __fmul_rn(step, v[t]));
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) v[t] = 0.0f;
-          if constexpr (WHAT == P_APPLY) {
-            if (i < m && j < np) {
-              const int64_t at = static_cast<int64_t>(i) * np + j;
-              *reinterpret_cast<h8*>(xh + at) = h8{};
-              *reinterpret_cast<h8*>(xl + at) = h8{};
-            }
+      for (int u = 0; u < kAhead; ++u) {
+        In8& x = in[group & 1][u];
+        const int i = min(row(group * kAhead + u), m - 1);   // rows past the end: any valid ones
+        const int64_t at = (static_cast<int64_t>(i) * jp + min(j, jp - 8)) * 2;
+        x.hi = *reinterpret_cast<const h8*>(in_hi + at);
+        x.lo = h8{};
+        if (read_lo) x.lo = *reinterpret_cast<const h8*>(in_lo + at);
+        x.d = diag[i];
+        if constexpr (WHAT == P_STEP) {
+          if (step_rows && whole_row) {
+            const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(out) + q.start + static_cast<int64_t>(i) * n + j);
+            x.p[0] = p[0];
+            x.p[1] = p[1];
           }
         }
       }
+    }
+  };
+  fetch(0);
+  float dj[8] = {};
+  if constexpr (WHAT == P_POLY) {
+    const f32x4* d = reinterpret_cast<const f32x4*>(diag + min(j, mp - 8));   // 256-byte padded: whole vectors
+#pragma unroll
+    for (int t = 0; t < 8; ++t) dj[t] = d[t / 4][t % 4];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int rr = wr * 64 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+        const int cc = wc * 64 + jj * 32 + lane % 32;
+        stage[rr * BM + (cc ^ (4 * (rr / 8 % 16)))] = acc[i][jj][r];
+      }
+  __syncthreads();
+  const bool mirror = kSym ? job.i != job.j : WHAT == P_APPLY || tall;
+#pragma unroll
+  for (int it = 0; it < kRows; ++it) {
+    if (it % kAhead == 0 && it + kAhead < kRows) fetch(it / kAhead + 1);
+    const In8& x = in[it / kAhead & 1][it % kAhead];
+    const int r = r0 + 16 * it, i = row(it), sw = 4 * (r / 8 % 16);
+    f32x4* s0 = reinterpret_cast<f32x4*>(stage + r * BM + (c ^ sw));
+    f32x4* s1 = reinterpret_cast<f32x4*>(stage + r * BM + ((c + 4) ^ sw));
+    float v[8];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) { v[t] = (*s0)[t]; v[4 + t] = (*s1)[t]; }
+    if constexpr (WHAT == P_GRAM) {
+      const float g = kOpScale / (ex * ex);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) v[t] *= g;
+      if (job.i == job.j) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (i == j + t) {
+            if (i < m) diag[i] = v[t] / kOpScale;
+            v[t] = 0.0f;
+          }
+      }
+    } else if constexpr (WHAT == P_POLY) {
+      float* db = reinterpret_cast<float*>(work + q.db);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float a = static_cast<float>(x.hi[t]) + static_cast<float>(x.lo[t]) * (1.0f / kLowScale);
+        const float a2 = v[t] * (1.0f / kOpScale);
+        float y = k.b * a + k.c * (a2 + (x.d + dj[t]) * a);
+        if (job.i == job.j && i == j + t) {
+          const float rest = k.b * x.d + k.c * (a2 * (1.0f / kOpScale) + x.d * x.d);
+          const bool all = x.d > 0.5f;
+          if (i < m) db[i] = all ? k.a + rest : k.a;
+          y = all ? 0.0f : rest * kOpScale;
+        }
+        v[t] = y;
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        v[t] = v[t] * (1.0f / kOpScale) +
+               x.d * (static_cast<float>(x.hi[t]) + static_cast<float>(x.lo[t]) * (1.0f / kLowScale));
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = i < m && j + t < jn ? v[t] : 0.0f;
+    if constexpr (!kLast) {
+      if (i < m && j < jp) {
+        h8 hi, lo;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          _Float16 a, b;
+          split(v[t], a, b);
+          hi[t] = a;
+          lo[t] = b;
+        }
+        const int64_t at = (static_cast<int64_t>(i) * jp + j) * 2;
+        *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.a : WHAT == P_POLY ? q.b : q.xh) + at) = hi;
+        if (WHAT == P_APPLY || two)
+          *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.al : WHAT == P_POLY ? q.bl : q.xl) + at) = lo;
+      }
+    } else if (!tall && i < m && j < n) {
+      finish(out, q.start + static_cast<int64_t>(i) * n + j, v, n - j, whole_row, f, k.decay, x.p);
+    }
+    if (mirror) {
       *s0 = f32x4{v[0], v[1], v[2], v[3]};
       *s1 = f32x4{v[4], v[5], v[6], v[7]};
     }
-    // column-wise: 8 rows per thread, 16 threads along a column of the pass
-    const bool mirror = kSym ? job.i != job.j : WHAT == P_APPLY || tall;
-    if (!mirror) return;
-    __syncthreads();
-    for (int e = tid; e < BM * 16; e += T::kNT) {
-      const int r = e % 16 * 8, c = e / 16;
-      const int i = i0 + (r / 64) * (T::NI * 32) + pass * 64 + r % 64, j = j0 + c;
-      const int sw = 4 * (r / 8 % 16);
-      float v[8];
-#pragma unroll
-      for (int t = 0; t < 8; ++t) v[t] = stage[(r + t) * BM + (c ^ sw)];
-      if (j >= jn) continue;
-      if constexpr (kSym || WHAT == P_APPLY) {
-        if (i < mp) {
-          h8 h;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) h[t] = static_cast<_Float16>(v[t]);
-          const int64_t at = static_cast<int64_t>(j) * mp + i;
-          *reinterpret_cast<h8*>((WHAT == P_GRAM ? pa : WHAT == P_POLY ? pb : xt) + at) = h;
-          if (two) *reinterpret_cast<h8*>((WHAT == P_GRAM ? pal : WHAT == P_POLY ? pbl : xtl) + at) = low_parts(v);
-        }
-      } else if (i < m) {
-        const int64_t o = q.start + static_cast<int64_t>(j) * m + i;
-        if constexpr (WHAT == P_OUT) {
-          uint16_t* dst = static_cast<uint16_t*>(out) + o;
-          uint32_t w[8];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) w[t] = bf16_rne(v[t] / ex);
-          if (m % 8 == 0) {
-            *reinterpret_cast<u32x4*>(dst) = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
-                                                   w[6] | w[7] << 16};
-          } else {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-              if (i + t < m) dst[t] = static_cast<uint16_t>(w[t]);
-          }
-        } else {
-          float* dst = static_cast<float*>(out) + o;
-          if (m % 4 == 0) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (i + 4 * h < m) {
-                f32x4 p = *reinterpret_cast<f32x4*>(dst + 4 * h);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) p[t] = __fsub_rn(__fmul_rn(p[t], k.decay), __fmul_rn(step, v[4 * h + t]));
-                *reinterpret_cast<f32x4*>(dst + 4 * h) = p;
-              }
-          } else {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-              if (i + t < m) dst[t] = __fsub_rn(__fmul_rn(dst[t], k.decay), __fmul_rn(step, v[t]));
-          }
-        }
+  }
+  if (!mirror) return;
+  // column-wise: eight rows per thread, 16 threads along a column of the pass
+  const int cr = tid % 16 * 8, csw = 4 * (cr / 8 % 16);
+  const int i = i0 + (cr / 64) * (T::NI * 32) + pass * 64 + cr % 64;
+  const bool whole_col = i + 8 <= m && m % 8 == 0;
+  f32x4 p[2][2] = {};
+  auto fetch_col = [&](int it) {
+    if constexpr (WHAT == P_STEP) {
+      const int jc = j0 + tid / 16 + it * (T::kNT / 16);
+      if (whole_col && jc < n) {
+        const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const float*>(out) + q.start + static_cast<int64_t>(jc) * m + i);
+        p[it & 1][0] = s[0];
+        p[it & 1][1] = s[1];
       }
     }
+  };
+  fetch_col(0);
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    if (it < 7) fetch_col(it + 1);
+    const int cc = tid / 16 + it * (T::kNT / 16), jc = j0 + cc;
+    float v[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = stage[(cr + t) * BM + (cc ^ csw)];
+    if (jc >= jn) continue;
+    if constexpr (!kLast) {
+      if (i < mp) {
+        h8 hi, lo;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          _Float16 a, b;
+          split(v[t], a, b);
+          hi[t] = a;
+          lo[t] = b;
+        }
+        const int64_t at = (static_cast<int64_t>(jc) * mp + i) * 2;
+        *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.a : WHAT == P_POLY ? q.b : q.xt[turn ^ 1]) + at) = hi;
+        if (two)
+          *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.al : WHAT == P_POLY ? q.bl : q.xtl[turn ^ 1]) + at) = lo;
+      }
+    } else if (i < m) {
+      finish(out, q.start + static_cast<int64_t>(jc) * m + i, v, m - i, whole_col, f, k.decay, p[it & 1]);
+    }
+  }
 }
 };
 
