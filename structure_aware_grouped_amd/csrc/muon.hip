@@ -221,36 +221,39 @@ enum Product {
   P_STEP     // the same, last step: the parameters' update
 };
 
-// C = P Q^T on one BM x BM output tile, BM * 2 threads: a 2 x BM/64 grid of
-// waves, each 64 * (BM / 128) rows x 64 columns in 32 x 32 accumulators.
-// Operands go straight from memory to LDS, kMatK wide, in two stages: while
-// one stage is multiplied the next is on its way. In LDS a row is 128 bytes,
-// eight 16-byte pieces, piece c of row r at place c ^ (r / 2 % 8): two rows
-// fill the 64 banks once, and any 16 neighbouring rows of a fragment spread
-// over all of them; the loads permute the pieces within each row's 128-byte
-// line in memory. The fragment of the next 16
-// columns is read while the current one is multiplied; the stage turns over
-// (wait, barrier, new loads) before the last multiplication of a stage.
+// C = P Q^T on one BM x BM output tile by a 2 x WC grid of waves, each with
+// NI x NJ accumulators of 32 x 32. Operands go straight from memory to LDS,
+// kMatK wide, in kStages stages: while one is multiplied the others are on
+// their way. In LDS a row is 128 bytes, eight 16-byte pieces, piece c of row
+// r at place c ^ (r / 2 % 8): two rows fill the 64 banks once, and any 16
+// neighbouring rows of a fragment spread over all of them; the loads permute
+// the pieces within each row's 128-byte line in memory. The fragment of the
+// next 16 columns is read while the current one is multiplied; the stage turns
+// over (wait, barrier, new loads) before the last multiplication of a stage.
+//   256: 64 KiB a stage, one workgroup per CU; what large products take. 128
+// and 64: two and two workgroups per CU, for products of few tiles; 64 keeps
+// three stages on their way, since few workgroups wait for memory.
 template <int BM>
 struct Tile {
-  static constexpr int kNT = BM * 2;
+  static constexpr int kNT = BM == 256 ? 512 : 256;
   static constexpr int kWaves = kNT / kWave;
-  static constexpr int WC = BM / 64;             // wave columns
-  static constexpr int NI = BM / 64;             // 32-row blocks per wave (2 wave rows)
-  static constexpr int NJ = 2;                   // 32-column blocks per wave
+  static constexpr int WC = kWaves / 2;          // wave columns
+  static constexpr int NI = BM / 64;             // 32-row blocks per wave
+  static constexpr int NJ = BM / (32 * WC);      // 32-column blocks per wave
+  static constexpr int kStages = BM == 64 ? 4 : 2;
   static constexpr int kStage = 2 * BM * kMatK * 2;   // bytes of both operands
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLds = kStages * kStage;
   static constexpr int kLoads = kStage / 1024 / kWaves;   // 1 KiB loads per wave and stage
-  static constexpr int kPasses = NI / 2;         // the epilogue stages 2 blocks of rows per wave at a time
-  static_assert(NI % 2 == 0 && 128 * BM * 4 <= kLds, "an epilogue pass fits the operand stages");
+  static constexpr int IB = NI < 2 ? NI : 2;     // 32-row blocks of a wave that are stored in one pass
+  static constexpr int kPasses = NI / IB;
 };
 
 // Waits for all but VM of the wave's loads (and LDS reads, with LGKM). The
 // builtin, unlike assembly text, tells the compiler what has arrived.
 template <int VM, bool LGKM>
 __device__ __forceinline__ void wait() {
-  static_assert(VM < 16, "the low four bits of the counter");
-  __builtin_amdgcn_s_waitcnt(VM | 0x70 | (LGKM ? 0 : 0xf00));
+  static_assert(VM < 64, "a six-bit counter");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (VM >> 4) << 14 | 0x70 | (LGKM ? 0 : 0xf00));
 }
 
 // Workgroup barrier without a wait of its own; no memory access moves across.
@@ -272,7 +275,7 @@ __device__ __forceinline__ int fresh_thread() {
 
 template <int BM>
 struct Acc {
-  f32x16 v[Tile<BM>::NI][2];
+  f32x16 v[Tile<BM>::NI][Tile<BM>::NJ];
 };
 
 template <int BM>
@@ -302,14 +305,14 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
     const int row = min(seg * 8 + lane / 8, (t < kHalf ? pr : qr) - 1);
     off[t] = static_cast<int>(row * row_bytes) + ((lane % 8) ^ ((seg * 8 + lane / 8) / 2 % 8)) * 16;
   }
-  // LDS: P's two stages, then Q's two stages, so that a stage and a block are
-  // immediate offsets of a fragment read
+  // LDS: P's stages, then Q's, so that a stage and a block are immediate
+  // offsets of a fragment read
   constexpr int kHalfStage = T::kStage / 2;
-  auto load = [&](int s) {
+  auto load = [&](int s, int stage) {
     const int k = (k0 + s) * static_cast<int>(kMatK) * 2;
 #pragma unroll
     for (int t = 0; t < T::kLoads; ++t) {
-      lds_char* dst = (lds_char*)lds + (t < kHalf ? 0 : T::kStage) + (s & 1) * kHalfStage + wave * 1024 +
+      lds_char* dst = (lds_char*)lds + (t < kHalf ? 0 : T::kStages * kHalfStage) + stage * kHalfStage + wave * 1024 +
                       (t % kHalf) * T::kWaves * 1024;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(t < kHalf ? rp : rq, dst, 16, off[t], k, 0, 0);
     }
@@ -321,12 +324,12 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
   for (int kk = 0; kk < 4; ++kk) {
     const int at = frow * 128 + (((kk * 2 + lane / 32) ^ (frow / 2 % 8)) * 16);
     fp[kk] = lds + at + wr * T::NI * 32 * 128;
-    fq[kk] = lds + at + T::kStage + wc * 64 * 128;
+    fq[kk] = lds + at + T::kStages * kHalfStage + wc * T::NJ * 32 * 128;
   }
-  h8 fa[2][T::NI], fb[2][2];
+  h8 fa[2][T::NI], fb[2][T::NJ];
   auto fetch = [&](int stage, int kk, int to) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) fb[to][j] = *reinterpret_cast<const h8*>(fq[kk] + stage * kHalfStage + j * 4096);
+    for (int j = 0; j < T::NJ; ++j) fb[to][j] = *reinterpret_cast<const h8*>(fq[kk] + stage * kHalfStage + j * 4096);
 #pragma unroll
     for (int i = 0; i < T::NI; ++i) fa[to][i] = *reinterpret_cast<const h8*>(fp[kk] + stage * kHalfStage + i * 4096);
   };
@@ -334,52 +337,54 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
 #pragma unroll
     for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < T::NJ; ++j)
         c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[from][i], fb[from][j], c.v[i][j], 0, 0, 0);
   };
   // one fragment read between multiplications, so that none of them waits
+  constexpr int kReads = T::NI + T::NJ, kMuls = T::NI * T::NJ, kPairs = kReads < kMuls ? kReads : kMuls;
   auto interleave = [&]() {
+    if constexpr (kReads > kPairs) __builtin_amdgcn_sched_group_barrier(0x100, kReads - kPairs, 0);   // LDS reads
 #pragma unroll
-    for (int i = 0; i < T::NI + 2; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+    for (int i = 0; i < kPairs; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one multiplication
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, T::NI * 2 - (T::NI + 2), 0);
+    if constexpr (kMuls > kPairs) __builtin_amdgcn_sched_group_barrier(0x008, kMuls - kPairs, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
   // One stage: three sixteen-column multiplications, each while the next
   // fragment is read; then, with every wave done reading this stage and the
-  // next stage arrived, the loads of the stage after that and the next
-  // stage's first fragment, under the fourth.
-  auto step = [&](int s, int stage, bool more_loads, bool more) {
+  // next stage arrived (full: later ones may still be on their way), the loads
+  // into this stage and the next stage's first fragment, under the fourth.
+  constexpr int S = T::kStages;
+  auto step = [&](int s, int stage, int next, bool full, bool more_loads, bool more) {
 #pragma unroll
     for (int kk = 0; kk < 3; ++kk) {
       fetch(stage, kk + 1, (kk + 1) & 1);
       mma(kk & 1);
       interleave();
     }
-    wait<0, true>();
+    if (full) wait<(S - 2) * T::kLoads, true>();
+    else wait<0, true>();
     barrier();
-    if (more_loads) load(s + 2);
-    if (more) fetch(stage ^ 1, 0, 0);
+    if (more_loads) load(s + S, stage);
+    if (more) fetch(next, 0, 0);
     mma(1);
     __builtin_amdgcn_sched_barrier(0);
   };
-  load(0);
-  if (ksteps > 1) {
-    load(1);
-    wait<T::kLoads, false>();
-  } else {
-    wait<0, false>();
-  }
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < ksteps) load(s, s);
+  if (ksteps >= S) wait<(S - 1) * T::kLoads, false>();
+  else wait<0, false>();
   barrier();
   fetch(0, 0, 0);
   int s = 0;
-  for (; s + 3 < ksteps; s += 2) {
-    step(s, 0, true, true);
-    step(s + 1, 1, true, true);
+  for (; s + 2 * S - 1 < ksteps; s += S) {
+#pragma unroll
+    for (int u = 0; u < S; ++u) step(s + u, u, (u + 1) % S, true, true, true);
   }
-  for (; s < ksteps; ++s) step(s, s & 1, s + 2 < ksteps, s + 1 < ksteps);
+  for (; s < ksteps; ++s) step(s, s % S, (s + 1) % S, s + S <= ksteps, s + S < ksteps, s + 1 < ksteps);
 }
 };
 
@@ -390,73 +395,81 @@ __device__ __forceinline__ float update_scale(int mode, int rows, int cols) {
   return 1.0f;
 }
 
-// The sums of one part of a cut tile, stored or added up in the order of the
-// parts. Slab element order is that of the registers: 16 bytes per thread.
-template <int BM>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t slab_of(char* slabs, int slab) {
-  constexpr int kSlab = BM * BM * 4;
-  return __builtin_amdgcn_make_buffer_rsrc(slabs + static_cast<int64_t>(slab) * kSlab, 0, kSlab, kRawBufferWord3);
-}
-
+// The sums of one part of a cut tile. Slab element order is that of the
+// registers: 16 bytes per thread.
 template <int BM>
 struct Slab {
 using T = Tile<BM>;
+static constexpr int kBytes = BM * BM * 4;
+
+__device__ static __forceinline__ __amdgpu_buffer_rsrc_t at(char* slabs, int slab) {
+  return __builtin_amdgcn_make_buffer_rsrc(slabs + static_cast<int64_t>(slab) * kBytes, 0, kBytes, kRawBufferWord3);
+}
+
 __device__ static __forceinline__ void store(const Acc<BM>& acc, char* slabs, int slab) {
   const int mine = fresh_thread() * 16;
-  const __amdgpu_buffer_rsrc_t r = slab_of<BM>(slabs, slab);
+  const __amdgpu_buffer_rsrc_t r = at(slabs, slab);
 #pragma unroll
   for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < T::NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const f32x4 x = {acc.v[i][j][4 * e], acc.v[i][j][4 * e + 1], acc.v[i][j][4 * e + 2], acc.v[i][j][4 * e + 3]};
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, mine, ((i * 2 + j) * 4 + e) * T::kNT * 16, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, mine, ((i * T::NJ + j) * 4 + e) * T::kNT * 16, 0);
       }
 }
 
-// Rows of 32-row blocks 2 * pass and 2 * pass + 1 of every wave.
-__device__ static __forceinline__ void load(f32x16 (&v)[2][2], char* slabs, int slab, int parts, int pass) {
-  const int mine = fresh_thread() * 16;
+// The sums over all parts of block row `strip` (32 rows of the tile), in the
+// order of the parts, by WC waves.
+__device__ static __forceinline__ void add(f32x16 (&v)[1][T::NJ], char* slabs, int slab, int parts, int strip) {
+  const int mine = (strip / T::NI * T::WC * kWave + fresh_thread()) * 16;
+  const int base = strip % T::NI * T::NJ * 4 * T::kNT * 16;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) v[i][j] = f32x16{};
+  for (int j = 0; j < T::NJ; ++j) v[0][j] = f32x16{};
+#pragma unroll 2
   for (int p = 0; p < parts; ++p) {
-    const __amdgpu_buffer_rsrc_t r = slab_of<BM>(slabs, slab + p);
-    f32x4 x[2][2][4];
+    const __amdgpu_buffer_rsrc_t r = at(slabs, slab + p);
+    f32x4 x[T::NJ][4];
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
-      x[q / 8][q / 4 % 2][q % 4] = __builtin_bit_cast(
-          f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, mine, (pass * 16 + q) * T::kNT * 16, 0));
+    for (int j = 0; j < T::NJ; ++j)
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
+      for (int e = 0; e < 4; ++e)
+        x[j][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, mine, base + (j * 4 + e) * T::kNT * 16, 0));
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[q / 8][q / 4 % 2][4 * (q % 4) + t] += x[q / 8][q / 4 % 2][q % 4][t];
+    for (int j = 0; j < T::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[0][j][4 * e + t] += x[j][e][t];
   }
 }
 };
 
-// What is stored of one tile, 128 rows (a pass) at a time. The accumulators of
-// the pass (two 32-row blocks of each wave) go through LDS: a row-wise phase
+// What is stored of some rows of one tile: in a product, of IB 32-row blocks of
+// each of the NW = 2 wave rows (a pass); in a join, of one block (NW = IB = 1).
+// The sums go through LDS: a row-wise phase
 // computes the result and stores it along its rows, a column-wise phase stores
-// its transpose. In LDS element (i, j) of a pass lies at
-// i * BM + (j ^ 4 * (i / 8 % 16)): 16-byte pieces along a row stay whole, and
-// the eight rows that a lane of the column-wise phase reads fall into banks of
-// their own. The pass's row r is the tile's row
-// (r / 64) * NI * 32 + pass * 64 + r % 64.
-//   In the row-wise phase a thread has eight columns of eight rows. What it
+// its transpose. In LDS element (r, j) lies at r * BM + (j ^ 4 * (r / 8 % 16)):
+// 16-byte pieces along a row stay whole, and the eight rows that a lane of the
+// column-wise phase reads fall into banks of their own. Row r of these is the
+// tile's row r / (32 IB) * 32 NI + base + r % (32 IB).
+//   In the row-wise phase a thread has eight columns of kRows rows. What it
 // reads of them from memory is fetched kAhead rows at a time, the first ones
-// before the accumulators go to LDS: one row at a time the loads of a row
-// waited for the stores of the one before (20 us for one 128-wide tile).
-template <int BM, Product WHAT>
+// before the sums go to LDS: one row at a time the loads of a row waited for
+// the stores of the one before (20 us for one 128-wide tile).
+template <int BM, Product WHAT, int NW, int IB>
 struct Store {
 using T = Tile<BM>;
+static constexpr int kNT = NW * T::WC * kWave;
+static constexpr int kHeight = NW * IB * 32;
+static constexpr int kBytes = kHeight * BM * 4;   // of LDS
 static constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY;
 static constexpr bool kLast = WHAT == P_OUT || WHAT == P_STEP;
-static constexpr int kRows = 8;
-static constexpr int kAhead = WHAT == P_STEP ? 2 : 4;
-static_assert(128 * (BM / 8) == kRows * T::kNT, "eight rows of eight columns per thread");
+static constexpr int kRows = kHeight * (BM / 8) / kNT, kRowStep = kNT / (BM / 8);
+static constexpr int kAhead = WHAT == P_STEP || kRows < 4 ? 2 : 4;
+static constexpr int kCols = BM * (kHeight / 8) / kNT, kColStep = kNT / (kHeight / 8);
+static_assert(kRows % kAhead == 0 && kRows * kRowStep == kHeight && kCols * kColStep == BM, "whole rows and columns");
 
 struct In8 {   // of one row: A (POLY) or X, high and low; parameters (STEP)
   h8 hi, lo;
@@ -498,8 +511,9 @@ __device__ static __forceinline__ void finish(void* out, int64_t at, const float
   }
 }
 
-__device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const ProductJob& job, const MuonMat& q, int pass,
-                                           char* work, char* lds, int turn, const MuonK& k, void* out) {
+// acc: the sums of each wave's IB block rows; base: the tile's row of row 0.
+__device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const ProductJob& job, const MuonMat& q,
+                                           int base, char* work, char* lds, int turn, const MuonK& k, void* out) {
   const int i0 = job.i * BM, j0 = job.j * BM;
   const int m = q.m, n = q.n, mp = q.mp, np = q.np;
   const bool two = q.two_part, tall = q.tall;
@@ -514,7 +528,8 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const Prod
 
   // row-wise: rows i0 + row(it), columns j .. j + 7
   const int r0 = tid / (BM / 8), c = tid % (BM / 8) * 8, j = j0 + c;
-  auto row = [&](int it) { return i0 + (it / 4) * (T::NI * 32) + pass * 64 + r0 + 16 * (it % 4); };
+  auto tile_row = [&](int r) { return i0 + r / (IB * 32) * (T::NI * 32) + base + r % (IB * 32); };
+  auto row = [&](int it) { return tile_row(r0 + it * kRowStep); };
   const char* in_hi = work + (WHAT == P_POLY ? q.a : q.xh);
   const char* in_lo = work + (WHAT == P_POLY ? q.al : q.xl);
   const bool read_lo = WHAT != P_POLY || two;
@@ -549,13 +564,13 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const Prod
     for (int t = 0; t < 8; ++t) dj[t] = d[t / 4][t % 4];
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < IB; ++i)
 #pragma unroll
-    for (int jj = 0; jj < 2; ++jj)
+    for (int jj = 0; jj < T::NJ; ++jj)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int rr = wr * 64 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-        const int cc = wc * 64 + jj * 32 + lane % 32;
+        const int rr = wr * IB * 32 + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+        const int cc = wc * T::NJ * 32 + jj * 32 + lane % 32;
         stage[rr * BM + (cc ^ (4 * (rr / 8 % 16)))] = acc[i][jj][r];
       }
   __syncthreads();
@@ -564,7 +579,7 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const Prod
   for (int it = 0; it < kRows; ++it) {
     if (it % kAhead == 0 && it + kAhead < kRows) fetch(it / kAhead + 1);
     const In8& x = in[it / kAhead & 1][it % kAhead];
-    const int r = r0 + 16 * it, i = row(it), sw = 4 * (r / 8 % 16);
+    const int r = r0 + kRowStep * it, i = row(it), sw = 4 * (r / 8 % 16);
     f32x4* s0 = reinterpret_cast<f32x4*>(stage + r * BM + (c ^ sw));
     f32x4* s1 = reinterpret_cast<f32x4*>(stage + r * BM + ((c + 4) ^ sw));
     float v[8];
@@ -629,14 +644,14 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const Prod
     }
   }
   if (!mirror) return;
-  // column-wise: eight rows per thread, 16 threads along a column of the pass
-  const int cr = tid % 16 * 8, csw = 4 * (cr / 8 % 16);
-  const int i = i0 + (cr / 64) * (T::NI * 32) + pass * 64 + cr % 64;
+  // column-wise: eight rows per thread, kHeight / 8 threads along a column
+  const int cr = tid % (kHeight / 8) * 8, csw = 4 * (cr / 8 % 16), c0 = tid / (kHeight / 8);
+  const int i = tile_row(cr);
   const bool whole_col = i + 8 <= m && m % 8 == 0;
   f32x4 p[2][2] = {};
   auto fetch_col = [&](int it) {
     if constexpr (WHAT == P_STEP) {
-      const int jc = j0 + tid / 16 + it * (T::kNT / 16);
+      const int jc = j0 + c0 + it * kColStep;
       if (whole_col && jc < n) {
         const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const float*>(out) + q.start + static_cast<int64_t>(jc) * m + i);
         p[it & 1][0] = s[0];
@@ -647,9 +662,9 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const Prod
   fetch_col(0);
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    if (it < 7) fetch_col(it + 1);
-    const int cc = tid / 16 + it * (T::kNT / 16), jc = j0 + cc;
+  for (int it = 0; it < kCols; ++it) {
+    if (it + 1 < kCols) fetch_col(it + 1);
+    const int cc = c0 + it * kColStep, jc = j0 + cc;
     float v[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) v[t] = stage[(cr + t) * BM + (cc ^ csw)];
@@ -678,10 +693,12 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[2][2], const Prod
 
 // One job of one product.
 template <int BM, Product WHAT>
-__global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __restrict__ mats,
+__global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMat* __restrict__ mats,
                                                              const ProductJob* __restrict__ jobs, char* work,
                                                              int64_t slabs, int turn, MuonK k, void* out) {
   using T = Tile<BM>;
+  using St = Store<BM, WHAT, 2, T::IB>;
+  static_assert(St::kBytes <= T::kLds, "a pass fits the operand stages");
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   const ProductJob job = jobs[blockIdx.x];
   const MuonMat& q = mats[job.mat];
@@ -697,7 +714,7 @@ __global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __re
 #pragma unroll
       for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc.v[i][j] *= 1.0f / kLowScale;
+        for (int j = 0; j < T::NJ; ++j) acc.v[i][j] *= 1.0f / kLowScale;
     }
     Multiply<BM>::run(reinterpret_cast<const _Float16*>(part == 1 ? p_lo : p_hi),
                       reinterpret_cast<const _Float16*>(part == 0 ? q_lo : q_hi), ld, job.i * BM, q.m, job.j * BM,
@@ -707,37 +724,41 @@ __global__ __launch_bounds__(BM * 2) void mat_product_kernel(const MuonMat* __re
     Slab<BM>::store(acc, work + slabs, job.slab);
     return;
   }
-  f32x16 (&v)[T::NI][2] = acc.v;
-  Store<BM, WHAT>::run(reinterpret_cast<const f32x16 (&)[2][2]>(v[0]), job, q, 0, work, lds, turn, k, out);
-  if constexpr (T::kPasses == 2) {
-    __syncthreads();
-    Store<BM, WHAT>::run(reinterpret_cast<const f32x16 (&)[2][2]>(v[2]), job, q, 1, work, lds, turn, k, out);
+#pragma unroll
+  for (int pass = 0; pass < T::kPasses; ++pass) {
+    if (pass) __syncthreads();
+    St::run(reinterpret_cast<const f32x16 (&)[T::IB][T::NJ]>(acc.v[pass * T::IB]), job, q, pass * T::IB * 32, work, lds,
+            turn, k, out);
   }
 }
 
-// One pass of one cut tile: its parts' sums added up, then stored as above.
+// 32 rows of one cut tile: its parts' sums added up, then stored as above.
 template <int BM, Product WHAT>
-__global__ __launch_bounds__(BM * 2) void mat_join_kernel(const MuonMat* __restrict__ mats,
-                                                          const ProductJob* __restrict__ joins, char* work,
-                                                          int64_t slabs, int turn, MuonK k, void* out) {
+__global__ __launch_bounds__(Tile<BM>::WC * kWave) void mat_join_kernel(const MuonMat* __restrict__ mats,
+                                                                        const ProductJob* __restrict__ joins,
+                                                                        char* work, int64_t slabs, int turn, MuonK k,
+                                                                        void* out) {
   using T = Tile<BM>;
-  __shared__ __attribute__((aligned(16))) char lds[128 * BM * 4];
-  const ProductJob job = joins[blockIdx.x / T::kPasses];
-  const int pass = blockIdx.x % T::kPasses;
-  f32x16 v[2][2];
-  Slab<BM>::load(v, work + slabs, job.slab, job.parts, pass);
-  Store<BM, WHAT>::run(v, job, mats[job.mat], pass, work, lds, turn, k, out);
+  using St = Store<BM, WHAT, 1, 1>;
+  __shared__ __attribute__((aligned(16))) char lds[St::kBytes];
+  const ProductJob job = joins[blockIdx.x / (BM / 32)];
+  const int strip = blockIdx.x % (BM / 32);
+  const MuonMat& q = mats[job.mat];
+  if (job.i * BM + strip * 32 >= q.mp) return;   // nothing of the matrix or its padding
+  f32x16 v[1][T::NJ];
+  Slab<BM>::add(v, work + slabs, job.slab, job.parts, strip);
+  St::run(v, job, q, strip * 32, work, lds, turn, k, out);
 }
 
 // ------------------------------------------------------------------ launches
 
 template <int BM, Product WHAT>
 void launch_tiles(const rs_plan* p, int list, char* work, int turn, const MuonK& k, void* out, hipStream_t s) {
-  hipLaunchKernelGGL((mat_product_kernel<BM, WHAT>), dim3(static_cast<unsigned>(p->n_mat_jobs[list])), dim3(BM * 2), 0,
-                     s, p->mats, p->mat_jobs[list], work, p->mat_slabs, turn, k, out);
+  hipLaunchKernelGGL((mat_product_kernel<BM, WHAT>), dim3(static_cast<unsigned>(p->n_mat_jobs[list])),
+                     dim3(Tile<BM>::kNT), 0, s, p->mats, p->mat_jobs[list], work, p->mat_slabs, turn, k, out);
   if (p->n_mat_joins[list])
     hipLaunchKernelGGL((mat_join_kernel<BM, WHAT>),
-                       dim3(static_cast<unsigned>(p->n_mat_joins[list] * Tile<BM>::kPasses)), dim3(BM * 2), 0, s,
+                       dim3(static_cast<unsigned>(p->n_mat_joins[list] * (BM / 32))), dim3(Tile<BM>::WC * kWave), 0, s,
                        p->mats, p->mat_joins[list], work, p->mat_slabs, turn, k, out);
 }
 
@@ -745,7 +766,8 @@ template <Product WHAT>
 void launch_product(const rs_plan* p, char* work, int turn, const MuonK& k, void* out, hipStream_t s) {
   constexpr int kList = WHAT == P_GRAM ? 0 : WHAT == P_POLY ? 1 : 2;
   if (p->mat_side[kList] == 256) launch_tiles<256, WHAT>(p, kList, work, turn, k, out, s);
-  else launch_tiles<128, WHAT>(p, kList, work, turn, k, out, s);
+  else if (p->mat_side[kList] == 128) launch_tiles<128, WHAT>(p, kList, work, turn, k, out, s);
+  else launch_tiles<64, WHAT>(p, kList, work, turn, k, out, s);
 }
 
 // Momentum (MUON), norm and Newton-Schulz on every matrix of the plan; the

@@ -595,11 +595,11 @@ void lower_product(const std::vector<MuonMat>& mats, bool sym, bool over_n, Prod
     }
     return c;
   };
-  out->side = count(256) >= kMatMinTiles ? 256 : 128;
-  // RS_MUON_TILE=128|256 forces one size
+  out->side = count(256) >= kMatMinTiles ? 256 : count(128) >= kMatMinTiles ? 128 : 64;
+  // RS_MUON_TILE=64|128|256 forces one size
   if (const char* e = std::getenv("RS_MUON_TILE")) {
     const int side = std::atoi(e);
-    if (side == 128 || side == 256) out->side = side;
+    if (side == 64 || side == 128 || side == 256) out->side = side;
   }
   // tiles in blocks of kBlock x kBlock: what runs together shares operand rows
   constexpr int64_t kBlock = 6;
@@ -615,7 +615,7 @@ void lower_product(const std::vector<MuonMat>& mats, bool sym, bool over_n, Prod
             if (!sym || j <= i)
               tiles.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j), steps, q.two_part ? 3 : 1});
   }
-  schedule(tiles, out->side == 256 ? kMatGroups : 2 * kMatGroups, out);
+  schedule(tiles, mat_places(out->side), out);
 }
 
 }  // namespace

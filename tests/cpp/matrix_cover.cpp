@@ -3,7 +3,7 @@
 // is run exactly once, the parts of a cut tile have slabs of their own in
 // order and are joined once, chunks and spread tiles cover each matrix once,
 // operands do not overlap in the workspace, and the launch's jobs, taken in
-// order by 256 (512 for 128-wide tiles) places, end together.
+// order by the places that run at once, end together.
 //
 // Reads "n" and n lines "rows cols" (WHOLE tensors) on stdin; prints "ok" and
 // per product the tile side, tiles, cut tiles, jobs and the end over the mean
@@ -88,7 +88,7 @@ int main(int argc, char** argv) {
   for (int w = 0; w < 3; ++w) {
     const ProductList& l = mt.list[w];
     std::map<std::tuple<int, int, int>, std::vector<ProductJob>> tiles;
-    std::vector<double> share(l.side == 256 ? kMatGroups : 2 * kMatGroups, 0.0);
+    std::vector<double> share(mat_places(l.side), 0.0);
     double total = 0;
     for (const ProductJob& p : l.jobs) {
       tiles[{p.mat, p.i, p.j}].push_back(p);

@@ -63,7 +63,7 @@ def _rel(x, y):
     return np.linalg.norm(x - y) / max(np.linalg.norm(y), 1e-300)
 
 
-@pytest.fixture(params=["128", "256"])
+@pytest.fixture(params=["64", "128", "256"])
 def tile(request, monkeypatch):
     monkeypatch.setenv("RS_MUON_TILE", request.param)
     return request.param

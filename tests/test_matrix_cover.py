@@ -41,7 +41,7 @@ def _run(exe, shapes, plant=0, tile=None):
     return r.stdout.strip()
 
 
-@pytest.mark.parametrize("tile", [None, 128, 256])
+@pytest.mark.parametrize("tile", [None, 64, 128, 256])
 @pytest.mark.parametrize("shapes", [[(64, 48)], [(2, 2)], [(2, 100000)], [(1024, 4096)], [(128, 2880), (333, 1001)],
                                     [(4096, 4096)], [(8192, 28672)], LAYER, [(5760, 2880), (2880, 2880)] * 8,
                                     [(16, 16)] * 700])
@@ -55,7 +55,7 @@ def test_random_groups(exe, seed):
     rng = random.Random(seed)
     shapes = [(rng.choice([2, 17, 64, 65, 300, 1000, 2049, 5000]), rng.choice([2, 33, 64, 129, 777, 2880, 6000]))
               for _ in range(rng.randint(1, 12))]
-    out = _run(exe, shapes, tile=rng.choice([None, 128, 256]))
+    out = _run(exe, shapes, tile=rng.choice([None, 64, 128, 256]))
     assert out.startswith("ok"), out
 
 
