@@ -173,7 +173,7 @@ int rs_plan_build(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t ali
  * RS_TM_KERNEL=direct runs the tile-major reorder of unpack / pack with
  * direct per-lane kernels instead of staging it through LDS. Both give
  * identical results. RS_MUON_TILE=64|128|256 forces the output tile of the
- * matrix products (rs_orthogonalize, rs_muon_step).
+ * matrix products (rs_orthogonalize, rs_muon_step), small matrices included.
  * On success *out owns host memory and one device allocation, released by
  * rs_plan_free. Errors: the above, RS_ENOMEM, RS_EHIP. */
 int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,

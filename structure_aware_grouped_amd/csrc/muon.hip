@@ -160,21 +160,60 @@ __global__ __launch_bounds__(kThreads) void mat_spread_kernel(const MuonMat* __r
   const MuonMat& q = mats[job.mat];
   const double inv = *reinterpret_cast<const double*>(work + q.inv);
   const int i0 = job.i * T, j0 = job.j * T;
-  for (int e = threadIdx.x; e < T * T; e += kThreads) {
-    const int r = e / T, c = e % T;                       // in the matrix's own orientation
-    const int i = q.tall ? c : r, j = q.tall ? r : c;     // in X's
-    float x = 0.0f;
-    if (i0 + i < q.m && j0 + j < q.n) {
-      const int64_t at = q.start + (q.tall ? static_cast<int64_t>(j0 + j) * q.m + i0 + i
-                                           : static_cast<int64_t>(i0 + i) * q.n + j0 + j);
-      float g = load_elem(grad, at, BF16);
-      if constexpr (MUON) {
-        const float m = mom[at];
-        g = k.nesterov ? __fadd_rn(g, __fmul_rn(k.mu, m)) : m;
+  // the matrix's own rows r0.. and columns c0.. ; element (r, c) is X's (r, c) or (c, r)
+  const int r0 = q.tall ? j0 : i0, c0 = q.tall ? i0 : j0;
+  auto put = [&](int r, int c, float g, float m) {
+    if constexpr (MUON) g = k.nesterov ? __fadd_rn(g, __fmul_rn(k.mu, m)) : m;
+    const float x = static_cast<float>(static_cast<double>(g) * inv);
+    if (q.tall) tile[c][r] = x;
+    else tile[r][c] = x;
+  };
+  if (q.cols % 4 == 0) {   // four neighbours per load, all of a thread's loads first
+    constexpr int kIt = T * T / 4 / kThreads;
+    const int c = threadIdx.x % (T / 4) * 4;
+    f32x4 g[kIt], m[kIt];
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const int r = threadIdx.x / (T / 4) + it * (kThreads / (T / 4));
+      g[it] = m[it] = f32x4{};
+      if (r0 + r < q.rows && c0 + c < q.cols) {
+        const int64_t at = q.start + static_cast<int64_t>(r0 + r) * q.cols + c0 + c;
+        if constexpr (BF16) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(grad) + at);
+          g[it] = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                        __uint_as_float(w.y & 0xffff0000u)};
+        } else {
+          g[it] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(grad) + at);
+        }
+        if constexpr (MUON) m[it] = *reinterpret_cast<const f32x4*>(mom + at);
       }
-      x = static_cast<float>(static_cast<double>(g) * inv);
     }
-    tile[i][j] = x;
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const int r = threadIdx.x / (T / 4) + it * (kThreads / (T / 4));
+      const bool in = r0 + r < q.rows && c0 + c < q.cols;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (in) put(r, c + t, g[it][t], m[it][t]);
+        else if (q.tall) tile[c + t][r] = 0.0f;
+        else tile[r][c + t] = 0.0f;
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int e = threadIdx.x; e < T * T; e += kThreads) {
+      const int r = e / T, c = e % T;
+      if (r0 + r < q.rows && c0 + c < q.cols) {
+        const int64_t at = q.start + static_cast<int64_t>(r0 + r) * q.cols + c0 + c;
+        float m = 0.0f;
+        if constexpr (MUON) m = mom[at];
+        put(r, c, load_elem(grad, at, BF16), m);
+      } else if (q.tall) {
+        tile[c][r] = 0.0f;
+      } else {
+        tile[r][c] = 0.0f;
+      }
+    }
   }
   __syncthreads();
   _Float16* xh = reinterpret_cast<_Float16*>(work + q.xh);
@@ -750,6 +789,180 @@ __global__ __launch_bounds__(Tile<BM>::WC * kWave) void mat_join_kernel(const Mu
   St::run(v, job, q, strip * 32, work, lds, turn, k, out);
 }
 
+// ------------------------------------------------------------------ small matrices
+
+// Matrices of at most 64 x 256 (X's sides), one workgroup each, whole call in
+// one launch: what a step of three launches waits for is latency, and X fits
+// LDS. Every wave holds its part of X in fp32 registers, as the 16 x 16 blocks
+// that v_mfma_f32_16x16x32_f16 gives; LDS holds the operands, high and low
+// parts of X, X^T and of A or the polynomial. Products are high * low +
+// low * high + high * high, and the polynomial's whole diagonal stays in fp32.
+// Rows in LDS are 16 bytes longer than their contents, so that the rows of a
+// fragment start in different banks.
+constexpr int kTinyThreads = 512, kTinyWaves = kTinyThreads / kWave;
+constexpr int kTinyM = static_cast<int>(kMatTinyM), kTinyN = static_cast<int>(kMatTinyN);
+constexpr int kTinyBlocks = (kTinyM / 16) * (kTinyN / 16) / kTinyWaves;   // of X, per wave
+typedef float f32v4 __attribute__((ext_vector_type(4)));
+
+struct TinyLds {
+  _Float16 x[2][kTinyM][kTinyN + 8];    // high, low
+  _Float16 xt[2][kTinyN][kTinyM + 8];
+  _Float16 a[2][kTinyM][kTinyM + 8];    // A, then the polynomial, without diagonal
+  float da[kTinyM], db[kTinyM];
+  double red[kTinyWaves];
+};
+
+// Sum over k of P[p0 + lane % 16][k] Q[q0 + ..][k], k < depth, both parts.
+template <int LD>
+__device__ __forceinline__ f32v4 tiny_product(const _Float16 (*P)[LD], const _Float16 (*Pl)[LD], int p0,
+                                              const _Float16 (*Q)[LD], const _Float16 (*Ql)[LD], int q0, int depth,
+                                              int lane) {
+  f32v4 cross = {}, c = {};
+  const int r = lane % 16, k0 = lane / 16 * 8;
+  for (int k = k0; k < depth; k += 32) {
+    const h8 p = *reinterpret_cast<const h8*>(&P[p0 + r][k]), pl = *reinterpret_cast<const h8*>(&Pl[p0 + r][k]);
+    const h8 q = *reinterpret_cast<const h8*>(&Q[q0 + r][k]), ql = *reinterpret_cast<const h8*>(&Ql[q0 + r][k]);
+    cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(p, ql, cross, 0, 0, 0);
+    cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, q, cross, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(p, q, c, 0, 0, 0);
+  }
+  return c + cross * (1.0f / kLowScale);
+}
+
+struct TinyCoeffs {
+  float v[kMuonMaxSteps][3];
+};
+
+template <bool BF16, bool MUON>
+__global__ __launch_bounds__(kTinyThreads) void mat_tiny_kernel(const MuonMat* __restrict__ mats, const void* grad,
+                                                                float* mom, void* out, MuonK k, TinyCoeffs coeffs,
+                                                                int steps, double eps) {
+  __shared__ __attribute__((aligned(16))) TinyLds s;
+  const MuonMat& q = mats[blockIdx.x];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int m = q.m, n = q.n, nb = (n + 15) / 16, depth = (n + 31) / 32 * 32;
+  // this wave's blocks: rows bi * 16, columns (bj + 2 b) * 16; this lane's
+  // elements of a block: rows i .. i + 3, column j
+  const int bi = wave % 4, bj = wave / 4, i = bi * 16 + lane / 16 * 4;
+  auto col = [&](int b) { return (bj + 2 * b) * 16 + lane % 16; };
+  auto at = [&](int r, int j) { return q.start + (q.tall ? static_cast<int64_t>(j) * m + i + r : static_cast<int64_t>(i + r) * n + j); };
+  float x[kTinyBlocks][4];
+  double sum = 0.0;
+#pragma unroll
+  for (int b = 0; b < kTinyBlocks; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[b][r] = 0.0f;
+      if (i + r < m && col(b) < n) {
+        const int64_t e = at(r, col(b));
+        float g = load_elem(grad, e, BF16);
+        if constexpr (MUON) {
+          const float mm = __fadd_rn(__fmul_rn(k.mu, mom[e]), g);
+          mom[e] = mm;
+          g = k.nesterov ? __fadd_rn(g, __fmul_rn(k.mu, mm)) : mm;
+        }
+        x[b][r] = g;
+        sum += static_cast<double>(g) * static_cast<double>(g);
+      }
+    }
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if (lane == 0) s.red[wave] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < kTinyWaves; ++w) sum += s.red[w];
+  const float ex = static_cast<float>(1 << q.ex);
+  const double inv = static_cast<double>(ex) / (sqrt(sum) + eps);
+  auto put_x = [&]() {
+#pragma unroll
+    for (int b = 0; b < kTinyBlocks; ++b) {
+      if ((bj + 2 * b) * 16 >= depth) break;
+      _Float16 h[4], l[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        split(x[b][r], h[r], l[r]);
+        s.x[0][i + r][col(b)] = h[r];
+        s.x[1][i + r][col(b)] = l[r];
+      }
+      typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<h4*>(&s.xt[0][col(b)][i]) = h4{h[0], h[1], h[2], h[3]};
+      *reinterpret_cast<h4*>(&s.xt[1][col(b)][i]) = h4{l[0], l[1], l[2], l[3]};
+    }
+  };
+#pragma unroll
+  for (int b = 0; b < kTinyBlocks; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[b][r] = static_cast<float>(static_cast<double>(x[b][r]) * inv);
+  put_x();
+  for (int t = 0; t < steps; ++t) {
+    const float ca = coeffs.v[t][0], cb = coeffs.v[t][1], cc = coeffs.v[t][2];
+    __syncthreads();
+    // A: blocks (bi, bj) and (bi, bj + 2)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int j = col(b);
+      const f32v4 v = tiny_product(s.x[0], s.x[1], bi * 16, s.x[0], s.x[1], (bj + 2 * b) * 16, depth, lane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float y = v[r] * (kOpScale / (ex * ex));
+        if (i + r == j) {
+          s.da[j] = y / kOpScale;
+          y = 0.0f;
+        }
+        split(y, s.a[0][i + r][j], s.a[1][i + r][j]);
+      }
+    }
+    __syncthreads();
+    float y[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int j = col(b);
+      const f32v4 v = tiny_product(s.a[0], s.a[1], bi * 16, s.a[0], s.a[1], (bj + 2 * b) * 16, kTinyM, lane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float a = static_cast<float>(s.a[0][i + r][j]) + static_cast<float>(s.a[1][i + r][j]) * (1.0f / kLowScale);
+        const float di = s.da[i + r], a2 = v[r] * (1.0f / kOpScale);
+        y[b][r] = cb * a + cc * (a2 + (di + s.da[j]) * a);
+        if (i + r == j) {
+          s.db[j] = ca + cb * di + cc * (a2 * (1.0f / kOpScale) + di * di);
+          y[b][r] = 0.0f;
+        }
+      }
+    }
+    __syncthreads();   // A is read
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) split(y[b][r], s.a[0][i + r][col(b)], s.a[1][i + r][col(b)]);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < kTinyBlocks; ++b) {
+      if (bj + 2 * b >= nb) break;
+      const f32v4 v = tiny_product(s.a[0], s.a[1], bi * 16, s.xt[0], s.xt[1], (bj + 2 * b) * 16, kTinyM, lane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[b][r] = v[r] * (1.0f / kOpScale) + s.db[i + r] * x[b][r];
+    }
+    if (t + 1 == steps) break;
+    __syncthreads();   // X and X^T are read
+    put_x();
+  }
+  const float f = MUON ? k.lr * update_scale(k.scale_mode, q.rows, q.cols) / ex : 1.0f / ex;
+#pragma unroll
+  for (int b = 0; b < kTinyBlocks; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (i + r < m && col(b) < n) {
+        const int64_t e = at(r, col(b));
+        if constexpr (MUON) {
+          float* p = static_cast<float*>(out);
+          p[e] = __fsub_rn(__fmul_rn(p[e], k.decay), __fmul_rn(f, x[b][r]));
+        } else {
+          static_cast<uint16_t*>(out)[e] = static_cast<uint16_t>(bf16_rne(x[b][r] * f));
+        }
+      }
+    }
+}
+
 // ------------------------------------------------------------------ launches
 
 template <int BM, Product WHAT>
@@ -775,6 +988,18 @@ void launch_product(const rs_plan* p, char* work, int turn, const MuonK& k, void
 template <bool MUON>
 int run_matrices(rs_plan* p, const void* grad, int32_t grad_dt, float* mom, const float* coeffs, int32_t steps,
                  float eps, MuonK k, void* out, char* work, hipStream_t s, const char* who) {
+  if (p->n_tiny) {
+    TinyCoeffs c{};
+    std::copy(coeffs, coeffs + 3 * steps, &c.v[0][0]);
+    const dim3 grid(static_cast<unsigned>(p->n_tiny));
+    if (grad_dt == RS_BF16)
+      hipLaunchKernelGGL((mat_tiny_kernel<true, MUON>), grid, dim3(kTinyThreads), 0, s, p->tiny, grad, mom, out, k, c,
+                         steps, static_cast<double>(eps));
+    else
+      hipLaunchKernelGGL((mat_tiny_kernel<false, MUON>), grid, dim3(kTinyThreads), 0, s, p->tiny, grad, mom, out, k, c,
+                         steps, static_cast<double>(eps));
+  }
+  if (p->n_mats == 0) return launched(who);
   const dim3 chunks(static_cast<unsigned>(p->n_mat_chunks)), spread(static_cast<unsigned>(p->n_mat_spread));
   if (grad_dt == RS_BF16) {
     hipLaunchKernelGGL((mat_norm_kernel<true, MUON>), chunks, dim3(kThreads), 0, s, p->mats, p->mat_chunks, grad, mom,
@@ -814,7 +1039,7 @@ int check_matrices(const rs_plan* p, const float* coeffs, int32_t steps, float e
   for (int i = 0; i < 3 * steps; ++i)
     if (!std::isfinite(coeffs[i])) return fail(RS_EINVAL, std::string(who) + ": coefficients must be finite");
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(RS_EINVAL, std::string(who) + ": eps must be finite and >= 0");
-  if (p->n_mats && !work) return fail(RS_EINVAL, std::string(who) + ": null workspace");
+  if (p->mat_work_bytes && !work) return fail(RS_EINVAL, std::string(who) + ": null workspace");
   if (!aligned16(work)) return fail(RS_EALIGN, std::string(who) + ": workspace must be 16-byte aligned");
   if (work_bytes < p->mat_work_bytes)
     return fail(RS_EINVAL, std::string(who) + ": workspace of " + std::to_string(work_bytes) + " bytes, " +
@@ -845,7 +1070,7 @@ extern "C" int rs_orthogonalize(rs_plan* p, const void* src, int32_t src_dt, voi
   st = check_matrices(p, coeffs, steps, eps, work, work_bytes, who);
   if (st != RS_OK) return st;
   if (!aligned16(src) || !aligned16(out)) return fail(RS_EALIGN, std::string(who) + ": buffers must be 16-byte aligned");
-  if (p->n_mats == 0) return RS_OK;
+  if (p->n_mats + p->n_tiny == 0) return RS_OK;
   return run_matrices<false>(p, src, src_dt, nullptr, coeffs, steps, eps, MuonK{}, out, static_cast<char*>(work),
                              static_cast<hipStream_t>(stream), who);
 }
@@ -867,7 +1092,7 @@ extern "C" int rs_muon_step(rs_plan* p, float* param, const void* grad, int32_t 
   if (st != RS_OK) return st;
   if (!aligned16(param) || !aligned16(grad) || !aligned16(momentum))
     return fail(RS_EALIGN, std::string(who) + ": buffers must be 16-byte aligned");
-  if (p->n_mats == 0) return RS_OK;
+  if (p->n_mats + p->n_tiny == 0) return RS_OK;
   MuonK k{};
   k.mu = hp->momentum;
   k.lr = hp->lr;

@@ -485,6 +485,14 @@ void lower_quant(const std::vector<Tensor>& t, int64_t top, QuantList* ql) {
 
 namespace {
 
+// RS_MUON_TILE=64|128|256: that tile for every product of every matrix, small
+// ones too; 0 if not set.
+int forced_tile() {
+  const char* e = std::getenv("RS_MUON_TILE");
+  const int side = e ? std::atoi(e) : 0;
+  return side == 64 || side == 128 || side == 256 ? side : 0;
+}
+
 struct ProductTile {
   int32_t mat;
   uint16_t i, j;
@@ -596,11 +604,7 @@ void lower_product(const std::vector<MuonMat>& mats, bool sym, bool over_n, Prod
     return c;
   };
   out->side = count(256) >= kMatMinTiles ? 256 : count(128) >= kMatMinTiles ? 128 : 64;
-  // RS_MUON_TILE=64|128|256 forces one size
-  if (const char* e = std::getenv("RS_MUON_TILE")) {
-    const int side = std::atoi(e);
-    if (side == 64 || side == 128 || side == 256) out->side = side;
-  }
+  if (const int side = forced_tile()) out->side = side;
   // tiles in blocks of kBlock x kBlock: what runs together shares operand rows
   constexpr int64_t kBlock = 6;
   std::vector<ProductTile> tiles;
@@ -655,6 +659,10 @@ void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
     q.np = static_cast<int32_t>(align_up(q.n, kMatK));
     // 2^ex is within sqrt(2) of sqrt(n): entries of an orthogonal X are about 1 then
     while ((int64_t(1) << (2 * q.ex + 1)) <= q.n) ++q.ex;
+    if (q.m <= kMatTinyM && q.n <= kMatTinyN && !forced_tile()) {
+      mt->tiny.push_back(q);
+      continue;
+    }
     q.n_part = static_cast<int32_t>(ceil_div(x->n, kMatChunk));
     q.xh = take(int64_t(2) * q.m * q.np);
     q.xl = take(int64_t(2) * q.m * q.np);
@@ -780,6 +788,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->gather_split8 = tb.gather_split8;
     p->gather_split4 = tb.gather_split4;
     p->n_mats = static_cast<int64_t>(mt.mats.size());
+    p->n_tiny = static_cast<int64_t>(mt.tiny.size());
     p->n_mat_chunks = static_cast<int64_t>(mt.chunks.size());
     p->n_mat_spread = static_cast<int64_t>(mt.spread.size());
     for (int w = 0; w < 3; ++w) {
@@ -823,6 +832,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
                           align_up(sizeof(GatherChunk) * std::max<int64_t>(p->n_gchunks, 1), 256) +
                           align_up(sizeof(QJob) * std::max<int64_t>(p->n_gtile + p->n_gflat, 1), 256) +
                           align_up(sizeof(MuonMat) * std::max<int64_t>(p->n_mats, 1), 256) +
+                          align_up(sizeof(MuonMat) * std::max<int64_t>(p->n_tiny, 1), 256) +
                           align_up(sizeof(MatChunk) * std::max<int64_t>(p->n_mat_chunks, 1), 256) +
                           align_up(sizeof(MatJob) * std::max<int64_t>(p->n_mat_spread, 1), 256) +
                           list_bytes +
@@ -841,6 +851,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->gchunks = carve<GatherChunk>(cur, p->n_gchunks);
     p->gjobs = carve<QJob>(cur, p->n_gtile + p->n_gflat);
     p->mats = carve<MuonMat>(cur, p->n_mats);
+    p->tiny = carve<MuonMat>(cur, p->n_tiny);
     p->mat_chunks = carve<MatChunk>(cur, p->n_mat_chunks);
     p->mat_spread = carve<MatJob>(cur, p->n_mat_spread);
     for (int w = 0; w < 3; ++w) {
@@ -857,7 +868,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
               (p->n_qjobs == 0 || hipMemcpy(p->qjobs, tb.qjobs.data(), sizeof(QJob) * p->n_qjobs, hipMemcpyHostToDevice) == hipSuccess) &&
               (p->n_gchunks == 0 || hipMemcpy(p->gchunks, tb.gchunks.data(), sizeof(GatherChunk) * p->n_gchunks, hipMemcpyHostToDevice) == hipSuccess) &&
               (tb.gjobs.empty() || hipMemcpy(p->gjobs, tb.gjobs.data(), sizeof(QJob) * tb.gjobs.size(), hipMemcpyHostToDevice) == hipSuccess) &&
-              upload(p->mats, mt.mats) && upload(p->mat_chunks, mt.chunks) && upload(p->mat_spread, mt.spread) &&
+              upload(p->mats, mt.mats) && upload(p->tiny, mt.tiny) && upload(p->mat_chunks, mt.chunks) && upload(p->mat_spread, mt.spread) &&
               upload(p->mat_jobs[0], mt.list[0].jobs) && upload(p->mat_joins[0], mt.list[0].joins) &&
               upload(p->mat_jobs[1], mt.list[1].jobs) && upload(p->mat_joins[1], mt.list[1].joins) &&
               upload(p->mat_jobs[2], mt.list[2].jobs) && upload(p->mat_joins[2], mt.list[2].joins);

@@ -322,6 +322,8 @@ constexpr int kXcds = 8;
 constexpr int kMatMaxParts = 8;    // a tile's contraction is cut into at most this many parts
 constexpr int kMatMinSteps = 4;    // steps of kMatK in a part, at least
 constexpr int kMatJoinSteps = 10;  // joining parts costs about this many steps
+// Matrices whose X is at most kMatTinyM x kMatTinyN run in one workgroup.
+constexpr int64_t kMatTinyM = 64, kMatTinyN = 256;
 // Elements per work item of the pass that updates momentum and sums squares.
 constexpr int64_t kMatChunk = 8192;
 // Tile of the pass that splits the scaled matrix into its operands.
@@ -378,6 +380,7 @@ struct ProductList {
 // The matrices of a plan and the work lists of their passes, on the host.
 struct MuonTables {
   std::vector<MuonMat> mats;         // longest contraction first
+  std::vector<MuonMat> tiny;         // run in one workgroup each; no workspace, no work items
   std::vector<MatChunk> chunks;
   std::vector<MatJob> spread;
   ProductList list[3];               // X X^T, A A, polynomial times X
@@ -457,6 +460,8 @@ struct rs_plan {
   int64_t n_gtile = 0, n_gflat = 0;
 
   rs::MuonMat* mats = nullptr;         // whole matrices and their work lists
+  rs::MuonMat* tiny = nullptr;         // those that run in one workgroup each
+  int64_t n_tiny = 0;
   rs::MatChunk* mat_chunks = nullptr;
   rs::MatJob* mat_spread = nullptr;
   rs::ProductJob* mat_jobs[3] = {};    // X X^T, A A, polynomial times X

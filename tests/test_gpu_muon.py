@@ -21,7 +21,7 @@ from workloads import TensorSpec
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 SHAPES = [(2, 2), (2, 3), (3, 2), (2, 1000), (1000, 2), (17, 5), (48, 64), (64, 48), (64, 64), (65, 64), (63, 129),
-          (128, 128), (129, 127), (256, 256), (257, 300), (300, 257), (333, 1001), (520, 130), (384, 640)]
+          (64, 256), (256, 33), (64, 257), (128, 128), (129, 127), (256, 256), (257, 300), (300, 257), (333, 1001), (520, 130), (384, 640)]
 
 
 def tol(steps):
@@ -63,8 +63,10 @@ def _rel(x, y):
     return np.linalg.norm(x - y) / max(np.linalg.norm(y), 1e-300)
 
 
-@pytest.fixture(params=["64", "128", "256"])
+@pytest.fixture(params=["", "64", "128", "256"])
 def tile(request, monkeypatch):
+    """The output tile of the products: the plan's own choice (small matrices in one workgroup
+    each), or one size for all."""
     monkeypatch.setenv("RS_MUON_TILE", request.param)
     return request.param
 
@@ -245,7 +247,7 @@ def test_another_stream(gpu_lib):
 def test_calls_that_are_refused(gpu_lib):
     import structure_aware_grouped_amd as rs
     from structure_aware_grouped_amd import binding as b
-    plan = _load(rs, [TensorSpec("a", 16, 32, "WHOLE")])
+    plan = _load(rs, [TensorSpec("a", 100, 300, "WHOLE")])
     n = plan.R_mat * plan.S
     src, work = torch.zeros(n, device=DEV), rs.rs_muon_workspace(plan)
     out = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
