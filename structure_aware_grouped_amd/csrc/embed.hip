@@ -11,10 +11,13 @@
 //   gradient:  packed[r] = [prev[r] +] sigma * sum over t with ids[t] = r of dy[t]
 //
 // Both move bytes only. The gradient sums in a fixed order without atomics:
-// the tokens are sorted by (row, token); whole chunks of 64 sorted tokens of
-// one row (common tokens) are summed by workgroups of their own; then each row
-// adds its chunk sums and its remaining tokens in order.
+// the tokens are sorted by row, in their own order within a row; whole chunks
+// of 64 sorted tokens of one row (common tokens) are summed by workgroups of
+// their own; then each row adds its chunk sums and its remaining tokens in
+// order.
 #include "host_common.h"
+
+#include <type_traits>
 
 namespace rs {
 namespace {
@@ -90,86 +93,193 @@ __global__ __launch_bounds__(kThreads) void embed_rows_kernel(const void* table,
   }
 }
 
-// ------------------------------------------------------------------ sort
+// ------------------------------------------------------------------ fill
 
-constexpr int kRun = 2048;            // keys sorted in LDS by one workgroup
-constexpr int kSortThreads = 1024;
-constexpr int kSumChunk = 64;         // sorted tokens of one row summed ahead
+// Elements [from, to) of the tensor's interval <- prev + 0.0, or +0.0. Where
+// few rows are named, this and a pass over the named rows are faster than one
+// pass that looks for tokens of every row (131072 x 4096, 16384 tokens: 390 us
+// instead of 491 + 63 us with the sort). The fill runs as the tail of the
+// grids of the sort, the merge and the chunk sums, a third in each: those are
+// short of workgroups and wait for memory.
+struct Fill {
+  const float* prev;
+  void* packed;
+  int64_t from, to;   // from: a multiple of 4
+  bool out16;
+};
 
-// Keys (row << 32 | token) of kRun tokens, sorted in LDS by a bitonic network
-// (every key differs, so the order is unique); n is the power of two that
-// holds the largest run. A single run goes out as the sorted rows and tokens.
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const void* ids, bool wide, int64_t n_ids,
-                                                                  uint32_t rows, int n, uint64_t* keys, uint32_t* srow,
-                                                                  uint32_t* stok) {
-  __shared__ uint64_t s[kRun];
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kRun;
-  for (int i = threadIdx.x; i < n; i += kSortThreads) {
-    const int64_t t = base + i;
-    s[i] = t < n_ids ? static_cast<uint64_t>(row_of(ids, wide, t, rows)) << 32 | static_cast<uint32_t>(t) : ~0ull;
-  }
-  for (int size = 2; size <= n; size *= 2) {
-    for (int step = size / 2; step > 0; step /= 2) {
-      __syncthreads();
-      for (int p = threadIdx.x; p < n / 2; p += kSortThreads) {
-        const int i = 2 * p - (p & (step - 1)), j = i + step;
-        const uint64_t a = s[i], b = s[j];
-        if ((a > b) == ((i & size) == 0)) {
-          s[i] = b;
-          s[j] = a;
-        }
+constexpr int kFillPer = 4;   // 16-byte vectors of fp32 a thread
+constexpr int64_t fill_piece(int threads) { return int64_t(threads) * 4 * kFillPer; }
+
+template <int NT>
+__device__ __forceinline__ void fill_block(const Fill& f, int64_t block) {
+  const int64_t first = f.from + block * fill_piece(NT) + threadIdx.x * 4;
+#pragma unroll
+  for (int k = 0; k < kFillPer; ++k) {
+    const int64_t e = first + k * (NT * 4);
+    f32x4 v = {};
+    if (e + 4 <= f.to) {
+      if (f.prev) {
+        v = ldg(reinterpret_cast<const f32x4*>(f.prev + e));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] = __fadd_rn(v[t], 0.0f);
       }
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n && base + i < n_ids; i += kSortThreads) {
-    if (keys) {
-      keys[base + i] = s[i];
+      if (f.out16)
+        stg(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(f.packed) + e),
+            u32x2{bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16});
+      else
+        stg(reinterpret_cast<f32x4*>(static_cast<float*>(f.packed) + e), v);
     } else {
-      srow[i] = static_cast<uint32_t>(s[i] >> 32);
-      stok[i] = static_cast<uint32_t>(s[i]);
+      for (int64_t t = e; t < f.to; ++t) {
+        const float x = f.prev ? __fadd_rn(f.prev[t], 0.0f) : 0.0f;
+        if (f.out16) static_cast<uint16_t*>(f.packed)[t] = static_cast<uint16_t>(bf16_rne(x));
+        else static_cast<float*>(f.packed)[t] = x;
+      }
     }
   }
 }
 
-// Sorted runs -> one sorted list: a key's place is its place in its own run
-// plus the number of smaller keys in every other run, found by binary search,
-// eight runs at a time so that their loads overlap.
-__global__ __launch_bounds__(kThreads) void embed_merge_kernel(const uint64_t* __restrict__ keys, int64_t n_ids,
-                                                               uint32_t* srow, uint32_t* stok) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= n_ids) return;
-  const uint64_t key = keys[i];
-  const int64_t own = i / kRun, runs = (n_ids + kRun - 1) / kRun;
-  int64_t place = i - own * kRun;
-  constexpr int kAt = 8;
-  for (int64_t r0 = 0; r0 < runs; r0 += kAt) {
-    int lo[kAt], len[kAt];   // smaller keys lie in [0, lo), the undecided ones in [lo, lo + len)
+// ------------------------------------------------------------------ sort
+
+constexpr int kRun = 2048;            // tokens sorted in LDS by one workgroup
+constexpr int kSortThreads = 1024;
+constexpr int kSortGroups = kRun / kWave;
+constexpr int kDigitBits = 6, kDigits = 1 << kDigitBits;
+constexpr int kSumChunk = 64;         // sorted tokens of one row summed ahead
+static_assert(kDigits * kSortGroups == 2 * kSortThreads && kRun == 2 * kSortThreads, "two counters and tokens a thread");
+
+// kRun tokens sorted by row in LDS, in their own order within a row: a radix
+// sort from the lowest six bits up, `passes` times. A group of 64 neighbours
+// finds equal digits by ballots; the counters, by digit and then group, are
+// added up in front of each other, and a token's place is its counter's sum
+// plus its rank among the group's equals. A bitonic network of the same 2048
+// took 21 us, most of it barriers.
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const void* ids, bool wide, int64_t n_ids,
+                                                                  uint32_t rows, int passes, uint32_t* out_row,
+                                                                  uint32_t* out_tok, unsigned runs, Fill fill) {
+  __shared__ uint32_t key[2][kRun];
+  __shared__ uint16_t idx[2][kRun];
+  __shared__ uint32_t count[kDigits * kSortGroups];
+  __shared__ uint32_t wave_sum[kSortThreads / kWave];
+  if (blockIdx.x >= runs) {
+    fill_block<kSortThreads>(fill, blockIdx.x - runs);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kRun;
 #pragma unroll
-    for (int r = 0; r < kAt; ++r) {
-      lo[r] = 0;
-      const int64_t at = (r0 + r) * kRun;
-      len[r] = r0 + r == own || at >= n_ids ? 0 : static_cast<int>(n_ids - at < kRun ? n_ids - at : kRun);
+  for (int k = 0; k < 2; ++k) {
+    const int i = (wave * 2 + k) * kWave + lane;
+    key[0][i] = base + i < n_ids ? row_of(ids, wide, base + i, rows) : kNoRow;
+    idx[0][i] = static_cast<uint16_t>(i);
+  }
+  int from = 0;
+  for (int p = 0; p < passes; ++p) {
+    for (int i = tid; i < kDigits * kSortGroups; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    uint32_t row[2], tok[2], rank[2], slot[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int group = wave * 2 + k, i = group * kWave + lane;
+      row[k] = key[from][i];
+      tok[k] = idx[from][i];
+      const uint32_t digit = row[k] >> (p * kDigitBits) & (kDigits - 1);
+      uint64_t equal = ~0ull;
+#pragma unroll
+      for (int b = 0; b < kDigitBits; ++b) {
+        const uint64_t set = __ballot(digit >> b & 1);
+        equal &= digit >> b & 1 ? set : ~set;
+      }
+      rank[k] = __popcll(equal & ((1ull << lane) - 1));
+      slot[k] = digit * kSortGroups + group;
+      if (rank[k] == 0) count[slot[k]] = __popcll(equal);
     }
-    for (int step = 0; step < 12; ++step) {   // 2^11 = kRun: twelve halvings leave nothing undecided
+    __syncthreads();
+    // exclusive sums over the counters, two neighbours a thread
+    const uint32_t c0 = count[2 * tid], c1 = count[2 * tid + 1];
+    uint32_t sum = c0 + c1;
 #pragma unroll
-      for (int r = 0; r < kAt; ++r) {
-        if (len[r] > 0) {
-          const int half = len[r] / 2;
-          if (keys[(r0 + r) * kRun + lo[r] + half] < key) {
-            lo[r] += half + 1;
-            len[r] -= half + 1;
-          } else {
-            len[r] = half;
-          }
+    for (int o = 1; o < kWave; o <<= 1) {
+      const uint32_t up = __shfl_up(sum, o, kWave);
+      if (lane >= o) sum += up;
+    }
+    if (lane == kWave - 1) wave_sum[wave] = sum;
+    __syncthreads();
+    uint32_t before = sum - c0 - c1;
+    for (int w = 0; w < wave; ++w) before += wave_sum[w];
+    count[2 * tid] = before;
+    count[2 * tid + 1] = before + c0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t to = count[slot[k]] + rank[k];
+      key[from ^ 1][to] = row[k];
+      idx[from ^ 1][to] = static_cast<uint16_t>(tok[k]);
+    }
+    from ^= 1;
+    __syncthreads();
+  }
+  // what lies behind the last token sorted behind the ids that name no row,
+  // which it equals: those come first, in their own order
+  for (int i = tid; i < kRun && base + i < n_ids; i += kSortThreads) {
+    out_row[base + i] = key[from][i];
+    out_tok[base + i] = static_cast<uint32_t>(base) + idx[from][i];
+  }
+}
+
+// Sorted runs -> one sorted list: a token's place is its place in its own run
+// plus, in every other run, the number of smaller rows, or of smaller and
+// equal rows where that run's tokens come first. The runs' rows are searched
+// in LDS, kMergeRuns at a time (in memory the 11 dependent reads of one search
+// took 15 us).
+constexpr int kMergeRuns = 8;
+
+__global__ __launch_bounds__(kThreads) void embed_merge_kernel(const uint32_t* __restrict__ rows,
+                                                               const uint32_t* __restrict__ toks, int64_t n_ids,
+                                                               uint32_t* srow, uint32_t* stok, unsigned blocks,
+                                                               Fill fill) {
+  __shared__ __attribute__((aligned(16))) uint32_t s[kMergeRuns][kRun];
+  if (blockIdx.x >= blocks) {
+    fill_block<kThreads>(fill, blockIdx.x - blocks);
+    return;
+  }
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const bool in = i < n_ids;
+  const uint32_t row = in ? rows[i] : 0u, tok = in ? toks[i] : 0u;
+  const int64_t own = i / kRun;
+  int64_t place = i - own * kRun;
+  for (int64_t r0 = 0; r0 * kRun < n_ids; r0 += kMergeRuns) {
+    __syncthreads();
+    uint32_t* flat = &s[0][0];
+    const int64_t at = r0 * kRun;
+    const int here = static_cast<int>(n_ids - at < kMergeRuns * kRun ? n_ids - at : kMergeRuns * kRun);
+#pragma unroll 8
+    for (int e = threadIdx.x * 4; e < here / 4 * 4; e += kThreads * 4)
+      *reinterpret_cast<u32x4*>(flat + e) = *reinterpret_cast<const u32x4*>(rows + at + e);
+    if (static_cast<int>(threadIdx.x) < here % 4) flat[here / 4 * 4 + threadIdx.x] = rows[at + here / 4 * 4 + threadIdx.x];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kMergeRuns; ++r) {
+      // rows below `row` (or not above it) lie in front of lo
+      const int64_t first = at + r * kRun;
+      const int len = first >= n_ids || r0 + r == own ? 0 : static_cast<int>(n_ids - first < kRun ? n_ids - first : kRun);
+      const bool equal = r0 + r < own;
+      int lo = 0;
+#pragma unroll
+      for (int step = kRun; step > 0; step /= 2) {
+        const int next = lo + step;
+        if (next <= len) {
+          const uint32_t x = s[r][next - 1];
+          if (equal ? x <= row : x < row) lo = next;
         }
       }
+      place += lo;
     }
-#pragma unroll
-    for (int r = 0; r < kAt; ++r) place += lo[r];
   }
-  srow[place] = static_cast<uint32_t>(key >> 32);
-  stok[place] = static_cast<uint32_t>(key);
+  if (in) {
+    srow[place] = row;
+    stok[place] = tok;
+  }
 }
 
 // ------------------------------------------------------------------ gradient
@@ -183,26 +293,23 @@ __device__ __forceinline__ int64_t col_of(int64_t c0, int lane, int e) {
   return VEC ? c0 + lane * 4 + e : c0 + e * kWave + lane;
 }
 
+// Lanes past the width read its last columns, which they do not store: a
+// branch around every load would keep the loads from going out together.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ f32x4 load_cols(const void* p, int64_t row_at, int64_t c0, int64_t cols, int lane) {
-  f32x4 x = {};
+  f32x4 x;
   if constexpr (VEC) {
-    const int64_t c = c0 + lane * 4;
-    if (c < cols) {
-      if constexpr (BF16) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + row_at + c);
-        x = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                  __uint_as_float(w.y & 0xffff0000u)};
-      } else {
-        x = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + row_at + c);
-      }
+    const int64_t at = row_at + min(c0 + lane * 4, cols - 4);
+    if constexpr (BF16) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + at);
+      x = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                __uint_as_float(w.y & 0xffff0000u)};
+    } else {
+      x = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = col_of<false>(c0, lane, e);
-      if (c < cols) x[e] = In<BF16>::elem(p, row_at + c);
-    }
+    for (int e = 0; e < 4; ++e) x[e] = In<BF16>::elem(p, row_at + min(col_of<false>(c0, lane, e), cols - 1));
   }
   return x;
 }
@@ -226,20 +333,22 @@ template <bool BF16, bool VEC>
 __device__ __forceinline__ f32x4 sum_tokens(f32x4 sum, const Window& w, int from, int to, const void* dy, int64_t c0,
                                             int64_t cols, int lane) {
   int i = from;
-  for (; i + 4 <= to; i += 4) {   // four rows on their way at a time
-    f32x4 x[4];
+  auto add = [&](auto count) {
+    constexpr int N = decltype(count)::value;
+    for (; i + N <= to; i += N) {
+      f32x4 x[N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w.tok), i + k));
-      x[k] = load_cols<BF16, VEC>(dy, static_cast<int64_t>(t) * cols, c0, cols, lane);
+      for (int k = 0; k < N; ++k) {
+        const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w.tok), i + k));
+        x[k] = load_cols<BF16, VEC>(dy, static_cast<int64_t>(t) * cols, c0, cols, lane);
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum += x[k];
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum += x[k];
-  }
-  for (; i < to; ++i) {
-    const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w.tok), i));
-    sum += load_cols<BF16, VEC>(dy, static_cast<int64_t>(t) * cols, c0, cols, lane);
-  }
+  };
+  add(std::integral_constant<int, 16>{});   // rows on their way at a time
+  add(std::integral_constant<int, 4>{});
+  add(std::integral_constant<int, 1>{});
   return sum;
 }
 
@@ -247,14 +356,19 @@ __device__ __forceinline__ f32x4 sum_tokens(f32x4 sum, const Window& w, int from
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const uint32_t* __restrict__ srow,
                                                                const uint32_t* __restrict__ stok, int64_t n_ids,
-                                                               const void* dy, int64_t cols, float* part) {
+                                                               const void* dy, int64_t cols, float* part,
+                                                               unsigned chunks, unsigned pieces, Fill fill) {
+  if (blockIdx.x >= chunks * pieces) {
+    fill_block<kThreads>(fill, blockIdx.x - chunks * pieces);
+    return;
+  }
   const int lane = threadIdx.x % kWave;
-  const int64_t chunk = blockIdx.x;
+  const int64_t chunk = blockIdx.x / pieces;
   Window w;
   w.at(chunk * kSumChunk, srow, stok, n_ids, lane);
   const uint32_t first = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(w.row)));
   if (first == kNoRow || !__all(w.row == first)) return;
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.x % pieces) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
   if (c0 >= cols) return;
   const f32x4 sum = sum_tokens<BF16, VEC>(f32x4{}, w, 0, kSumChunk, dy, c0, cols, lane);
 #pragma unroll
@@ -275,9 +389,9 @@ __device__ __forceinline__ f32x4 sum_row(uint32_t r, int64_t& pos, Window& w, co
     const int from = static_cast<int>(pos - w.base);
     const int count = __popcll(__ballot(w.row == r && lane >= from));   // a row's positions are neighbours
     if (count == 0) break;
-    if (part && count == kSumChunk)
+    if (part && count == kSumChunk) {
       sum += load_cols<false, VEC>(part, w.base / kSumChunk * cols, c0, cols, lane);
-    else
+    } else
       sum = sum_tokens<BF16, VEC>(sum, w, from, from + count, dy, c0, cols, lane);
     pos += count;
     if (from + count < kSumChunk) break;   // the row ends inside the window
@@ -335,7 +449,6 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* srow, int64_t n, 
 
 constexpr int kGradRows = 8;   // table rows per wave of the pass over the whole table
 constexpr int kGradPos = 4;    // sorted positions per wave of the pass over the named rows
-
 // The whole table: each wave writes kGradRows rows of its columns.
 template <bool BF16, bool OUT16, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_table_kernel(const uint32_t* __restrict__ srow,
@@ -354,32 +467,49 @@ __global__ __launch_bounds__(kThreads) void embed_table_kernel(const uint32_t* _
   }
 }
 
-// The named rows alone, in place: each wave takes the rows that begin in its
-// kGradPos sorted positions.
-template <bool BF16, bool VEC>
+// The named rows alone: each wave takes the rows that begin in its kGradPos
+// sorted positions. The tokens of all its positions are on their way together;
+// a row that goes on behind them is summed by itself.
+template <bool BF16, bool OUT16, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_named_kernel(const uint32_t* __restrict__ srow,
                                                                const uint32_t* __restrict__ stok, int64_t n_ids,
-                                                               const void* dy, const float* part, float* packed,
-                                                               int64_t cols, float sigma) {
+                                                               const void* dy, const float* part, const float* prev,
+                                                               void* packed, int64_t cols, float sigma) {
+  static_assert(kSumChunk % kGradPos == 0, "a wave's positions lie in one window");
   const int lane = threadIdx.x % kWave;
   const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
   if (c0 >= cols) return;
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kGradPos;
-  const int64_t end = p0 + kGradPos < n_ids ? p0 + kGradPos : n_ids;
   Window w;
-  int64_t pos = p0;
-  uint32_t before = p0 ? srow[p0 - 1] : kNoRow;
-  while (pos < end) {
-    w.at(pos, srow, stok, n_ids, lane);
-    const uint32_t r = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w.row), static_cast<int>(pos - w.base)));
-    if (r == kNoRow) break;              // tokens without a row come last
-    if (r == before) {                   // a row that began in front of this wave's positions
-      ++pos;
-      continue;
+  w.at(p0, srow, stok, n_ids, lane);
+  const uint32_t before = p0 ? srow[p0 - 1] : kNoRow, behind = p0 + kGradPos < n_ids ? srow[p0 + kGradPos] : kNoRow;
+  const int at = static_cast<int>(p0 - w.base);
+  uint32_t row[kGradPos + 1];
+  f32x4 x[kGradPos];
+#pragma unroll
+  for (int k = 0; k < kGradPos; ++k) {
+    row[k] = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w.row), at + k));   // kNoRow behind the last token
+    const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w.tok), at + k));
+    x[k] = f32x4{};
+    if (row[k] != kNoRow && row[k] != before) x[k] = load_cols<BF16, VEC>(dy, static_cast<int64_t>(t) * cols, c0, cols, lane);
+  }
+  row[kGradPos] = behind;
+  f32x4 sum = {};
+  int start = 0;
+#pragma unroll
+  for (int k = 0; k < kGradPos; ++k) {
+    if (row[k] == kNoRow || row[k] == before) continue;   // no row, or one that began in front of these positions
+    if (k == 0 || row[k] != row[k - 1]) {
+      sum = f32x4{};
+      start = k;
     }
-    before = r;
-    const f32x4 sum = sum_row<BF16, VEC>(r, pos, w, srow, stok, n_ids, dy, part, c0, cols, lane);
-    store_row<false, VEC>(packed, packed, static_cast<int64_t>(r) * cols, sum, sigma, c0, cols, lane);
+    sum += x[k];
+    if (row[k] == row[k + 1]) {
+      if (k + 1 < kGradPos) continue;
+      int64_t pos = p0 + start;
+      sum = sum_row<BF16, VEC>(row[k], pos, w, srow, stok, n_ids, dy, part, c0, cols, lane);
+    }
+    store_row<OUT16, VEC>(packed, prev, static_cast<int64_t>(row[k]) * cols, sum, sigma, c0, cols, lane);
   }
 }
 
@@ -406,16 +536,18 @@ int check_ids(const void* ids, int32_t id_bytes, int64_t n_ids, const char* who)
 }
 
 struct EmbedWork {
-  int64_t keys, srow, stok, part, bytes;
+  int64_t rrow, rtok, srow, stok, part, bytes;   // sorted runs, sorted list, chunk sums
 };
 
 EmbedWork embed_work(int64_t n_ids, int64_t cols) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   EmbedWork w{};
-  w.keys = 0;
-  w.srow = w.keys + (n_ids > kRun ? up(8 * n_ids) : 0);
-  w.stok = w.srow + up(4 * n_ids);
-  w.part = w.stok + up(4 * n_ids);
+  const int64_t list = up(4 * n_ids), runs = n_ids > kRun ? list : 0;
+  w.rrow = 0;
+  w.rtok = w.rrow + runs;
+  w.srow = w.rtok + runs;
+  w.stok = w.srow + list;
+  w.part = w.stok + list;
   w.bytes = w.part + up(n_ids / kSumChunk * cols * 4);
   return w;
 }
@@ -433,31 +565,82 @@ void launch_rows(bool vec, const void* table, const void* ids, bool wide, int64_
                        static_cast<uint32_t>(units), static_cast<uint32_t>(t.rows), t.cols, scale, out);
 }
 
+struct GradCall {
+  const void* ids;
+  bool wide;
+  int64_t n_ids;
+  const void* dy;
+  const float* prev;   // of the tensor's interval, like packed
+  void* packed;
+  bool out16;
+  float sigma;
+  char* work;
+};
+
 template <bool BF16, bool VEC>
-void launch_grad(const Tensor& t, int64_t n_ids, const void* dy, const float* prev, void* packed, bool out16,
-                 float sigma, char* work, hipStream_t s) {
-  const EmbedWork w = embed_work(n_ids, t.cols);
-  uint32_t* srow = reinterpret_cast<uint32_t*>(work + w.srow);
-  uint32_t* stok = reinterpret_cast<uint32_t*>(work + w.stok);
+void launch_grad(const Tensor& t, const GradCall& c, hipStream_t s) {
+  const int64_t n = c.n_ids;
+  const EmbedWork w = embed_work(n, t.cols);
+  uint32_t* srow = reinterpret_cast<uint32_t*>(c.work + w.srow);
+  uint32_t* stok = reinterpret_cast<uint32_t*>(c.work + w.stok);
   const int64_t per = kWaveCols * (kThreads / kWave);
   const unsigned pieces = static_cast<unsigned>((t.cols + per - 1) / per);
-  float* part = n_ids >= kSumChunk ? reinterpret_cast<float*>(work + w.part) : nullptr;
-  if (part)
-    hipLaunchKernelGGL((embed_chunk_kernel<BF16, VEC>), dim3(static_cast<unsigned>(n_ids / kSumChunk), pieces),
-                       dim3(kThreads), 0, s, srow, stok, n_ids, dy, t.cols, part);
-  if (prev == packed) {
-    hipLaunchKernelGGL((embed_named_kernel<BF16, VEC>),
-                       dim3(static_cast<unsigned>((n_ids + kGradPos - 1) / kGradPos), pieces), dim3(kThreads), 0, s,
-                       srow, stok, n_ids, dy, part, static_cast<float*>(packed), t.cols, sigma);
+  const int64_t runs = (n + kRun - 1) / kRun;
+  float* part = n >= kSumChunk ? reinterpret_cast<float*>(c.work + w.part) : nullptr;
+  const bool in_place = c.prev == c.packed, named = in_place || n < t.rows / 2;
+  // the fill, in equal shares of the launches ahead of the named rows' pass
+  const int64_t fill = named && !in_place ? t.n : 0;
+  const int launches = 1 + (runs > 1) + (part != nullptr);
+  int64_t filled = 0;
+  int launch = 0;
+  auto share = [&](int threads, unsigned* blocks) {
+    const int64_t to = ++launch == launches ? fill : fill * launch / launches / 16 * 16;
+    const Fill f = {c.prev, c.packed, filled, to, c.out16};
+    *blocks = static_cast<unsigned>((to - filled + fill_piece(threads) - 1) / fill_piece(threads));
+    filled = to;
+    return f;
+  };
+  unsigned extra = 0;
+  Fill f = share(kSortThreads, &extra);
+  // digits that tell the rows apart from each other and from kNoRow, whose low
+  // digits are all ones
+  int passes = 1;
+  while (passes * kDigitBits < 32 && t.rows >> (passes * kDigitBits) > 0) ++passes;
+  uint32_t* rrow = runs > 1 ? reinterpret_cast<uint32_t*>(c.work + w.rrow) : srow;
+  uint32_t* rtok = runs > 1 ? reinterpret_cast<uint32_t*>(c.work + w.rtok) : stok;
+  if (runs + extra)
+    hipLaunchKernelGGL(embed_sort_kernel, dim3(static_cast<unsigned>(runs) + extra), dim3(kSortThreads), 0, s, c.ids,
+                       c.wide, n, static_cast<uint32_t>(t.rows), passes, rrow, rtok, static_cast<unsigned>(runs), f);
+  if (runs > 1) {
+    const unsigned blocks = static_cast<unsigned>((n + kThreads - 1) / kThreads);
+    f = share(kThreads, &extra);
+    hipLaunchKernelGGL(embed_merge_kernel, dim3(blocks + extra), dim3(kThreads), 0, s, rrow, rtok, n, srow, stok,
+                       blocks, f);
+  }
+  if (part) {
+    const unsigned chunks = static_cast<unsigned>(n / kSumChunk);
+    f = share(kThreads, &extra);
+    hipLaunchKernelGGL((embed_chunk_kernel<BF16, VEC>), dim3(chunks * pieces + extra), dim3(kThreads), 0, s, srow, stok,
+                       n, c.dy, t.cols, part, chunks, pieces, f);
+  }
+  if (named) {
+    if (n == 0) return;
+    const dim3 grid(static_cast<unsigned>((n + kGradPos - 1) / kGradPos), pieces);
+    if (c.out16)
+      hipLaunchKernelGGL((embed_named_kernel<BF16, true, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
+                         c.prev, c.packed, t.cols, c.sigma);
+    else
+      hipLaunchKernelGGL((embed_named_kernel<BF16, false, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
+                         c.prev, c.packed, t.cols, c.sigma);
     return;
   }
   const dim3 grid(static_cast<unsigned>((t.rows + kGradRows - 1) / kGradRows), pieces);
-  if (out16)
-    hipLaunchKernelGGL((embed_table_kernel<BF16, true, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n_ids, dy, part,
-                       prev, packed, static_cast<uint32_t>(t.rows), t.cols, sigma);
+  if (c.out16)
+    hipLaunchKernelGGL((embed_table_kernel<BF16, true, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
+                       c.prev, c.packed, static_cast<uint32_t>(t.rows), t.cols, c.sigma);
   else
-    hipLaunchKernelGGL((embed_table_kernel<BF16, false, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n_ids, dy, part,
-                       prev, packed, static_cast<uint32_t>(t.rows), t.cols, sigma);
+    hipLaunchKernelGGL((embed_table_kernel<BF16, false, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
+                       c.prev, c.packed, static_cast<uint32_t>(t.rows), t.cols, c.sigma);
 }
 
 }  // namespace
@@ -528,26 +711,13 @@ extern "C" int rs_embed_grad(rs_plan* p, int64_t tensor, const void* ids, int32_
                           ? static_cast<float>(static_cast<double>(scale) / static_cast<double>(p->V))
                           : scale;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  char* ws = static_cast<char*>(work);
-  uint32_t* srow = reinterpret_cast<uint32_t*>(ws + w.srow);
-  uint32_t* stok = reinterpret_cast<uint32_t*>(ws + w.stok);
-  if (n_ids) {
-    const int64_t runs = (n_ids + kRun - 1) / kRun;
-    int n = 2;
-    while (n < std::min<int64_t>(n_ids, kRun)) n *= 2;
-    uint64_t* keys = runs > 1 ? reinterpret_cast<uint64_t*>(ws + w.keys) : nullptr;
-    hipLaunchKernelGGL(embed_sort_kernel, dim3(static_cast<unsigned>(runs)), dim3(kSortThreads), 0, s, ids,
-                       id_bytes == 8, n_ids, static_cast<uint32_t>(t.rows), n, keys, srow, stok);
-    if (runs > 1)
-      hipLaunchKernelGGL(embed_merge_kernel, dim3(static_cast<unsigned>((n_ids + kThreads - 1) / kThreads)),
-                         dim3(kThreads), 0, s, keys, n_ids, srow, stok);
-  }
   void* out = static_cast<char*>(packed) + t.start * elem_bytes(packed_dt);
-  const float* pv = prev ? prev + t.start : nullptr;
-  const bool vec = t.cols % 4 == 0, out16 = packed_dt == RS_BF16;
-  if (dy_dt == RS_BF16 && vec) launch_grad<true, true>(t, n_ids, dy, pv, out, out16, sigma, ws, s);
-  else if (dy_dt == RS_BF16) launch_grad<true, false>(t, n_ids, dy, pv, out, out16, sigma, ws, s);
-  else if (vec) launch_grad<false, true>(t, n_ids, dy, pv, out, out16, sigma, ws, s);
-  else launch_grad<false, false>(t, n_ids, dy, pv, out, out16, sigma, ws, s);
+  const GradCall c = {ids, id_bytes == 8, n_ids, dy, prev ? prev + t.start : nullptr, out, packed_dt == RS_BF16, sigma,
+                      static_cast<char*>(work)};
+  const bool vec = t.cols % 4 == 0;
+  if (dy_dt == RS_BF16 && vec) launch_grad<true, true>(t, c, s);
+  else if (dy_dt == RS_BF16) launch_grad<true, false>(t, c, s);
+  else if (vec) launch_grad<false, true>(t, c, s);
+  else launch_grad<false, false>(t, c, s);
   return launched(who);
 }
