@@ -97,26 +97,44 @@ __global__ __launch_bounds__(kThreads) void embed_rows_kernel(const void* table,
 
 // Elements [from, to) of the tensor's interval <- prev + 0.0, or +0.0. Where
 // few rows are named, this and a pass over the named rows are faster than one
-// pass that looks for tokens of every row (131072 x 4096, 16384 tokens: 390 us
-// instead of 491 + 63 us with the sort). The fill runs as the tail of the
-// grids of the sort, the merge and the chunk sums, a third in each: those are
-// short of workgroups and wait for memory.
+// pass that looks for tokens of every row (131072 x 4096, 16384 tokens: 370 us
+// instead of 554). The fill runs as the tail of the grids of the sort (a
+// sixteenth) and of the chunk sums, which are short of workgroups and wait for
+// memory (the merge's 64 KiB of LDS would leave room for few fill blocks). One 16-byte nt-sc1 store a thread in workgroups of 256
+// filled 2 GiB at 7.16 TB/s, four a thread at 6.07, 64 threads at 4.82.
 struct Fill {
   const float* prev;
   void* packed;
-  int64_t from, to;   // from: a multiple of 4
+  int64_t from, to;   // from: a multiple of 16
   bool out16;
 };
 
-constexpr int kFillPer = 4;   // 16-byte vectors of fp32 a thread
-constexpr int64_t fill_piece(int threads) { return int64_t(threads) * 4 * kFillPer; }
+// elements of one block
+constexpr int64_t fill_piece(int threads, bool out16) { return int64_t(threads) * (out16 ? 8 : 4); }
 
 template <int NT>
 __device__ __forceinline__ void fill_block(const Fill& f, int64_t block) {
-  const int64_t first = f.from + block * fill_piece(NT) + threadIdx.x * 4;
+  const int64_t first = f.from + block * fill_piece(NT, f.out16);
+  if (f.out16) {
+    const int64_t e = first + threadIdx.x * 8;
+    float v[8] = {};
+    if (e + 8 <= f.to) {
+      if (f.prev) {
+        load8<false>(f.prev, e, v);
 #pragma unroll
-  for (int k = 0; k < kFillPer; ++k) {
-    const int64_t e = first + k * (NT * 4);
+        for (int t = 0; t < 8; ++t) v[t] = __fadd_rn(v[t], 0.0f);
+      }
+      uint32_t b[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) b[t] = bf16_rne(v[t]);
+      sts_at<kStoreNtSc1>(static_cast<uint16_t*>(f.packed) + first, threadIdx.x * 16,
+                          u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16});
+    } else {
+      for (int64_t t = e; t < f.to; ++t)
+        static_cast<uint16_t*>(f.packed)[t] = static_cast<uint16_t>(bf16_rne(f.prev ? __fadd_rn(f.prev[t], 0.0f) : 0.0f));
+    }
+  } else {
+    const int64_t e = first + threadIdx.x * 4;
     f32x4 v = {};
     if (e + 4 <= f.to) {
       if (f.prev) {
@@ -124,17 +142,9 @@ __device__ __forceinline__ void fill_block(const Fill& f, int64_t block) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) v[t] = __fadd_rn(v[t], 0.0f);
       }
-      if (f.out16)
-        stg(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(f.packed) + e),
-            u32x2{bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16});
-      else
-        stg(reinterpret_cast<f32x4*>(static_cast<float*>(f.packed) + e), v);
+      sts_at<kStoreNtSc1>(static_cast<float*>(f.packed) + first, threadIdx.x * 16, v);
     } else {
-      for (int64_t t = e; t < f.to; ++t) {
-        const float x = f.prev ? __fadd_rn(f.prev[t], 0.0f) : 0.0f;
-        if (f.out16) static_cast<uint16_t*>(f.packed)[t] = static_cast<uint16_t>(bf16_rne(x));
-        else static_cast<float*>(f.packed)[t] = x;
-      }
+      for (int64_t t = e; t < f.to; ++t) static_cast<float*>(f.packed)[t] = f.prev ? __fadd_rn(f.prev[t], 0.0f) : 0.0f;
     }
   }
 }
@@ -236,13 +246,8 @@ constexpr int kMergeRuns = 8;
 
 __global__ __launch_bounds__(kThreads) void embed_merge_kernel(const uint32_t* __restrict__ rows,
                                                                const uint32_t* __restrict__ toks, int64_t n_ids,
-                                                               uint32_t* srow, uint32_t* stok, unsigned blocks,
-                                                               Fill fill) {
+                                                               uint32_t* srow, uint32_t* stok) {
   __shared__ __attribute__((aligned(16))) uint32_t s[kMergeRuns][kRun];
-  if (blockIdx.x >= blocks) {
-    fill_block<kThreads>(fill, blockIdx.x - blocks);
-    return;
-  }
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const bool in = i < n_ids;
   const uint32_t row = in ? rows[i] : 0u, tok = in ? toks[i] : 0u;
@@ -448,17 +453,18 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* srow, int64_t n, 
 }
 
 constexpr int kGradRows = 8;   // table rows per wave of the pass over the whole table
-constexpr int kGradPos = 4;    // sorted positions per wave of the pass over the named rows
+constexpr int kGradPos = 8;    // sorted positions per wave of the pass over the named rows
 // The whole table: each wave writes kGradRows rows of its columns.
 template <bool BF16, bool OUT16, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_table_kernel(const uint32_t* __restrict__ srow,
                                                                const uint32_t* __restrict__ stok, int64_t n_ids,
                                                                const void* dy, const float* part, const float* prev,
-                                                               void* packed, uint32_t rows, int64_t cols, float sigma) {
+                                                               void* packed, uint32_t rows, int64_t cols, float sigma,
+                                                               unsigned pieces) {
   const int lane = threadIdx.x % kWave;
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.x % pieces) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
   if (c0 >= cols) return;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGradRows;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / pieces) * kGradRows;
   int64_t pos = lower_bound(srow, n_ids, static_cast<uint32_t>(r0), lane);
   Window w;
   for (int64_t r = r0; r < r0 + kGradRows && r < rows; ++r) {
@@ -474,12 +480,13 @@ template <bool BF16, bool OUT16, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_named_kernel(const uint32_t* __restrict__ srow,
                                                                const uint32_t* __restrict__ stok, int64_t n_ids,
                                                                const void* dy, const float* part, const float* prev,
-                                                               void* packed, int64_t cols, float sigma) {
+                                                               void* packed, int64_t cols, float sigma,
+                                                               unsigned pieces) {
   static_assert(kSumChunk % kGradPos == 0, "a wave's positions lie in one window");
   const int lane = threadIdx.x % kWave;
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.x % pieces) * (kThreads / kWave) + threadIdx.x / kWave) * kWaveCols;
   if (c0 >= cols) return;
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kGradPos;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x / pieces) * kGradPos;
   Window w;
   w.at(p0, srow, stok, n_ids, lane);
   const uint32_t before = p0 ? srow[p0 - 1] : kNoRow, behind = p0 + kGradPos < n_ids ? srow[p0 + kGradPos] : kNoRow;
@@ -588,20 +595,18 @@ void launch_grad(const Tensor& t, const GradCall& c, hipStream_t s) {
   const int64_t runs = (n + kRun - 1) / kRun;
   float* part = n >= kSumChunk ? reinterpret_cast<float*>(c.work + w.part) : nullptr;
   const bool in_place = c.prev == c.packed, named = in_place || n < t.rows / 2;
-  // the fill, in equal shares of the launches ahead of the named rows' pass
+  // the fill, in shares of the launches ahead of the named rows' pass; the
+  // chunk sums' launch takes the rest, with or without chunks
   const int64_t fill = named && !in_place ? t.n : 0;
-  const int launches = 1 + (runs > 1) + (part != nullptr);
   int64_t filled = 0;
-  int launch = 0;
-  auto share = [&](int threads, unsigned* blocks) {
-    const int64_t to = ++launch == launches ? fill : fill * launch / launches / 16 * 16;
+  auto share = [&](int64_t to, int threads, unsigned* blocks) {
     const Fill f = {c.prev, c.packed, filled, to, c.out16};
-    *blocks = static_cast<unsigned>((to - filled + fill_piece(threads) - 1) / fill_piece(threads));
+    *blocks = static_cast<unsigned>((to - filled + fill_piece(threads, c.out16) - 1) / fill_piece(threads, c.out16));
     filled = to;
     return f;
   };
   unsigned extra = 0;
-  Fill f = share(kSortThreads, &extra);
+  Fill f = share(fill / 16 / 16 * 16, kSortThreads, &extra);
   // digits that tell the rows apart from each other and from kNoRow, whose low
   // digits are all ones
   int passes = 1;
@@ -611,36 +616,32 @@ void launch_grad(const Tensor& t, const GradCall& c, hipStream_t s) {
   if (runs + extra)
     hipLaunchKernelGGL(embed_sort_kernel, dim3(static_cast<unsigned>(runs) + extra), dim3(kSortThreads), 0, s, c.ids,
                        c.wide, n, static_cast<uint32_t>(t.rows), passes, rrow, rtok, static_cast<unsigned>(runs), f);
-  if (runs > 1) {
-    const unsigned blocks = static_cast<unsigned>((n + kThreads - 1) / kThreads);
-    f = share(kThreads, &extra);
-    hipLaunchKernelGGL(embed_merge_kernel, dim3(blocks + extra), dim3(kThreads), 0, s, rrow, rtok, n, srow, stok,
-                       blocks, f);
-  }
-  if (part) {
-    const unsigned chunks = static_cast<unsigned>(n / kSumChunk);
-    f = share(kThreads, &extra);
+  if (runs > 1)
+    hipLaunchKernelGGL(embed_merge_kernel, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads),
+                       0, s, rrow, rtok, n, srow, stok);
+  const unsigned chunks = static_cast<unsigned>(n / kSumChunk);
+  f = share(fill, kThreads, &extra);
+  if (chunks + extra)
     hipLaunchKernelGGL((embed_chunk_kernel<BF16, VEC>), dim3(chunks * pieces + extra), dim3(kThreads), 0, s, srow, stok,
                        n, c.dy, t.cols, part, chunks, pieces, f);
-  }
   if (named) {
     if (n == 0) return;
-    const dim3 grid(static_cast<unsigned>((n + kGradPos - 1) / kGradPos), pieces);
+    const dim3 grid(static_cast<unsigned>((n + kGradPos - 1) / kGradPos) * pieces);
     if (c.out16)
       hipLaunchKernelGGL((embed_named_kernel<BF16, true, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
-                         c.prev, c.packed, t.cols, c.sigma);
+                         c.prev, c.packed, t.cols, c.sigma, pieces);
     else
       hipLaunchKernelGGL((embed_named_kernel<BF16, false, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
-                         c.prev, c.packed, t.cols, c.sigma);
+                         c.prev, c.packed, t.cols, c.sigma, pieces);
     return;
   }
-  const dim3 grid(static_cast<unsigned>((t.rows + kGradRows - 1) / kGradRows), pieces);
+  const dim3 grid(static_cast<unsigned>((t.rows + kGradRows - 1) / kGradRows) * pieces);
   if (c.out16)
     hipLaunchKernelGGL((embed_table_kernel<BF16, true, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
-                       c.prev, c.packed, static_cast<uint32_t>(t.rows), t.cols, c.sigma);
+                       c.prev, c.packed, static_cast<uint32_t>(t.rows), t.cols, c.sigma, pieces);
   else
     hipLaunchKernelGGL((embed_table_kernel<BF16, false, VEC>), grid, dim3(kThreads), 0, s, srow, stok, n, c.dy, part,
-                       c.prev, c.packed, static_cast<uint32_t>(t.rows), t.cols, c.sigma);
+                       c.prev, c.packed, static_cast<uint32_t>(t.rows), t.cols, c.sigma, pieces);
 }
 
 }  // namespace

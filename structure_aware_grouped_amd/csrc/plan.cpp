@@ -500,6 +500,16 @@ struct ProductTile {
   int32_t weight;  // multiplications per step (3 with high and low parts)
 };
 
+// from .. to-1 in an order in which what one XCD runs (places x, x + 8, ... of
+// the list that they continue at place `at`) are neighbours.
+std::vector<int> deal(int from, int to, size_t at) {
+  std::vector<int> order(to - from);
+  for (int x = 0, next = from; x < kXcds; ++x)
+    for (int b = 0; b < to - from; ++b)
+      if ((at + b) % kXcds == static_cast<size_t>(x)) order[b] = next++;
+  return order;
+}
+
 // The jobs of one product. Whole rounds of one tile per workgroup come first:
 // the workgroups of an XCD take neighbouring tiles and run in step, so that
 // they share operand rows in its L2 (out of step, with tiles cut at different
@@ -549,7 +559,7 @@ void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* ou
   const int64_t least = std::max<int64_t>(ceil_div(longest, kMatMaxParts - 1), kMatMinSteps);
   // no cuts where they would save less than joining the parts costs
   if (load[0] + longest - std::max(end, load[0] + least) <= kMatJoinSteps) {
-    for (int t = whole; t < n; ++t) give(t);
+    for (int t : deal(whole, n, out->jobs.size())) give(t);
     return;
   }
   int c = 0;
@@ -588,7 +598,10 @@ void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* ou
                      count[a.tile] < 2 ? -1 : first ? slab[a.tile] : jobs.back().second.slab + 1}});
   }
   std::stable_sort(jobs.begin(), jobs.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
-  for (const auto& j : jobs) out->jobs.push_back(j.second);
+  for (int from = 0, to = 0; from < static_cast<int>(jobs.size()); from = to) {   // of about the same length
+    while (to < static_cast<int>(jobs.size()) && 4 * jobs[to].first >= 3 * jobs[from].first) ++to;
+    for (int j : deal(from, to, out->jobs.size())) out->jobs.push_back(jobs[j].second);
+  }
 }
 
 // The tiles of one product over all matrices and their schedule. sym: only

@@ -314,14 +314,14 @@ constexpr int64_t kMatMaxSide = int64_t(1) << 20;
 constexpr int64_t kMatMaxMin = int64_t(1) << 16;
 // A product takes 256 x 256 output tiles where the plan's matrices give at
 // least kMatMinTiles of them, else 128 x 128 by the same rule, else 64 x 64.
-constexpr int64_t kMatMinTiles = 200;
+constexpr int64_t kMatMinTiles = 320;
 // Workgroups of a product that run at once: one per CU with 256-wide tiles
 // (128 KiB of LDS each), two with the others (64 KiB).
 constexpr int mat_places(int side) { return side == 256 ? 256 : 512; }
 constexpr int kXcds = 8;
 constexpr int kMatMaxParts = 8;    // a tile's contraction is cut into at most this many parts
 constexpr int kMatMinSteps = 4;    // steps of kMatK in a part, at least
-constexpr int kMatJoinSteps = 10;  // joining parts costs about this many steps
+constexpr int kMatJoinSteps = 16;  // joining parts costs about this many steps
 // Matrices whose X is at most kMatTinyM x kMatTinyN run in one workgroup.
 constexpr int64_t kMatTinyM = 64, kMatTinyN = 256;
 // Elements per work item of the pass that updates momentum and sums squares.
