@@ -173,7 +173,9 @@ int rs_plan_build(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t ali
  * RS_TM_KERNEL=direct runs the tile-major reorder of unpack / pack with
  * direct per-lane kernels instead of staging it through LDS. Both give
  * identical results. RS_MUON_TILE=64|128|256 forces the output tile of the
- * matrix products (rs_orthogonalize, rs_muon_step), small matrices included.
+ * matrix products (rs_orthogonalize, rs_muon_step), small matrices included;
+ * RS_MUON_PAIRS=1 runs their first two steps together for every matrix with
+ * more than 64 rows and columns.
  * On success *out owns host memory and one device allocation, released by
  * rs_plan_free. Errors: the above, RS_ENOMEM, RS_EHIP. */
 int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,
@@ -395,7 +397,11 @@ int rs_embed_workspace(const rs_plan* plan, int64_t tensor, int64_t n_ids, int64
  * Products take fp16 operands with fp32 sums; X is carried as a high and a
  * low fp16 part and the diagonals of A and of the polynomial in fp32, which
  * keeps the result within about 1e-3 of the exact one (Frobenius norm), ahead
- * of the bf16 rounding. The polynomials must keep every singular value below
+ * of the bf16 rounding, for polynomials of slopes up to about 2 between 0.3
+ * and 1.2, such as the published quintic; steeper ones raise each step's
+ * rounding by their slope. Where that costs less, the first two polynomials
+ * (|a| <= 4) are multiplied with each other and applied to X once. The
+ * polynomials must keep every singular value below
  * 7 (A is held to 2^16 / 2^10) and the off-diagonal entries of b A + c A^2
  * below 60. The norm is summed in fp64. The sums have a fixed order: the same
  * call gives the same bits. A zero matrix gives zeros; a NaN or an infinity

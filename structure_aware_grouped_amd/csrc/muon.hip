@@ -255,10 +255,50 @@ __global__ __launch_bounds__(kThreads) void mat_spread_kernel(const MuonMat* __r
 enum Product {
   P_GRAM,    // A = X X^T: off-diagonal part and diagonal
   P_POLY,    // a I + b A + c A^2: off-diagonal part and diagonal
+  P_MUL,     // a product of two polynomials in A: off-diagonal part and diagonal
   P_APPLY,   // polynomial times X: the next X
   P_OUT,     // the same, last step: the result in bf16
   P_STEP     // the same, last step: the parameters' update
 };
+
+// The first two steps of a paired matrix as one. With P = a I + b A + c A^2
+// the first one's polynomial, X X^T becomes P A P, so the second polynomial
+// can be had without X:
+//   A (P_GRAM), P (P_POLY), T = P A, A1 = T P (P_MUL), Q = a' I + b' A1 + c' A1^2
+//   (P_POLY), S = Q P (P_MUL), X <- S X (P_APPLY).
+// All of them are polynomials in A, so symmetric, and each product costs m^3;
+// X X^T and S X, the long products, are needed once. The rounding of A reaches
+// further than in a single step: it is raised by a^2, so this is done only for
+// |a| <= kPairMaxA and for the first two steps, where the singular values are
+// small (simulated: the same error as single steps; the third and fourth as
+// one gave 2 to 5 times the error).
+enum PairPart { kPairT = 0, kPairA1 = 1, kPairS = 2 };
+constexpr float kPairMaxA = 4.0f;
+
+// Where the operands and the result of one product of one matrix lie, in the
+// workspace. pair: the second of two paired steps (P_POLY, P_APPLY), or which
+// product (P_MUL).
+struct Where {
+  int64_t p, q, out, dp, dq, dout;   // offdiagonal parts and diagonals
+  int turn;                          // which transposed X is read
+};
+
+template <Product WHAT>
+__device__ __forceinline__ Where where(const MuonMat& m, int turn, int pair) {
+  if constexpr (WHAT == P_GRAM) return {m.xh, m.xh, m.a, 0, 0, m.da, 0};
+  if constexpr (WHAT == P_POLY) {
+    return pair && m.paired ? Where{m.a, m.a, m.c, m.da2, m.da2, m.dc, 0} : Where{m.a, m.a, m.b, m.da, m.da, m.db, 0};
+  }
+  if constexpr (WHAT == P_MUL) {
+    return pair == kPairT    ? Where{m.b, m.a, m.t, m.db, m.da, m.dt, 0}
+           : pair == kPairA1 ? Where{m.t, m.b, m.a, m.dt, m.db, m.da2, 0}
+                             : Where{m.c, m.b, m.t, m.dc, m.db, m.dt, 0};
+  }
+  // paired matrices have changed X once less
+  const int from = m.paired && turn > 0 && pair >= 0 ? (turn - 1) & 1 : turn & 1;
+  const bool s = pair == 1 && m.paired;
+  return {s ? m.t : m.b, m.xt[from], m.xt[from ^ 1], s ? m.dt : m.db, 0, 0, from};
+}
 
 // C = P Q^T on one BM x BM output tile by a 2 x WC grid of waves, each with
 // NI x NJ accumulators of 32 x 32. Operands go straight from memory to LDS,
@@ -406,8 +446,10 @@ __device__ static __forceinline__ void run(const _Float16* P, const _Float16* Q,
     if (full) wait<(S - 2) * T::kLoads, true>();
     else wait<0, true>();
     barrier();
-    if (more_loads) load(s + S, stage);
     if (more) fetch(next, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (more_loads) load(s + S, stage);
+    __builtin_amdgcn_sched_barrier(0);
     mma(1);
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -503,14 +545,14 @@ using T = Tile<BM>;
 static constexpr int kNT = NW * T::WC * kWave;
 static constexpr int kHeight = NW * IB * 32;
 static constexpr int kBytes = kHeight * BM * 4;   // of LDS
-static constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY;
+static constexpr bool kSym = WHAT == P_GRAM || WHAT == P_POLY || WHAT == P_MUL;
 static constexpr bool kLast = WHAT == P_OUT || WHAT == P_STEP;
 static constexpr int kRows = kHeight * (BM / 8) / kNT, kRowStep = kNT / (BM / 8);
-static constexpr int kAhead = WHAT == P_STEP || kRows < 4 ? 2 : 4;
+static constexpr int kAhead = WHAT == P_STEP || WHAT == P_MUL || (WHAT == P_POLY && BM == 256) || kRows < 4 ? 2 : 4;
 static constexpr int kCols = BM * (kHeight / 8) / kNT, kColStep = kNT / (kHeight / 8);
 static_assert(kRows % kAhead == 0 && kRows * kRowStep == kHeight && kCols * kColStep == BM, "whole rows and columns");
 
-struct In8 {   // of one row: A (POLY) or X, high and low; parameters (STEP)
+struct In8 {   // of one row: A (POLY) or X, high and low; both factors (MUL); parameters (STEP)
   h8 hi, lo;
   float d;
   f32x4 p[2];
@@ -552,7 +594,9 @@ __device__ static __forceinline__ void finish(void* out, int64_t at, const float
 
 // acc: the sums of each wave's IB block rows; base: the tile's row of row 0.
 __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const ProductJob& job, const MuonMat& q,
-                                           int base, char* work, char* lds, int turn, const MuonK& k, void* out) {
+                                           int base, char* work, char* lds, int turn, int pair, const MuonK& k,
+                                           void* out) {
+  const Where at_ = where<WHAT>(q, turn, pair);
   const int i0 = job.i * BM, j0 = job.j * BM;
   const int m = q.m, n = q.n, mp = q.mp, np = q.np;
   const bool two = q.two_part, tall = q.tall;
@@ -563,14 +607,14 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
   const float ex = static_cast<float>(1 << q.ex);
   // factor of the stored X in the result
   const float f = WHAT == P_STEP ? k.lr * update_scale(k.scale_mode, q.rows, q.cols) / ex : 1.0f / ex;
-  float* diag = reinterpret_cast<float*>(work + (WHAT == P_GRAM || WHAT == P_POLY ? q.da : q.db));
+  float* diag = reinterpret_cast<float*>(work + (WHAT == P_GRAM ? at_.dout : at_.dp));
 
   // row-wise: rows i0 + row(it), columns j .. j + 7
   const int r0 = tid / (BM / 8), c = tid % (BM / 8) * 8, j = j0 + c;
   auto tile_row = [&](int r) { return i0 + r / (IB * 32) * (T::NI * 32) + base + r % (IB * 32); };
   auto row = [&](int it) { return tile_row(r0 + it * kRowStep); };
-  const char* in_hi = work + (WHAT == P_POLY ? q.a : q.xh);
-  const char* in_lo = work + (WHAT == P_POLY ? q.al : q.xl);
+  const char* in_hi = work + (kSym ? at_.p : q.xh);
+  const char* in_lo = work + (WHAT == P_MUL ? at_.q : WHAT == P_POLY ? q.al : q.xl);
   const bool read_lo = WHAT != P_POLY || two;
   const bool step_rows = WHAT == P_STEP && !tall, whole_row = j + 8 <= n && n % 8 == 0;
   In8 in[2][kAhead];
@@ -597,8 +641,8 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
   };
   fetch(0);
   float dj[8] = {};
-  if constexpr (WHAT == P_POLY) {
-    const f32x4* d = reinterpret_cast<const f32x4*>(diag + min(j, mp - 8));   // 256-byte padded: whole vectors
+  if constexpr (WHAT == P_POLY || WHAT == P_MUL) {
+    const f32x4* d = reinterpret_cast<const f32x4*>(work + at_.dq + min(j, mp - 8) * 4);   // 256-byte padded: whole vectors
 #pragma unroll
     for (int t = 0; t < 8; ++t) dj[t] = d[t / 4][t % 4];
   }
@@ -637,7 +681,7 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
           }
       }
     } else if constexpr (WHAT == P_POLY) {
-      float* db = reinterpret_cast<float*>(work + q.db);
+      float* db = reinterpret_cast<float*>(work + at_.dout);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const float a = static_cast<float>(x.hi[t]) + static_cast<float>(x.lo[t]) * (1.0f / kLowScale);
@@ -648,6 +692,20 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
           const bool all = x.d > 0.5f;
           if (i < m) db[i] = all ? k.a + rest : k.a;
           y = all ? 0.0f : rest * kOpScale;
+        }
+        v[t] = y;
+      }
+    } else if constexpr (WHAT == P_MUL) {
+      float* dout = reinterpret_cast<float*>(work + at_.dout);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float y = v[t] * (1.0f / kOpScale) + (x.d * static_cast<float>(x.lo[t]) + static_cast<float>(x.hi[t]) * dj[t]);
+        if (job.i == job.j && i == j + t) {
+          const float full = y * (1.0f / kOpScale) + x.d * dj[t];
+          // S: its diagonal as in a single step, by the row's length before both
+          const float d = pair != kPairS || (i < m && reinterpret_cast<const float*>(work + q.da)[i] > 0.5f) ? full : k.a;
+          if (i < m) dout[i] = d;
+          y = (full - d) * kOpScale;
         }
         v[t] = y;
       }
@@ -670,8 +728,8 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
           lo[t] = b;
         }
         const int64_t at = (static_cast<int64_t>(i) * jp + j) * 2;
-        *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.a : WHAT == P_POLY ? q.b : q.xh) + at) = hi;
-        if (WHAT == P_APPLY || two)
+        *reinterpret_cast<h8*>(work + (kSym ? at_.out : q.xh) + at) = hi;
+        if (WHAT == P_APPLY || (WHAT != P_MUL && two))
           *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.al : WHAT == P_POLY ? q.bl : q.xl) + at) = lo;
       }
     } else if (!tall && i < m && j < n) {
@@ -719,9 +777,9 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
           lo[t] = b;
         }
         const int64_t at = (static_cast<int64_t>(jc) * mp + i) * 2;
-        *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.a : WHAT == P_POLY ? q.b : q.xt[turn ^ 1]) + at) = hi;
-        if (two)
-          *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.al : WHAT == P_POLY ? q.bl : q.xtl[turn ^ 1]) + at) = lo;
+        *reinterpret_cast<h8*>(work + at_.out + at) = hi;
+        if (WHAT != P_MUL && two)
+          *reinterpret_cast<h8*>(work + (WHAT == P_GRAM ? q.al : WHAT == P_POLY ? q.bl : q.xtl[at_.turn ^ 1]) + at) = lo;
       }
     } else if (i < m) {
       finish(out, q.start + static_cast<int64_t>(jc) * m + i, v, m - i, whole_col, f, k.decay, p[it & 1]);
@@ -734,7 +792,8 @@ __device__ static __forceinline__ void run(const f32x16 (&acc)[IB][T::NJ], const
 template <int BM, Product WHAT>
 __global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMat* __restrict__ mats,
                                                              const ProductJob* __restrict__ jobs, char* work,
-                                                             int64_t slabs, int turn, MuonK k, void* out) {
+                                                             int64_t slabs, int turn, int pair, MuonK k,
+                                                             void* out) {
   using T = Tile<BM>;
   using St = Store<BM, WHAT, 2, T::IB>;
   static_assert(St::kBytes <= T::kLds, "a pass fits the operand stages");
@@ -742,10 +801,10 @@ __global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMa
   const ProductJob job = jobs[blockIdx.x];
   const MuonMat& q = mats[job.mat];
   const int ld = WHAT == P_GRAM ? q.np : q.mp;
-  const char* p_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.b);
-  const char* q_hi = work + (WHAT == P_GRAM ? q.xh : WHAT == P_POLY ? q.a : q.xt[turn]);
+  const Where at = where<WHAT>(q, turn, pair);
+  const char *p_hi = work + at.p, *q_hi = work + at.q;
   const char* p_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.bl);
-  const char* q_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.xtl[turn]);
+  const char* q_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.xtl[at.turn]);
   const bool two = q.two_part;
   Acc<BM> acc = {};
   for (int part = two ? 0 : 2; part < 3; ++part) {   // high * low, low * high, high * high
@@ -757,7 +816,7 @@ __global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMa
     }
     Multiply<BM>::run(reinterpret_cast<const _Float16*>(part == 1 ? p_lo : p_hi),
                       reinterpret_cast<const _Float16*>(part == 0 ? q_lo : q_hi), ld, job.i * BM, q.m, job.j * BM,
-                      WHAT == P_GRAM || WHAT == P_POLY ? q.m : q.n, job.k0, job.k1, lds, acc);
+                      St::kSym ? q.m : q.n, job.k0, job.k1, lds, acc);
   }
   if (job.parts > 1) {
     Slab<BM>::store(acc, work + slabs, job.slab);
@@ -767,7 +826,7 @@ __global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMa
   for (int pass = 0; pass < T::kPasses; ++pass) {
     if (pass) __syncthreads();
     St::run(reinterpret_cast<const f32x16 (&)[T::IB][T::NJ]>(acc.v[pass * T::IB]), job, q, pass * T::IB * 32, work, lds,
-            turn, k, out);
+            turn, pair, k, out);
   }
 }
 
@@ -775,8 +834,8 @@ __global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMa
 template <int BM, Product WHAT>
 __global__ __launch_bounds__(Tile<BM>::WC * kWave) void mat_join_kernel(const MuonMat* __restrict__ mats,
                                                                         const ProductJob* __restrict__ joins,
-                                                                        char* work, int64_t slabs, int turn, MuonK k,
-                                                                        void* out) {
+                                                                        char* work, int64_t slabs, int turn, int pair,
+                                                                        MuonK k, void* out) {
   using T = Tile<BM>;
   using St = Store<BM, WHAT, 1, 1>;
   __shared__ __attribute__((aligned(16))) char lds[St::kBytes];
@@ -786,7 +845,7 @@ __global__ __launch_bounds__(Tile<BM>::WC * kWave) void mat_join_kernel(const Mu
   if (job.i * BM + strip * 32 >= q.mp) return;   // nothing of the matrix or its padding
   f32x16 v[1][T::NJ];
   Slab<BM>::add(v, work + slabs, job.slab, job.parts, strip);
-  St::run(v, job, q, strip * 32, work, lds, turn, k, out);
+  St::run(v, job, q, strip * 32, work, lds, turn, pair, k, out);
 }
 
 // ------------------------------------------------------------------ small matrices
@@ -966,21 +1025,21 @@ __global__ __launch_bounds__(kTinyThreads) void mat_tiny_kernel(const MuonMat* _
 // ------------------------------------------------------------------ launches
 
 template <int BM, Product WHAT>
-void launch_tiles(const rs_plan* p, int list, char* work, int turn, const MuonK& k, void* out, hipStream_t s) {
+void launch_tiles(const rs_plan* p, int list, char* work, int turn, int pair, const MuonK& k, void* out, hipStream_t s) {
   hipLaunchKernelGGL((mat_product_kernel<BM, WHAT>), dim3(static_cast<unsigned>(p->n_mat_jobs[list])),
-                     dim3(Tile<BM>::kNT), 0, s, p->mats, p->mat_jobs[list], work, p->mat_slabs, turn, k, out);
+                     dim3(Tile<BM>::kNT), 0, s, p->mats, p->mat_jobs[list], work, p->mat_slabs, turn, pair, k, out);
   if (p->n_mat_joins[list])
     hipLaunchKernelGGL((mat_join_kernel<BM, WHAT>),
                        dim3(static_cast<unsigned>(p->n_mat_joins[list] * (BM / 32))), dim3(Tile<BM>::WC * kWave), 0, s,
-                       p->mats, p->mat_joins[list], work, p->mat_slabs, turn, k, out);
+                       p->mats, p->mat_joins[list], work, p->mat_slabs, turn, pair, k, out);
 }
 
 template <Product WHAT>
-void launch_product(const rs_plan* p, char* work, int turn, const MuonK& k, void* out, hipStream_t s) {
-  constexpr int kList = WHAT == P_GRAM ? 0 : WHAT == P_POLY ? 1 : 2;
-  if (p->mat_side[kList] == 256) launch_tiles<256, WHAT>(p, kList, work, turn, k, out, s);
-  else if (p->mat_side[kList] == 128) launch_tiles<128, WHAT>(p, kList, work, turn, k, out, s);
-  else launch_tiles<64, WHAT>(p, kList, work, turn, k, out, s);
+void launch_product(const rs_plan* p, int list, char* work, int turn, int pair, const MuonK& k, void* out, hipStream_t s) {
+  if (p->n_mat_jobs[list] == 0) return;
+  if (p->mat_side[list] == 256) launch_tiles<256, WHAT>(p, list, work, turn, pair, k, out, s);
+  else if (p->mat_side[list] == 128) launch_tiles<128, WHAT>(p, list, work, turn, pair, k, out, s);
+  else launch_tiles<64, WHAT>(p, list, work, turn, pair, k, out, s);
 }
 
 // Momentum (MUON), norm and Newton-Schulz on every matrix of the plan; the
@@ -1017,14 +1076,35 @@ int run_matrices(rs_plan* p, const void* grad, int32_t grad_dt, float* mom, cons
     hipLaunchKernelGGL((mat_spread_kernel<false, MUON>), spread, dim3(kThreads), 0, s, p->mats, p->mat_spread, grad,
                        mom, work, k);
   }
-  for (int t = 0; t < steps; ++t) {
+  auto polynomial = [&](int t) {
     k.a = coeffs[3 * t];
     k.b = coeffs[3 * t + 1];
     k.c = coeffs[3 * t + 2];
-    launch_product<P_GRAM>(p, work, t & 1, k, nullptr, s);
-    launch_product<P_POLY>(p, work, t & 1, k, nullptr, s);
-    if (t + 1 < steps) launch_product<P_APPLY>(p, work, t & 1, k, nullptr, s);
-    else launch_product<MUON ? P_STEP : P_OUT>(p, work, t & 1, k, out, s);
+  };
+  auto apply = [&](int list, int t, int pair) {
+    if (t + 1 < steps) launch_product<P_APPLY>(p, list, work, t, pair, k, nullptr, s);
+    else launch_product<MUON ? P_STEP : P_OUT>(p, list, work, t, pair, k, out, s);
+  };
+  const bool pairs = p->mat_any_paired && steps >= 2 && std::fabs(coeffs[0]) <= kPairMaxA && std::fabs(coeffs[3]) <= kPairMaxA;
+  if (pairs) {
+    polynomial(0);
+    launch_product<P_GRAM>(p, kGram, work, 0, 0, k, nullptr, s);
+    launch_product<P_POLY>(p, kSquare, work, 0, 0, k, nullptr, s);
+    launch_product<P_MUL>(p, kSquarePaired, work, 0, kPairT, k, nullptr, s);
+    launch_product<P_MUL>(p, kSquarePaired, work, 0, kPairA1, k, nullptr, s);
+    apply(kApplySingle, 0, 0);
+    launch_product<P_GRAM>(p, kGramSingle, work, 0, 0, k, nullptr, s);
+    polynomial(1);
+    launch_product<P_POLY>(p, kSquare, work, 0, 1, k, nullptr, s);
+    k.a = coeffs[0] * coeffs[3];
+    launch_product<P_MUL>(p, kSquarePaired, work, 0, kPairS, k, nullptr, s);
+    apply(kApply, 1, 1);
+  }
+  for (int t = pairs ? 2 : 0; t < steps; ++t) {
+    polynomial(t);
+    launch_product<P_GRAM>(p, kGram, work, t, 0, k, nullptr, s);
+    launch_product<P_POLY>(p, kSquare, work, t, 0, k, nullptr, s);
+    apply(kApply, t, pairs ? 0 : -1);   // -1: no matrix has two steps as one
   }
   return launched(who);
 }

@@ -493,6 +493,13 @@ int forced_tile() {
   return side == 64 || side == 128 || side == 256 ? side : 0;
 }
 
+// RS_MUON_PAIRS=1: the first two steps together for every matrix whose
+// operands have one part.
+bool forced_pairs() {
+  const char* e = std::getenv("RS_MUON_PAIRS");
+  return e && std::strcmp(e, "1") == 0;
+}
+
 struct ProductTile {
   int32_t mat;
   uint16_t i, j;
@@ -604,13 +611,17 @@ void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* ou
   }
 }
 
-// The tiles of one product over all matrices and their schedule. sym: only
-// tiles on and below the diagonal of an m x m product; over_n: the
-// contraction runs over n (X X^T), else over m.
-void lower_product(const std::vector<MuonMat>& mats, bool sym, bool over_n, ProductList* out) {
+// The tiles of one product over the matrices of a list and their schedule.
+// m x m products are symmetric: only tiles on and below the diagonal.
+void lower_product(const std::vector<MuonMat>& mats, int list, ProductList* out) {
+  const bool sym = list != kApply && list != kApplySingle, over_n = list == kGram || list == kGramSingle;
+  auto listed = [&](const MuonMat& q) {
+    return list == kSquarePaired ? q.paired : list == kGramSingle || list == kApplySingle ? !q.paired : true;
+  };
   auto count = [&](int64_t side) {
     int64_t c = 0;
     for (const MuonMat& q : mats) {
+      if (!listed(q)) continue;
       const int64_t a = ceil_div(q.m, side), b = ceil_div(q.n, side);
       c += sym ? a * (a + 1) / 2 : a * b;
     }
@@ -623,6 +634,7 @@ void lower_product(const std::vector<MuonMat>& mats, bool sym, bool over_n, Prod
   std::vector<ProductTile> tiles;
   for (int32_t k = 0; k < static_cast<int32_t>(mats.size()); ++k) {
     const MuonMat& q = mats[k];
+    if (!listed(q)) continue;
     const int64_t ti = ceil_div(q.m, out->side), tj = sym ? ti : ceil_div(q.n, out->side);
     const int32_t steps = static_cast<int32_t>((over_n ? q.np : q.mp) / kMatK);
     for (int64_t i0 = 0; i0 < ti; i0 += kBlock)
@@ -688,6 +700,12 @@ void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
       q.al = take(int64_t(2) * q.m * q.mp);
       q.bl = take(int64_t(2) * q.m * q.mp);
     }
+    q.paired = mat_paired(q.m, q.n) || (forced_pairs() && !q.two_part);
+    if (q.paired) {
+      q.c = take(int64_t(2) * q.m * q.mp);
+      q.t = take(int64_t(2) * q.m * q.mp);
+      for (int64_t* d : {&q.dc, &q.dt, &q.da2}) *d = take(int64_t(4) * q.m);
+    }
     q.da = take(int64_t(4) * q.m);
     q.db = take(int64_t(4) * q.m);
     q.part = take(int64_t(8) * q.n_part);
@@ -702,8 +720,8 @@ void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
         mt->spread.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j)});
   }
   int64_t slab_bytes = 0;
-  for (int w = 0; w < 3; ++w) {
-    lower_product(mt->mats, w != 2, w == 0, &mt->list[w]);
+  for (int w = 0; w < kMatLists; ++w) {
+    lower_product(mt->mats, w, &mt->list[w]);
     const ProductList& l = mt->list[w];
     slab_bytes = std::max(slab_bytes, int64_t(4) * l.side * l.side * l.slabs);
   }
@@ -804,7 +822,8 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->n_tiny = static_cast<int64_t>(mt.tiny.size());
     p->n_mat_chunks = static_cast<int64_t>(mt.chunks.size());
     p->n_mat_spread = static_cast<int64_t>(mt.spread.size());
-    for (int w = 0; w < 3; ++w) {
+    for (const MuonMat& q : mt.mats) p->mat_any_paired |= q.paired != 0;
+    for (int w = 0; w < kMatLists; ++w) {
       p->n_mat_jobs[w] = static_cast<int64_t>(mt.list[w].jobs.size());
       p->n_mat_joins[w] = static_cast<int64_t>(mt.list[w].joins.size());
       p->mat_side[w] = mt.list[w].side;
@@ -867,7 +886,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->tiny = carve<MuonMat>(cur, p->n_tiny);
     p->mat_chunks = carve<MatChunk>(cur, p->n_mat_chunks);
     p->mat_spread = carve<MatJob>(cur, p->n_mat_spread);
-    for (int w = 0; w < 3; ++w) {
+    for (int w = 0; w < kMatLists; ++w) {
       p->mat_jobs[w] = carve<ProductJob>(cur, p->n_mat_jobs[w]);
       p->mat_joins[w] = carve<ProductJob>(cur, p->n_mat_joins[w]);
     }
@@ -881,10 +900,9 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
               (p->n_qjobs == 0 || hipMemcpy(p->qjobs, tb.qjobs.data(), sizeof(QJob) * p->n_qjobs, hipMemcpyHostToDevice) == hipSuccess) &&
               (p->n_gchunks == 0 || hipMemcpy(p->gchunks, tb.gchunks.data(), sizeof(GatherChunk) * p->n_gchunks, hipMemcpyHostToDevice) == hipSuccess) &&
               (tb.gjobs.empty() || hipMemcpy(p->gjobs, tb.gjobs.data(), sizeof(QJob) * tb.gjobs.size(), hipMemcpyHostToDevice) == hipSuccess) &&
-              upload(p->mats, mt.mats) && upload(p->tiny, mt.tiny) && upload(p->mat_chunks, mt.chunks) && upload(p->mat_spread, mt.spread) &&
-              upload(p->mat_jobs[0], mt.list[0].jobs) && upload(p->mat_joins[0], mt.list[0].joins) &&
-              upload(p->mat_jobs[1], mt.list[1].jobs) && upload(p->mat_joins[1], mt.list[1].joins) &&
-              upload(p->mat_jobs[2], mt.list[2].jobs) && upload(p->mat_joins[2], mt.list[2].joins);
+              upload(p->mats, mt.mats) && upload(p->tiny, mt.tiny) && upload(p->mat_chunks, mt.chunks) && upload(p->mat_spread, mt.spread);
+    for (int w = 0; w < kMatLists; ++w)
+      ok = ok && upload(p->mat_jobs[w], mt.list[w].jobs) && upload(p->mat_joins[w], mt.list[w].joins);
     if (!ok) {
       release(p);
       (void)hipSetDevice(prev);

@@ -308,6 +308,12 @@ static_assert(kGatherMaxRun / 4 < 65536, "a run of several rows keeps its vector
 constexpr int64_t kMatK = 64;
 // Matrices of at most this many rows of X have high and low parts throughout.
 constexpr int64_t kMatTwoPart = 64;
+// The first two steps of a matrix with n >= 1.5 m are applied to X together:
+// with r = n / m, 3 r + 5 instead of 6 r + 2 products of m^3 (halves of
+// symmetric ones counted). Only from kMatPairMin rows on, where products are
+// what a step's time goes into.
+constexpr int64_t kMatPairMin = 1024;
+constexpr bool mat_paired(int64_t m, int64_t n) { return m >= kMatPairMin && 2 * n >= 3 * m; }
 // Largest side and smallest-side limits of a matrix: byte offsets inside one
 // 256-row panel of an operand stay under 2^31, tile numbers fit 16 bits.
 constexpr int64_t kMatMaxSide = int64_t(1) << 20;
@@ -337,6 +343,7 @@ struct MuonMat {
   int64_t xt[2];      // n x mp: the transposed high part, read and written in turn
   int64_t a, b;       // m x mp: X X^T and the polynomial without (part of) their diagonals
   int64_t xtl[2], al, bl;   // low parts of xt, a and b (two_part only)
+  int64_t c, t, dc, dt, da2;   // paired only: two more like a and b, and their and A1's diagonals
   int64_t da, db;     // m fp32: their diagonals
   int64_t part;       // doubles: partial sums of squares
   int64_t inv;        // one double: 2^ex / (norm + eps)
@@ -345,6 +352,8 @@ struct MuonMat {
   int32_t ex;         // X is stored times 2^ex
   int32_t n_part;
   int32_t two_part;   // m <= kMatTwoPart: every operand has a low part
+  int32_t paired;     // the first two steps may be applied to X as one
+  int32_t unused;
 };
 
 // Work items of the matrix passes: a chunk of kMatChunk elements; a spread
@@ -377,13 +386,18 @@ struct ProductList {
   int32_t slabs = 0;
 };
 
+// The lists of a plan: X X^T, m x m products and polynomial times X of all
+// matrices, m x m products of the paired ones, and X X^T and polynomial times
+// X of the others.
+enum { kGram = 0, kSquare = 1, kApply = 2, kSquarePaired = 3, kGramSingle = 4, kApplySingle = 5, kMatLists = 6 };
+
 // The matrices of a plan and the work lists of their passes, on the host.
 struct MuonTables {
   std::vector<MuonMat> mats;         // longest contraction first
   std::vector<MuonMat> tiny;         // run in one workgroup each; no workspace, no work items
   std::vector<MatChunk> chunks;
   std::vector<MatJob> spread;
-  ProductList list[3];               // X X^T, A A, polynomial times X
+  ProductList list[kMatLists];
   int64_t work_bytes = 0;
   int64_t slabs = 0;                 // in the workspace
   bool too_large = false;            // a matrix beyond kMatMaxSide / kMatMaxMin
@@ -464,10 +478,11 @@ struct rs_plan {
   int64_t n_tiny = 0;
   rs::MatChunk* mat_chunks = nullptr;
   rs::MatJob* mat_spread = nullptr;
-  rs::ProductJob* mat_jobs[3] = {};    // X X^T, A A, polynomial times X
-  rs::ProductJob* mat_joins[3] = {};   // their cut tiles
-  int64_t n_mat_jobs[3] = {}, n_mat_joins[3] = {};
-  int mat_side[3] = {};
+  rs::ProductJob* mat_jobs[rs::kMatLists] = {};
+  rs::ProductJob* mat_joins[rs::kMatLists] = {};   // their cut tiles
+  int64_t n_mat_jobs[rs::kMatLists] = {}, n_mat_joins[rs::kMatLists] = {};
+  int mat_side[rs::kMatLists] = {};
+  bool mat_any_paired = false;
   int64_t n_mats = 0, n_mat_chunks = 0, n_mat_spread = 0;
   int64_t mat_work_bytes = 0, mat_slabs = 0;
   bool mat_too_large = false;

@@ -70,6 +70,9 @@ int main(int argc, char** argv) {
     for (auto r : {std::make_pair(q.xh, x), {q.xl, x}, {q.xt[0], xt}, {q.xt[1], xt}, {q.a, a}, {q.b, a},
                    {q.da, int64_t(4) * q.m}, {q.db, int64_t(4) * q.m}, {q.part, int64_t(8) * q.n_part}, {q.inv, int64_t(8)}})
       use.push_back({r.first, r.first + r.second});
+    if (q.paired)
+      for (auto r : {std::make_pair(q.c, a), {q.t, a}, {q.dc, int64_t(4) * q.m}, {q.dt, int64_t(4) * q.m}, {q.da2, int64_t(4) * q.m}})
+        use.push_back({r.first, r.first + r.second});
     if (q.two_part)
       for (auto r : {std::make_pair(q.xtl[0], xt), {q.xtl[1], xt}, {q.al, a}, {q.bl, a}}) use.push_back({r.first, r.first + r.second});
   }
@@ -85,8 +88,9 @@ int main(int argc, char** argv) {
   if (end > mt.work_bytes) return bad("workspace size");
 
   std::string text;
-  for (int w = 0; w < 3; ++w) {
+  for (int w = 0; w < kMatLists; ++w) {
     const ProductList& l = mt.list[w];
+    const bool apply = w == kApply || w == kApplySingle;
     std::map<std::tuple<int, int, int>, std::vector<ProductJob>> tiles;
     std::vector<double> share(mat_places(l.side), 0.0);
     double total = 0;
@@ -99,8 +103,9 @@ int main(int argc, char** argv) {
     size_t need = 0, cut = 0;
     for (size_t k = 0; k < mt.mats.size(); ++k) {
       const MuonMat& q = mt.mats[k];
-      const int64_t ti = ceil_div(q.m, l.side), tj = w == 2 ? ceil_div(q.n, l.side) : ti;
-      need += w == 2 ? ti * tj : ti * (ti + 1) / 2;
+      if (w == kSquarePaired ? !q.paired : (w == kGramSingle || w == kApplySingle) && q.paired) continue;
+      const int64_t ti = ceil_div(q.m, l.side), tj = apply ? ceil_div(q.n, l.side) : ti;
+      need += apply ? ti * tj : ti * (ti + 1) / 2;
     }
     if (tiles.size() != need) return bad("tiles missing");
     std::map<std::tuple<int, int, int>, ProductJob> joins;
@@ -109,8 +114,8 @@ int main(int argc, char** argv) {
     std::vector<char> slab(l.slabs, 0);
     for (auto& [key, js] : tiles) {
       const MuonMat& q = mt.mats[std::get<0>(key)];
-      const int i = std::get<1>(key), j = std::get<2>(key), steps = (w == 0 ? q.np : q.mp) / kMatK;
-      if (int64_t(i) * l.side >= q.m || int64_t(j) * l.side >= (w == 2 ? q.n : q.m) || (w != 2 && j > i)) return bad("tile outside");
+      const int i = std::get<1>(key), j = std::get<2>(key), steps = (w == kGram || w == kGramSingle ? q.np : q.mp) / kMatK;
+      if (int64_t(i) * l.side >= q.m || int64_t(j) * l.side >= (apply ? q.n : q.m) || (!apply && j > i)) return bad("tile outside");
       std::sort(js.begin(), js.end(), [](const ProductJob& a, const ProductJob& b) { return a.k0 < b.k0; });
       int k = 0, number = 0;
       for (const ProductJob& p : js) {

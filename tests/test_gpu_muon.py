@@ -63,11 +63,12 @@ def _rel(x, y):
     return np.linalg.norm(x - y) / max(np.linalg.norm(y), 1e-300)
 
 
-@pytest.fixture(params=["", "64", "128", "256"])
+@pytest.fixture(params=["", "64", "128", "256", "64 pairs", "128 pairs", "256 pairs"])
 def tile(request, monkeypatch):
     """The output tile of the products: the plan's own choice (small matrices in one workgroup
-    each), or one size for all."""
-    monkeypatch.setenv("RS_MUON_TILE", request.param)
+    each), or one size for all; and the first two steps together."""
+    monkeypatch.setenv("RS_MUON_TILE", request.param.split(" ")[0])
+    monkeypatch.setenv("RS_MUON_PAIRS", "1" if "pairs" in request.param else "0")
     return request.param
 
 
@@ -144,7 +145,7 @@ def test_steps_and_coefficients_per_step(gpu_lib, tile):
     mats = [_gaussian(rng, sp.rows, sp.cols) for sp in specs]
     src, work = _flat(plan, mats), rs.rs_muon_workspace(plan)
     out = torch.zeros(plan.R_mat * plan.S, dtype=torch.bfloat16, device=DEV)
-    for coeffs in ([(1.5, -0.5, 0.0)], [(3.4445, -4.775, 2.0315)] * 3 + [(1.875, -1.25, 0.375)] * 3):
+    for coeffs in ([(1.5, -0.5, 0.0)], [(1.5, -0.5, 0.0)] * 2, [(2.0, -1.5, 0.5)] * 3, [(4.5, -6.0, 2.5), (1.5, -0.5, 0.0)], [(3.4445, -4.775, 2.0315)] * 3 + [(1.875, -1.25, 0.375)] * 3):
         rs.rs_orthogonalize(plan, src, out, work, coeffs=coeffs, steps=len(coeffs))
         for i, g in enumerate(mats):
             want = OM.orthogonalize(g, [tuple(float(np.float32(v)) for v in r) for r in coeffs])
