@@ -351,8 +351,9 @@ int rs_adam8_step(rs_plan* plan, float* param, const float* grad, void* q_m, flo
  * gathered: device, R_mat*S elements of dt (RS_F32 or RS_BF16). ids: device,
  * n_ids signed integers of id_bytes (4 or 8) bytes. scale: finite. out:
  * device, n_ids x cols row-major of out_dt (RS_F32 or RS_BF16), overlapping
- * neither input. gathered and out 16-byte aligned. n_ids may be 0. rows, cols
- * and n_ids under 2^31, n_ids * cols at most 2^39.
+ * neither input. gathered and out 16-byte aligned. n_ids may be 0.
+ * Limits (RS_ERANGE): rows under 2^27, rows * cols at most 2^34, n_ids under
+ * 2^26, n_ids * cols at most 2^33.
  * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
 int rs_embed_rows(rs_plan* plan, int64_t tensor, const void* gathered, int32_t dt, const void* ids,
                   int32_t id_bytes, int64_t n_ids, float scale, void* out, int32_t out_dt, void* stream);
@@ -375,7 +376,7 @@ int rs_embed_rows(rs_plan* plan, int64_t tensor, const void* gathered, int32_t d
  * device fp32 R_mat*S or NULL. packed: device R_mat*S of packed_dt (RS_F32 or
  * RS_BF16). work: device memory of rs_embed_workspace bytes, contents not
  * kept between calls; calls that may overlap need a workspace each. All
- * 16-byte aligned; ids as in rs_embed_rows.
+ * 16-byte aligned; ids and limits as in rs_embed_rows.
  * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
 int rs_embed_grad(rs_plan* plan, int64_t tensor, const void* ids, int32_t id_bytes, int64_t n_ids,
                   const void* dy, int32_t dy_dt, const float* prev, void* packed, int32_t packed_dt,
@@ -412,7 +413,8 @@ int rs_embed_workspace(const rs_plan* plan, int64_t tensor, int64_t n_ids, int64
  * zero matrix gives NaN). work: device memory of rs_muon_workspace bytes,
  * whose contents need not be kept between calls; calls that may overlap (on
  * other streams, or in graphs that may) need a workspace each. All 16-byte
- * aligned. A matrix needs both sides at most 2^20 and one at most 2^16.
+ * aligned. Limits (RS_ERANGE): a matrix's sides at most 2^20, one of them at
+ * most 2^16, and the matrices of a plan at most 2^22 tiles of 64 x 64.
  * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
 int rs_orthogonalize(rs_plan* plan, const void* src, int32_t src_dt, void* out, const float* coeffs,
                      int32_t steps, float eps, void* work, int64_t work_bytes, void* stream);

@@ -215,8 +215,10 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const void* id
     }
     if (lane == kWave - 1) wave_sum[wave] = sum;
     __syncthreads();
-    uint32_t before = sum - c0 - c1;
-    for (int w = 0; w < wave; ++w) before += wave_sum[w];
+    uint32_t waves = lane < wave ? wave_sum[lane] : 0u;   // of the waves in front, 15 at most
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) waves += __shfl_xor(waves, o, kWave);
+    const uint32_t before = sum - c0 - c1 + __shfl(waves, 0, kWave);
     count[2 * tid] = before;
     count[2 * tid + 1] = before + c0;
     __syncthreads();
@@ -522,15 +524,20 @@ __global__ __launch_bounds__(kThreads) void embed_named_kernel(const uint32_t* _
 
 // ------------------------------------------------------------------ host
 
+// Limits that keep every launch under 2^32 work-items: 32 per row or token in
+// the gradient's passes, a quarter per element in the fill and the lookup.
+constexpr int64_t kEmbedMaxRows = int64_t(1) << 27, kEmbedMaxIds = int64_t(1) << 26;
+constexpr int64_t kEmbedMaxTable = int64_t(1) << 34, kEmbedMaxElems = int64_t(1) << 33;
+
 // The table of an embedding call: a tensor of the plan in row-major order.
 int check_table(const rs_plan* p, int64_t tensor, int64_t n_ids, const char* who) {
   if (tensor < 0 || tensor >= p->n) return fail(RS_EINVAL, std::string(who) + ": no such tensor");
   const Tensor& t = p->t[tensor];
   if (t.kind == RS_TILEMAJOR) return fail(RS_EINVAL, std::string(who) + ": a TILEMAJOR tensor has no contiguous rows");
   if (n_ids < 0) return fail(RS_EINVAL, std::string(who) + ": negative number of tokens");
-  if (t.rows >= (int64_t(1) << 31) || t.cols >= (int64_t(1) << 31) || n_ids >= (int64_t(1) << 31) ||
-      n_ids * t.cols > kMaxElems)
-    return fail(RS_ERANGE, std::string(who) + ": rows, columns and tokens must be under 2^31, tokens * columns at most 2^39");
+  if (t.rows >= kEmbedMaxRows || t.n > kEmbedMaxTable || n_ids >= kEmbedMaxIds || n_ids * t.cols > kEmbedMaxElems)
+    return fail(RS_ERANGE, std::string(who) + ": rows under 2^27, tokens under 2^26, table at most 2^34 elements, "
+                               "tokens * columns at most 2^33");
   return RS_OK;
 }
 

@@ -1113,7 +1113,7 @@ int check_matrices(const rs_plan* p, const float* coeffs, int32_t steps, float e
                    int64_t work_bytes, const char* who) {
   if (p->mat_too_large)
     return fail(RS_ERANGE, std::string(who) + ": a WHOLE matrix has a side over " + std::to_string(kMatMaxSide) +
-                               " or both over " + std::to_string(kMatMaxMin));
+                               " or both over " + std::to_string(kMatMaxMin) + ", or there are too many");
   if (!coeffs || steps < 1 || steps > kMuonMaxSteps)
     return fail(RS_EINVAL, std::string(who) + ": 1 to " + std::to_string(kMuonMaxSteps) + " steps of three coefficients");
   for (int i = 0; i < 3 * steps; ++i)

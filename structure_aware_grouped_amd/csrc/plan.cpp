@@ -653,6 +653,7 @@ void lower_product(const std::vector<MuonMat>& mats, int list, ProductList* out)
 // the work lists of the passes over them (rs_orthogonalize, rs_muon_step).
 void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
   std::vector<const Tensor*> ms;
+  int64_t tiles = 0;
   for (const Tensor& x : t) {
     if (x.kind != RS_WHOLE || x.rows < 2 || x.cols < 2) continue;
     if (std::max(x.rows, x.cols) > kMatMaxSide || std::min(x.rows, x.cols) > kMatMaxMin) {
@@ -660,6 +661,11 @@ void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
       continue;
     }
     ms.push_back(&x);
+    tiles += ceil_div(x.rows, kMatSpread) * ceil_div(x.cols, kMatSpread);
+  }
+  if (tiles > kMatMaxTiles) {
+    mt->too_large = true;
+    return;
   }
   // longest products first, so that the last ones to start are short
   std::stable_sort(ms.begin(), ms.end(), [](const Tensor* a, const Tensor* b) {
@@ -845,7 +851,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     // RS_ADAM_TILE_KERNEL=workgroup: the Adam step gives every tile a 256-thread
     // workgroup even when one wave would hold it (=wave: the default choice)
     if (const char* ak = std::getenv("RS_ADAM_TILE_KERNEL")) p->adam_wave_tiles = std::strcmp(ak, "workgroup") != 0;
-    // RS_MAX_GRID=n caps every launch at n workgroups (rounded down to a
+    // RS_MAX_GRID=n caps every launch of the transforms at n workgroups (rounded down to a
     // multiple of 8, at least 8), so the workgroups loop over work items; the
     // results do not change.
     if (const char* mg = std::getenv("RS_MAX_GRID")) {

@@ -318,6 +318,7 @@ constexpr bool mat_paired(int64_t m, int64_t n) { return m >= kMatPairMin && 2 *
 // 256-row panel of an operand stay under 2^31, tile numbers fit 16 bits.
 constexpr int64_t kMatMaxSide = int64_t(1) << 20;
 constexpr int64_t kMatMaxMin = int64_t(1) << 16;
+constexpr int64_t kMatMaxTiles = int64_t(1) << 22;   // 64 x 64 tiles of all matrices: launches under 2^32 work-items
 // A product takes 256 x 256 output tiles where the plan's matrices give at
 // least kMatMinTiles of them, else 128 x 128 by the same rule, else 64 x 64.
 constexpr int64_t kMatMinTiles = 320;
@@ -400,7 +401,7 @@ struct MuonTables {
   ProductList list[kMatLists];
   int64_t work_bytes = 0;
   int64_t slabs = 0;                 // in the workspace
-  bool too_large = false;            // a matrix beyond kMatMaxSide / kMatMaxMin
+  bool too_large = false;            // beyond the limits above: the matrix calls return RS_ERANGE
 };
 void lower_muon(const std::vector<Tensor>& t, MuonTables* mt);
 
