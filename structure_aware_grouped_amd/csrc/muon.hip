@@ -123,11 +123,9 @@ __global__ __launch_bounds__(kThreads) void mat_norm_kernel(const MuonMat* __res
   }
 }
 
-// 2^ex / (norm + eps) of each matrix, one workgroup per matrix; the partial
-// sums are added in a fixed order.
-__global__ __launch_bounds__(kThreads) void mat_scale_kernel(const MuonMat* __restrict__ mats, char* work, double eps) {
-  __shared__ double red[kThreads / kWave];
-  const MuonMat& q = mats[blockIdx.x];
+// 2^ex / (norm + eps) of a matrix, by one workgroup; the partial sums are
+// added in a fixed order.
+__device__ __forceinline__ double mat_scale(const MuonMat& q, const char* work, double eps, double* red) {
   const double* part = reinterpret_cast<const double*>(work + q.part);
   double sum = 0.0;
   for (int i = threadIdx.x; i < q.n_part; i += kThreads) sum += part[i];
@@ -135,10 +133,18 @@ __global__ __launch_bounds__(kThreads) void mat_scale_kernel(const MuonMat* __re
   for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
   if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / kWave; ++w) sum += red[w];
-    *reinterpret_cast<double*>(work + q.inv) = static_cast<double>(1 << q.ex) / (sqrt(sum) + eps);
-  }
+  sum = 0.0;
+  for (int w = 0; w < kThreads / kWave; ++w) sum += red[w];
+  return static_cast<double>(1 << q.ex) / (sqrt(sum) + eps);
+}
+
+// The same for every matrix ahead of the split, where adding up the sums in
+// every workgroup of the split would cost more than a launch.
+__global__ __launch_bounds__(kThreads) void mat_scale_kernel(const MuonMat* __restrict__ mats, char* work, double eps) {
+  __shared__ double red[kThreads / kWave];
+  const MuonMat& q = mats[blockIdx.x];
+  const double inv = mat_scale(q, work, eps, red);
+  if (threadIdx.x == 0) *reinterpret_cast<double*>(work + q.inv) = inv;
 }
 
 // x as a high and a low fp16 part.
@@ -153,12 +159,14 @@ __device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
 template <bool BF16, bool MUON>
 __global__ __launch_bounds__(kThreads) void mat_spread_kernel(const MuonMat* __restrict__ mats,
                                                               const MatJob* __restrict__ jobs, const void* grad,
-                                                              const float* mom, char* work, MuonK k) {
+                                                              const float* mom, char* work, MuonK k, bool own_scale,
+                                                              double eps) {
   constexpr int T = kMatSpread;
   __shared__ float tile[T][T + 1];   // [row of X][column of X]
+  __shared__ double red[kThreads / kWave];
   const MatJob job = jobs[blockIdx.x];
   const MuonMat& q = mats[job.mat];
-  const double inv = *reinterpret_cast<const double*>(work + q.inv);
+  const double inv = own_scale ? mat_scale(q, work, eps, red) : *reinterpret_cast<const double*>(work + q.inv);
   const int i0 = job.i * T, j0 = job.j * T;
   // the matrix's own rows r0.. and columns c0.. ; element (r, c) is X's (r, c) or (c, r)
   const int r0 = q.tall ? j0 : i0, c0 = q.tall ? i0 : j0;
@@ -199,20 +207,26 @@ __global__ __launch_bounds__(kThreads) void mat_spread_kernel(const MuonMat* __r
         else tile[r][c + t] = 0.0f;
       }
     }
-  } else {
-#pragma unroll 4
-    for (int e = threadIdx.x; e < T * T; e += kThreads) {
-      const int r = e / T, c = e % T;
+  } else {   // single elements; again a thread's loads first
+    constexpr int kIt = T * T / kThreads;
+    const int c = threadIdx.x % T;
+    float g[kIt], m[kIt];
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const int r = threadIdx.x / T + it * (kThreads / T);
+      g[it] = m[it] = 0.0f;
       if (r0 + r < q.rows && c0 + c < q.cols) {
         const int64_t at = q.start + static_cast<int64_t>(r0 + r) * q.cols + c0 + c;
-        float m = 0.0f;
-        if constexpr (MUON) m = mom[at];
-        put(r, c, load_elem(grad, at, BF16), m);
-      } else if (q.tall) {
-        tile[c][r] = 0.0f;
-      } else {
-        tile[r][c] = 0.0f;
+        g[it] = load_elem(grad, at, BF16);
+        if constexpr (MUON) m[it] = mom[at];
       }
+    }
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const int r = threadIdx.x / T + it * (kThreads / T);
+      if (r0 + r < q.rows && c0 + c < q.cols) put(r, c, g[it], m[it]);
+      else if (q.tall) tile[c][r] = 0.0f;
+      else tile[r][c] = 0.0f;
     }
   }
   __syncthreads();
@@ -1067,14 +1081,16 @@ int run_matrices(rs_plan* p, const void* grad, int32_t grad_dt, float* mom, cons
     hipLaunchKernelGGL((mat_norm_kernel<false, MUON>), chunks, dim3(kThreads), 0, s, p->mats, p->mat_chunks, grad, mom,
                        work, k);
   }
-  hipLaunchKernelGGL(mat_scale_kernel, dim3(static_cast<unsigned>(p->n_mats)), dim3(kThreads), 0, s, p->mats, work,
+  const bool own_scale = p->mat_own_scale;
+  if (!own_scale)
+    hipLaunchKernelGGL(mat_scale_kernel, dim3(static_cast<unsigned>(p->n_mats)), dim3(kThreads), 0, s, p->mats, work,
                      static_cast<double>(eps));
   if (grad_dt == RS_BF16) {
     hipLaunchKernelGGL((mat_spread_kernel<true, MUON>), spread, dim3(kThreads), 0, s, p->mats, p->mat_spread, grad,
-                       mom, work, k);
+                       mom, work, k, own_scale, static_cast<double>(eps));
   } else {
     hipLaunchKernelGGL((mat_spread_kernel<false, MUON>), spread, dim3(kThreads), 0, s, p->mats, p->mat_spread, grad,
-                       mom, work, k);
+                       mom, work, k, own_scale, static_cast<double>(eps));
   }
   auto polynomial = [&](int t) {
     k.a = coeffs[3 * t];

@@ -828,7 +828,11 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     p->n_tiny = static_cast<int64_t>(mt.tiny.size());
     p->n_mat_chunks = static_cast<int64_t>(mt.chunks.size());
     p->n_mat_spread = static_cast<int64_t>(mt.spread.size());
-    for (const MuonMat& q : mt.mats) p->mat_any_paired |= q.paired != 0;
+    p->mat_own_scale = true;
+    for (const MuonMat& q : mt.mats) {
+      p->mat_any_paired |= q.paired != 0;
+      p->mat_own_scale &= q.n_part <= kMatOwnParts;
+    }
     for (int w = 0; w < kMatLists; ++w) {
       p->n_mat_jobs[w] = static_cast<int64_t>(mt.list[w].jobs.size());
       p->n_mat_joins[w] = static_cast<int64_t>(mt.list[w].joins.size());

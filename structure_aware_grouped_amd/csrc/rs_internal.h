@@ -328,11 +328,14 @@ constexpr int mat_places(int side) { return side == 256 ? 256 : 512; }
 constexpr int kXcds = 8;
 constexpr int kMatMaxParts = 8;    // a tile's contraction is cut into at most this many parts
 constexpr int kMatMinSteps = 4;    // steps of kMatK in a part, at least
-constexpr int kMatJoinSteps = 16;  // joining parts costs about this many steps
+constexpr int kMatJoinSteps = 24;  // joining parts costs about this many steps
 // Matrices whose X is at most kMatTinyM x kMatTinyN run in one workgroup.
 constexpr int64_t kMatTinyM = 64, kMatTinyN = 256;
 // Elements per work item of the pass that updates momentum and sums squares.
 constexpr int64_t kMatChunk = 8192;
+// Up to this many partial sums of each matrix are added up by every workgroup
+// of the split; more by a launch of their own.
+constexpr int kMatOwnParts = 512;
 // Tile of the pass that splits the scaled matrix into its operands.
 constexpr int64_t kMatSpread = 64;
 constexpr int kMuonMaxSteps = 32;
@@ -484,6 +487,7 @@ struct rs_plan {
   int64_t n_mat_jobs[rs::kMatLists] = {}, n_mat_joins[rs::kMatLists] = {};
   int mat_side[rs::kMatLists] = {};
   bool mat_any_paired = false;
+  bool mat_own_scale = false;          // the split adds up the partial sums of squares itself
   int64_t n_mats = 0, n_mat_chunks = 0, n_mat_spread = 0;
   int64_t mat_work_bytes = 0, mat_slabs = 0;
   bool mat_too_large = false;

@@ -274,3 +274,58 @@ def test_calls_that_are_refused(gpu_lib):
     torch.cuda.synchronize()
     assert not out.any()
     plan.close()
+
+
+def _exact_on_device(g):
+    x = g.double()
+    x = x.T.contiguous() if x.shape[0] > x.shape[1] else x
+    x = x / (x.square().sum().sqrt() + 1e-7)
+    for a, b, c in (OM.COEFFS,) * 5:
+        s = torch.mm(x, x.T.contiguous())
+        x = a * x + torch.mm(b * s + c * torch.mm(s, s), x)
+    return x.T if g.shape[0] > g.shape[1] else x
+
+
+@pytest.mark.parametrize("shapes", [[(4100, 5300)], [(2050, 4100), (1031, 4097), (700, 300), (50, 60)], [(6001, 5900)],
+                                    [(3000, 1100)] * 5 + [(40, 3000)]])
+def test_the_plans_own_choice_at_larger_sizes(gpu_lib, shapes):
+    """256-wide tiles, cut tiles and joins, the first two steps together, single- and two-part
+    matrices and small ones in one group, against torch's products in 64 bits."""
+    import structure_aware_grouped_amd as rs
+    torch.manual_seed(18)
+    plan = _load(rs, [TensorSpec(f"w{i}", r, c, "WHOLE") for i, (r, c) in enumerate(shapes)])
+    src = torch.full((plan.R_mat * plan.S,), float("nan"), device=DEV)
+    for (r, c), at in zip(shapes, plan.starts):
+        low = torch.randn(r, 8, device=DEV) @ torch.randn(8, c, device=DEV)
+        src[at:at + r * c] = (low + torch.randn(r, c, device=DEV)).reshape(-1) * 1e-3
+    out = torch.zeros(src.numel(), dtype=torch.bfloat16, device=DEV)
+    work = rs.rs_muon_workspace(plan)
+    work.fill_(0xFF)
+    rs.rs_orthogonalize(plan, src, out, work)
+    for (r, c), at in zip(shapes, plan.starts):
+        want = _exact_on_device(src[at:at + r * c].view(r, c))
+        got = out[at:at + r * c].view(r, c).double()
+        assert ((got - want).norm() / want.norm()).item() <= math.hypot(tol(5), 2.0 ** -8), (r, c)
+    plan.close()
+
+
+def test_two_calls_at_once_with_a_workspace_each(gpu_lib):
+    import structure_aware_grouped_amd as rs
+    rng = np.random.default_rng(19)
+    specs = [TensorSpec("a", 700, 900, "WHOLE"), TensorSpec("b", 100, 50, "WHOLE")]
+    plan = _load(rs, specs)
+    srcs = [_flat(plan, [_gaussian(rng, sp.rows, sp.cols) for sp in specs], fill=0.0) for _ in range(2)]
+    want = [torch.zeros(s.numel(), dtype=torch.bfloat16, device=DEV) for s in srcs]
+    works = [rs.rs_muon_workspace(plan) for _ in srcs]
+    for s, o in zip(srcs, want):
+        rs.rs_orthogonalize(plan, s, o, works[0])
+    torch.cuda.synchronize()
+    got = [torch.zeros_like(o) for o in want]
+    streams = [torch.cuda.Stream() for _ in srcs]
+    for _ in range(5):
+        for s, o, w, st in zip(srcs, got, works, streams):
+            with torch.cuda.stream(st):
+                rs.rs_orthogonalize(plan, s, o, w)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    plan.close()
