@@ -5,14 +5,15 @@
 // work items. Everything here is in an anonymous namespace: each kernel file
 // gets its own copy.
 //
-// Every kernel is HBM-bound streaming work over plan-indexed work lists made
-// once by rs_plan_load, with 16-byte vector loads (nontemporal) and stores
-// (nontemporal, or with nt and sc1 set where that measured faster). The
-// streaming transforms split each work item over small, short-lived
-// workgroups (64-128 threads, one or two vectors each), which keep more
-// independent streams in flight on gfx950 than one large workgroup per item;
-// piece_index can keep runs of consecutive pieces on one XCD. No MFMA: nothing
-// here is a dense contraction.
+// The transforms, quantisers and Adam steps are HBM-bound streaming work over
+// plan-indexed work lists made once by rs_plan_load, with 16-byte vector loads
+// (nontemporal) and stores (nontemporal, or with nt and sc1 set where that
+// measured faster). The streaming transforms split each work item over small,
+// short-lived workgroups (64-128 threads, one or two vectors each), which keep
+// more independent streams in flight on gfx950 than one large workgroup per
+// item; piece_index can keep runs of consecutive pieces on one XCD. None of
+// them is a dense contraction; the matrix operators' products are, and have
+// matrix-core kernels of their own.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -50,6 +50,9 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) 
 
 constexpr int kLookVecs = 4;   // vectors (or elements) per thread
 
+// Bound by memory: 16384 tokens of 8192 bf16 columns take 91 us, 5.9 TB/s with
+// every token's row counted, as a copy does, whatever the vectors a thread
+// (2, 4 and 8 alike, one 104 us), the cache policy or the XCD order.
 // Work is numbered over tokens * units of a row: a unit is 8 elements (VEC),
 // or one element where the width is no multiple of 8. 32-bit arithmetic after
 // the workgroup's own first token.

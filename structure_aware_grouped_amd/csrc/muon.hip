@@ -31,10 +31,19 @@
 // worst of them, and the published polynomial's slope reaches 1.6: for
 // m <= kMatTwoPart all operands have a high and a low part, and a product is
 // high * low + low * high + high * high.
-// On simulated matrices of 48 to 2048 rows with one part, with spectra flat, falling by 10^4
-// or of a few directions 100 times above the others, the relative error of
-// the result against 64 bits is 2e-4 to 1.4e-3; plain fp16 operands give 1e-3
-// to 4e-2, bf16 ones 1e-2 and more.
+// On matrices of 100 to 2048 rows with one part, with spectra flat, falling by
+// 10^4 or of a few directions 100 times above the others, the relative error
+// of the result against 64 bits is 2e-4 to 1.2e-3 (computed with the same
+// roundings on the CPU); plain fp16 operands give 1e-3 to 4e-2, bf16 ones 1e-2
+// and more.
+//
+// What bounds it. The products: with 256-wide tiles the matrix cores are busy
+// 63 to 75% of the time at the 1.66 GHz that the card holds under them
+// (8192 x 28672: polynomial times X 3.54 ms, 1087 TFLOP/s, X X^T 1185; a
+// library fp16 product of that size reaches 1373). Small matrices: the latency
+// of about 17 launches. The passes around the products move bytes: momentum
+// and norm 5.8 TB/s, the split into operands 5.1 TB/s on the Llama-3-8B layer's
+// 218 M elements, 7% of its 14.5 ms.
 #include "host_common.h"
 
 namespace rs {
@@ -284,8 +293,8 @@ enum Product {
 // X X^T and S X, the long products, are needed once. The rounding of A reaches
 // further than in a single step: it is raised by a^2, so this is done only for
 // |a| <= kPairMaxA and for the first two steps, where the singular values are
-// small (simulated: the same error as single steps; the third and fourth as
-// one gave 2 to 5 times the error).
+// small (the same error as single steps; the third and fourth as one gave 2 to
+// 5 times the error). 8192 x 28672: 29.2 -> 25.9 ms a step.
 enum PairPart { kPairT = 0, kPairA1 = 1, kPairS = 2 };
 constexpr float kPairMaxA = 4.0f;
 
@@ -324,8 +333,11 @@ __device__ __forceinline__ Where where(const MuonMat& m, int turn, int pair) {
 // next 16 columns is read while the current one is multiplied; the stage turns
 // over (wait, barrier, new loads) before the last multiplication of a stage.
 //   256: 64 KiB a stage, one workgroup per CU; what large products take. 128
-// and 64: two and two workgroups per CU, for products of few tiles; 64 keeps
-// three stages on their way, since few workgroups wait for memory.
+// and 64: two workgroups per CU, for products of few tiles; 64 keeps three
+// stages on their way, since few workgroups wait for memory. Whole calls, 64 /
+// 128 / 256 wide: 1024 x 4096 266 / 323 / 543 us, 4096 x 4096 2.25 / 1.62 /
+// 1.86 ms, 4096 x 14336 6.67 / 4.56 / 4.81 ms (4.37 with the rule: 128 for the
+// m x m products, 256 for the m x n ones).
 template <int BM>
 struct Tile {
   static constexpr int kNT = BM == 256 ? 512 : 256;
@@ -866,7 +878,7 @@ __global__ __launch_bounds__(Tile<BM>::WC * kWave) void mat_join_kernel(const Mu
 
 // Matrices of at most 64 x 256 (X's sides), one workgroup each, whole call in
 // one launch: what a step of three launches waits for is latency, and X fits
-// LDS. Every wave holds its part of X in fp32 registers, as the 16 x 16 blocks
+// LDS (64 x 48: 25 us, 104 us by launches). Every wave holds its part of X in fp32 registers, as the 16 x 16 blocks
 // that v_mfma_f32_16x16x32_f16 gives; LDS holds the operands, high and low
 // parts of X, X^T and of A or the polynomial. Products are high * low +
 // low * high + high * high, and the polynomial's whole diagonal stays in fp32.
