@@ -428,7 +428,8 @@ def rs_embed_grad(plan: Plan, tensor: int, ids: torch.Tensor, dy: torch.Tensor, 
     n = _table(plan, tensor, ids, dy, "dy")
     _dev_check(plan, ids, dy, packed, work, prev)
     _flat_check(plan, packed, (torch.float32, torch.bfloat16), "packed")
-    _work_check(work, _embed_bytes(plan, tensor, n))
+    if work.dtype != torch.uint8:      # its size is checked by the call itself
+        raise ValueError("work: uint8")
     apart = {"ids": ids, "dy": dy, "packed": packed, "work": work}
     if prev is not None:
         _flat_check(plan, prev, (torch.float32,), "prev")
@@ -469,10 +470,16 @@ def _flat_check(plan: Plan, t: torch.Tensor, dtypes, what: str):
 
 def _apart_check(**tensors: torch.Tensor):
     """The named buffers share no byte: the kernels read some while they write others."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), k) for k, t in tensors.items())
-    for (_, end, a), (start, stop, b) in zip(spans, spans[1:]):
-        if start < end and start < stop:
-            raise ValueError(f"{a} and {b} overlap")
+    spans = []
+    for name, t in tensors.items():
+        size = t.nbytes
+        if size:
+            at = t.data_ptr()
+            spans.append((at, at + size, name))
+    spans.sort()
+    for k in range(1, len(spans)):
+        if spans[k][0] < spans[k - 1][1]:
+            raise ValueError(f"{spans[k - 1][2]} and {spans[k][2]} overlap")
 
 
 def _work_check(work: torch.Tensor, need: int):

@@ -32,7 +32,6 @@ def test_null_plans(monkeypatch):
 def test_binding_refuses_bad_buffers(monkeypatch):
     from structure_aware_grouped_amd import binding
     monkeypatch.setattr(binding, "_dev_check", lambda plan, *t: None)
-    monkeypatch.setattr(binding, "_embed_bytes", lambda plan, tensor, n: 100)
     plan = binding.Plan.__new__(binding.Plan)
     plan._h, plan.numels, plan.device, plan.R_mat, plan.S, plan.n_qblocks = None, [64], 0, 1, 64, 0
     plan.specs, plan.starts, plan.V = [TensorSpec("w", 8, 8, "ROWS", 1)], [0], 1
@@ -46,7 +45,7 @@ def test_binding_refuses_bad_buffers(monkeypatch):
            lambda: binding.rs_embed_rows(plan, 0, flat[:60], ids, rows),
            lambda: binding.rs_embed_rows(plan, 0, flat.double(), ids, rows),
            lambda: binding.rs_embed_rows(plan, 0, flat, ids, flat[:24]),
-           lambda: binding.rs_embed_grad(plan, 0, ids, rows, flat, w[:99]),
+           lambda: binding.rs_embed_grad(plan, 0, ids, rows, flat, w.float()),
            lambda: binding.rs_embed_grad(plan, 0, ids, rows, flat.double(), w),
            lambda: binding.rs_embed_grad(plan, 0, ids, rows.int(), flat, w),
            lambda: binding.rs_embed_grad(plan, 0, ids, flat[:24], flat, w),
