@@ -103,7 +103,8 @@ __global__ __launch_bounds__(kThreads) void embed_rows_kernel(const void* table,
 // pass that looks for tokens of every row (131072 x 4096, 16384 tokens: 370 us
 // instead of 554). The fill runs as the tail of the grids of the sort (a
 // sixteenth) and of the chunk sums, which are short of workgroups and wait for
-// memory (the merge's 64 KiB of LDS would leave room for few fill blocks). One 16-byte nt-sc1 store a thread in workgroups of 256
+// memory (the merge's 64 KiB of LDS would leave room for few fill blocks). One
+// 16-byte nt-sc1 store a thread in workgroups of 256
 // filled 2 GiB at 7.16 TB/s, four a thread at 6.07, 64 threads at 4.82.
 struct Fill {
   const float* prev;
