@@ -6,8 +6,8 @@
 // order by the places that run at once, end together.
 //
 // Reads "n" and n lines "rows cols" (WHOLE tensors) on stdin; prints "ok" and
-// per product the tile side, tiles, cut tiles, jobs and the end over the mean
-// share, or the first violation. With an argument 1-4 it
+// per product the tile side, tiles, cut tiles, jobs, the end over the mean
+// share and how many steps it is behind it, or the first violation. With an argument 1-4 it
 // first plants a mistake (a job dropped, a step doubled, a slab shared, two
 // operands overlapping), which must be reported. Includes plan.cpp for
 // lower_muon(); link with planner.cpp.
@@ -45,8 +45,9 @@ int main(int argc, char** argv) {
   if (plant == 1) mt.list[0].jobs.pop_back();
   if (plant == 2) mt.list[2].jobs[0].k1 += 1;
   if (plant == 3)
-    for (auto& j : mt.list[1].jobs)
-      if (j.parts > 1) j.slab = mt.list[1].joins[0].slab;
+    for (auto& l : mt.list)
+      for (auto& j : l.jobs)
+        if (j.parts > 1) j.slab = l.joins[0].slab;
   if (plant == 4) mt.mats[0].xl = mt.mats[0].xh;
 
   std::map<int32_t, int64_t> chunks;
@@ -133,8 +134,9 @@ int main(int argc, char** argv) {
     }
     if (joins.size() != cut) return bad("joins");
     char line[200];
-    std::snprintf(line, sizeof line, " [%d tiles of %d, %zu cut, %zu jobs, share %.2f]", static_cast<int>(need), l.side, cut,
-                  l.jobs.size(), total ? *std::max_element(share.begin(), share.end()) / (total / share.size()) : 1.0);
+    std::snprintf(line, sizeof line, " [%d tiles of %d, %zu cut, %zu jobs, share %.2f, behind %.1f]", static_cast<int>(need), l.side, cut,
+                  l.jobs.size(), total ? *std::max_element(share.begin(), share.end()) / (total / share.size()) : 1.0,
+                  *std::max_element(share.begin(), share.end()) - total / share.size());
     text += line;
   }
   std::printf("ok%s\n", text.c_str());

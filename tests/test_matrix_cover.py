@@ -60,10 +60,15 @@ def test_random_groups(exe, seed):
 
 
 def test_large_products_are_shared_evenly(exe):
-    """With at least as many tiles as workgroups the last one ends at most a tenth behind the mean."""
+    """With at least as many tiles as workgroups the last one ends at most a tenth behind the mean,
+    or less than 25 steps: cut tiles need a second launch, so they are cut only where that saves more
+    than 24 steps (kMatJoinSteps) over the mean, which is rounded up to whole steps. So 700 tiles of
+    64 steps on 256 workgroups, which end after 3 * 64 = 192 steps, 17 behind the mean, stay whole."""
     for shapes in (LAYER, [(8192, 28672)], [(5760, 2880), (2880, 2880)] * 8):
-        for share in re.findall(r"share ([0-9.]+)", _run(exe, shapes, tile=256)):
-            assert float(share) <= 1.1, (shapes, share)
+        found = re.findall(r"share ([0-9.]+), behind ([0-9.]+)", _run(exe, shapes, tile=256))
+        assert found
+        for share, behind in found:
+            assert float(share) <= 1.1 or float(behind) < 25, (shapes, share, behind)
 
 
 @pytest.mark.parametrize("plant", [1, 2, 3, 4])
