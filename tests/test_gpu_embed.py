@@ -166,6 +166,28 @@ def test_sums_of_whole_numbers_are_exact_over_many_runs(gpu_lib):
     plan.close()
 
 
+@pytest.mark.parametrize("packed_dt,with_prev", [("f32", False), ("f32", True), ("bf16", False), ("bf16", True)])
+def test_a_large_table_is_filled_to_both_ends(gpu_lib, packed_dt, with_prev):
+    """More rows without a token than the sort's launch fills (96 MiB): the rest is the chunk sums'
+    launch's. Whole numbers: sums, prev and the bf16 results (below 256) are exact."""
+    import structure_aware_grouped_amd as rs
+    rows, cols, n = 12007, 4501, 300
+    plan = _group(rs, rows, cols)
+    at, total = plan.starts[1], plan.R_mat * plan.S
+    ids = torch.randint(0, 40, (n,), device=DEV) * 300
+    ids[:2] = torch.tensor([0, rows - 1], device=DEV)
+    dy = torch.randint(-1, 2, (n, cols), device=DEV).float()
+    packed = torch.full((total,), float("nan"), dtype=DT[packed_dt], device=DEV)
+    prev = torch.randint(-3, 4, (total,), device=DEV).float() if with_prev else None
+    rs.rs_embed_grad(plan, 1, ids, dy, packed, rs.rs_embed_workspace(plan, 1, n), prev=prev)
+    want = torch.zeros(rows, cols, device=DEV) if prev is None else prev[at:at + rows * cols].view(rows, cols).clone()
+    want.index_add_(0, ids, dy)
+    assert want.abs().max().item() < 256
+    assert torch.equal(packed[at:at + rows * cols].float().view(rows, cols), want)
+    assert bool(torch.isnan(packed[:at]).all()) and bool(torch.isnan(packed[at + rows * cols:]).all())
+    plan.close()
+
+
 def test_same_call_same_bits_and_no_read_of_padding_tokens(gpu_lib):
     import structure_aware_grouped_amd as rs
     plan = _group(rs, 200, 100)
