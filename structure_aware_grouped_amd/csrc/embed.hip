@@ -105,12 +105,12 @@ __global__ __launch_bounds__(kThreads) void embed_rows_kernel(const void* table,
 // instead of 554). The fill runs as the tail of the grids of the sort and of
 // the chunk sums, which are short of workgroups and wait for memory (the
 // merge's 64 KiB of LDS would leave room for few fill blocks). The sort takes
-// kSortFill bytes of it, about what is moved while the runs are sorted: a
-// 32001 x 1001 bf16 table with 4097 tokens took 43 us with a sixteenth of the
-// fill there and 38.5 with 64 or 96 MiB; 131072 x 4096 took 375 us with 32,
-// 371 with 64, 368 with 96 and 369 with a sixteenth (128). One 16-byte nt-sc1
-// store a thread in workgroups of 256 filled 2 GiB at 7.16 TB/s, four a thread
-// at 6.07, 64 threads at 4.82.
+// kSortFill bytes of it or a sixteenth, about what is moved while the runs are
+// sorted: a 32001 x 1001 bf16 table with 4097 tokens took 43 us with the
+// sixteenth and 38.5 with 64 or 96 MiB; 131072 x 4096 took 375 us with 32 MiB,
+// 371 with 64, 368 with 96 and 369 with the sixteenth (128). One 16-byte
+// nt-sc1 store a thread in workgroups of 256 filled 2 GiB at 7.16 TB/s, four a
+// thread at 6.07, 64 threads at 4.82.
 constexpr int64_t kSortFill = int64_t(96) << 20;
 struct Fill {
   const float* prev;
@@ -623,7 +623,9 @@ void launch_grad(const Tensor& t, const GradCall& c, hipStream_t s) {
     return f;
   };
   unsigned extra = 0;
-  Fill f = share(std::min(fill, kSortFill / ((c.out16 ? 2 : 4) + (c.prev ? 4 : 0))), kSortThreads, &extra);
+  // at least a sixteenth: the chunk sums' launch then stays under 2^32 work-items
+  const int64_t early = std::max(kSortFill / ((c.out16 ? 2 : 4) + (c.prev ? 4 : 0)), fill / 16 / 16 * 16);
+  Fill f = share(std::min(fill, early), kSortThreads, &extra);
   // digits that tell the rows apart from each other and from kNoRow, whose low
   // digits are all ones
   int passes = 1;
