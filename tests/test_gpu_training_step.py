@@ -4,6 +4,10 @@ gradients packed (the table's by rs_embed_grad beside its dense one from the
 tied output, the others' by rs_pack_scatter), the Muon step on the matrices and
 the 8-bit AdamW step on the rest. Against the same steps in plain torch and the
 oracles; and every quantisation block, matrix and table keeps its own values."""
+import os
+import re
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -90,3 +94,24 @@ def test_embedding_network_and_optimiser_steps(gpu_lib):
         # steps that stay finite whatever AdamW did to the small values
         param.nan_to_num_(0.0).clamp_(-2.0, 2.0)
     plan.close()
+
+
+def test_the_readme_example_of_these_calls_runs(gpu_lib):
+    import structure_aware_grouped_amd as rs
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    block = re.search(r"same flat buffers \(imports as above\):\n\n((?:    .*\n|\n)+)", text).group(1)
+    env = {"torch": torch, "rs": rs, "TensorSpec": TensorSpec}
+    exec(compile(textwrap.dedent(block), "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    (t, w), S = env["starts"], env["S"]
+    table = env["gathered"][t:t + 32000 * 4096].view(32000, 4096)
+    assert torch.equal(env["x"], table[env["ids"]] * 64)      # a power of two
+    want = torch.zeros(32000, 4096, device=DEV).index_add_(0, env["ids"], env["x"].float())
+    count = torch.zeros(32000, device=DEV).index_add_(0, env["ids"], torch.ones(2048, device=DEV))
+    got = env["packed"][t:t + 32000 * 4096].view(32000, 4096) / 64
+    # equal tokens have equal rows here: k - 1 roundings on either side of a sum of one sign
+    assert bool(((got - want).abs() <= 2 * count[:, None] * 2.0 ** -24 * want.abs()).all())
+    inside = torch.zeros(8 * S, dtype=torch.bool, device=DEV)
+    inside[w:w + 4096 * 4096] = True
+    assert torch.equal(env["momentum"], torch.where(inside, env["grads"], 0.0))   # 0.95 * 0 + g
+    assert bool(torch.isfinite(env["params"]).all())
