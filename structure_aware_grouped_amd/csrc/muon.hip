@@ -836,17 +836,18 @@ __global__ __launch_bounds__(Tile<BM>::kNT) void mat_product_kernel(const MuonMa
   const char* q_lo = work + (WHAT == P_GRAM ? q.xl : WHAT == P_POLY ? q.al : q.xtl[at.turn]);
   const bool two = q.two_part;
   Acc<BM> acc = {};
-  for (int part = two ? 0 : 2; part < 3; ++part) {   // high * low, low * high, high * high
-    if (two && part == 2) {
+  auto multiply = [&](const char* x, const char* y) {
+    Multiply<BM>::run(reinterpret_cast<const _Float16*>(x), reinterpret_cast<const _Float16*>(y), ld, job.i * BM, q.m,
+                      job.j * BM, St::kSym ? q.m : q.n, job.k0, job.k1, lds, acc);
+  };
+  if (two) {   // high * low + low * high, ahead of high * high
+    for (int part = 0; part < 2; ++part) multiply(part ? p_lo : p_hi, part ? q_hi : q_lo);
 #pragma unroll
-      for (int i = 0; i < T::NI; ++i)
+    for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-        for (int j = 0; j < T::NJ; ++j) acc.v[i][j] *= 1.0f / kLowScale;
-    }
-    Multiply<BM>::run(reinterpret_cast<const _Float16*>(part == 1 ? p_lo : p_hi),
-                      reinterpret_cast<const _Float16*>(part == 0 ? q_lo : q_hi), ld, job.i * BM, q.m, job.j * BM,
-                      St::kSym ? q.m : q.n, job.k0, job.k1, lds, acc);
+      for (int j = 0; j < T::NJ; ++j) acc.v[i][j] *= 1.0f / kLowScale;
   }
+  multiply(p_hi, q_hi);
   if (job.parts > 1) {
     Slab<BM>::store(acc, work + slabs, job.slab);
     return;
