@@ -882,12 +882,12 @@ __global__ __launch_bounds__(Tile<BM>::WC * kWave) void mat_join_kernel(const Mu
 
 // Matrices of at most 64 x 256 (X's sides), one workgroup each, whole call in
 // one launch: what a step of three launches waits for is latency, and X fits
-// LDS (64 x 48: 25 us, 104 us by launches). Every wave holds its part of X in fp32 registers, as the 16 x 16 blocks
-// that v_mfma_f32_16x16x32_f16 gives; LDS holds the operands, high and low
-// parts of X, X^T and of A or the polynomial. Products are high * low +
-// low * high + high * high, and the polynomial's whole diagonal stays in fp32.
-// Rows in LDS are 16 bytes longer than their contents, so that the rows of a
-// fragment start in different banks.
+// LDS (64 x 48: 25 us, 104 us by launches). Every wave holds its part of X in
+// fp32 registers, as the 16 x 16 blocks that v_mfma_f32_16x16x32_f16 gives; LDS
+// holds the operands, high and low parts of X, X^T and of A or the polynomial.
+// Products are high * low + low * high + high * high, and the polynomial's
+// whole diagonal stays in fp32. Rows in LDS are 16 bytes longer than their
+// contents, so that the rows of a fragment start in different banks.
 constexpr int kTinyThreads = 512, kTinyWaves = kTinyThreads / kWave;
 constexpr int kTinyM = static_cast<int>(kMatTinyM), kTinyN = static_cast<int>(kMatTinyN);
 constexpr int kTinyBlocks = (kTinyM / 16) * (kTinyN / 16) / kTinyWaves;   // of X, per wave
