@@ -13,6 +13,7 @@
  * Calls (all extern "C", all return rs_status unless noted):
  *   rs_plan_build       host planner: S and the starts s_i
  *   rs_plan_load        validate a plan and lower it to device work lists
+ *   rs_plan_load_with   the same, with options
  *   rs_plan_info / rs_plan_free
  *   rs_unpack_gathered  gathered flat buffer -> N full tensors
  *   rs_pack_scatter     N full gradients -> flat buffer, fused scale/add/zero
@@ -174,12 +175,26 @@ int rs_plan_build(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t ali
  * direct per-lane kernels instead of staging it through LDS. Both give
  * identical results. RS_MUON_TILE=64|128|256 forces the output tile of the
  * matrix products (rs_orthogonalize, rs_muon_step), small matrices included;
- * RS_MUON_PAIRS=1 runs their first two steps together for every matrix with
- * more than 64 rows and columns.
+ * RS_MUON_PAIRS=1 runs their first two steps together for every matrix whose
+ * operands have one part (more than 64 rows and columns).
  * On success *out owns host memory and one device allocation, released by
  * rs_plan_free. Errors: the above, RS_ENOMEM, RS_EHIP. */
 int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,
                  const int64_t* starts, int64_t R_mat, int32_t device, rs_plan** out);
+
+/* What a plan's calls do that its tensors do not say; all zero is what
+ * rs_plan_load takes. */
+typedef struct rs_plan_options {
+  int32_t muon_parts;   /* fp16 parts of the operands of rs_orthogonalize and rs_muon_step: 1 (or
+                         * 0), or 2 for every matrix, for results as near as fp32 products' */
+  int32_t reserved[7];  /* must be 0 */
+} rs_plan_options;
+
+/* rs_plan_load with options (NULL: none). Errors: as there, and RS_EINVAL for
+ * an option outside its values. */
+int rs_plan_load_with(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,
+                      const int64_t* starts, int64_t R_mat, int32_t device,
+                      const rs_plan_options* options, rs_plan** out);
 
 /* Plan facts; any output pointer may be NULL. n_qblocks is the number of
  * quantisation blocks, i.e. the length of rs_block_quant's scale array:
@@ -400,7 +415,11 @@ int rs_embed_workspace(const rs_plan* plan, int64_t tensor, int64_t n_ids, int64
  * keeps the result within about 1e-3 of the exact one (Frobenius norm), ahead
  * of the bf16 rounding, for polynomials of slopes up to about 2 between 0.3
  * and 1.2, such as the published quintic; steeper ones raise each step's
- * rounding by their slope. Where that costs less, the first two polynomials
+ * rounding by their slope. Matrices of at most 64 rows or columns, and every
+ * matrix of a plan loaded with muon_parts = 2, have all operands in two parts,
+ * which keeps the result as near as fp32 products do (5e-7; 1.5e-5 where
+ * directions are 100 times weaker than others) at 1.4 to 2.9 times the time.
+ * With one part, where that costs less, the first two polynomials
  * (|a| <= 4) are multiplied with each other and applied to X once. The
  * polynomials must keep every singular value below
  * 7 (A is held to 2^16 / 2^10) and the off-diagonal entries of b A + c A^2

@@ -25,7 +25,7 @@ KINDS = {"ELEM": 0, "ROWS": 1, "TILE": 2, "FLAT": 3, "WHOLE": 4, "TILEMAJOR": 5}
 ORDER_KINDS = {0: "default", 1: "by_block_size", 2: "by_shape"}
 RS_F32, RS_BF16, RS_E4M3, RS_I8, RS_U8 = 0, 1, 2, 3, 4
 CODE_FORMATS = {"e4m3": RS_E4M3, "i8": RS_I8, "u8": RS_U8}
-EXPORTS = ("rs_plan_build", "rs_plan_load", "rs_plan_info", "rs_plan_free", "rs_unpack_gathered",
+EXPORTS = ("rs_plan_build", "rs_plan_load", "rs_plan_load_with", "rs_plan_info", "rs_plan_free", "rs_unpack_gathered",
            "rs_pack_scatter", "rs_block_quant", "rs_block_dequant", "rs_unpack_dequant", "rs_adam8_step",
            "rs_last_error", "rs_block_quant_noalloc", "rs_orthogonalize", "rs_muon_step", "rs_muon_workspace",
            "rs_embed_rows", "rs_embed_grad", "rs_embed_workspace")
@@ -47,6 +47,10 @@ class MuonHParamsC(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("eps", ctypes.c_float), ("steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
                 ("scale_mode", ctypes.c_int32)]
+
+
+class PlanOptionsC(ctypes.Structure):
+    _fields_ = [("muon_parts", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7)]
 
 
 class TensorSpecC(ctypes.Structure):
@@ -72,6 +76,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rs_plan_build.argtypes = [ctypes.POINTER(TensorSpecC), I64, I64, I64, I32, PI64, PI64, PI64, PI32]
     lib.rs_plan_load.argtypes = [ctypes.POINTER(TensorSpecC), I64, I64, I64, PI64, I64, I32,
                                  ctypes.POINTER(P)]
+    lib.rs_plan_load_with.argtypes = [ctypes.POINTER(TensorSpecC), I64, I64, I64, PI64, I64, I32,
+                                      ctypes.POINTER(PlanOptionsC), ctypes.POINTER(P)]
     lib.rs_plan_info.argtypes = [P, PI64, PI64, PI64]
     lib.rs_plan_free.argtypes = [P]
     lib.rs_plan_free.restype = None
@@ -236,14 +242,18 @@ class Plan:
 
 
 def rs_plan_load(specs, V: int, S: int, starts: Sequence[int], R_mat: Optional[int] = None,
-                 device: int = 0) -> Plan:
+                 device: int = 0, muon_parts: int = 1) -> Plan:
+    """Validate a plan and build its work lists on `device`. muon_parts: fp16 parts of the operands
+    of rs_orthogonalize and rs_muon_step; 2 brings their results as near as fp32 products', at
+    1.4 to 2.9 times the time and up to 1.7 times the workspace."""
     lib = load()
     n = len(specs)
     if R_mat is None:
         R_mat = V
     h = ctypes.c_void_p()
-    _check(lib.rs_plan_load(specs_array(specs), n, int(V), int(S), _i64(starts), int(R_mat),
-                            int(device), ctypes.byref(h)))
+    options = PlanOptionsC(muon_parts=int(muon_parts))
+    _check(lib.rs_plan_load_with(specs_array(specs), n, int(V), int(S), _i64(starts), int(R_mat),
+                                 int(device), ctypes.byref(options), ctypes.byref(h)))
     return Plan(h, specs, int(V), int(S), starts, int(R_mat), int(device))
 
 

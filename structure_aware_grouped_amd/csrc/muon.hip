@@ -29,16 +29,18 @@
 //   - the diagonal of A in fp32, zeros in its place in the fp16 operand.
 // A matrix of few rows has few singular values, so its error is that of the
 // worst of them, and the published polynomial's slope reaches 1.6: for
-// m <= kMatTwoPart all operands have a high and a low part, and a product is
+// m <= kMatTwoPart, and for every matrix of a plan loaded with muon_parts = 2,
+// all operands have a high and a low part, and a product is
 // high * low + low * high + high * high.
 // On matrices of 100 to 2048 rows with one part, with spectra flat, falling by
 // 10^4 or of a few directions 100 times above the others, the relative error
 // of the result against 64 bits is 2e-4 to 1.2e-3 (computed with the same
 // roundings on the CPU); plain fp16 operands give 1e-3 to 4e-2, bf16 ones 1e-2
 // and more. Two parts for every matrix give 4e-7 to 1.2e-6 on the card (one:
-// 2.3e-4 to 9.6e-4) at 1.4 (100 x 110) to 2.9 (4096 x 14336) times the time;
-// the error of one is below the bf16 rounding of rs_orthogonalize's result,
-// and in rs_muon_step it comes times the rate.
+// 2.3e-4 to 9.6e-4), 1.4e-5 where most directions are 100 times weaker than a
+// few (fp32 products give 2.8e-5 there), at 1.4 (100 x 110) to 2.9
+// (4096 x 14336: 4.0 -> 11.8 ms) times the time, so one is the default: its error is below the bf16 rounding of
+// rs_orthogonalize's result, and in rs_muon_step it comes times the rate.
 //
 // What bounds it. The products: with 256-wide tiles the matrix cores are busy
 // 63 to 75% of the time at the 1.66 GHz that the card holds under them
@@ -166,8 +168,8 @@ __device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
 }
 
 // One 64 x 64 tile of X from the gradient (and momentum): scaled, split, and
-// written as X's high and low parts and the transposed high part (for
-// m <= kMatTwoPart the low one too), zeros in the padding of the contraction dimensions.
+// written as X's high and low parts and the transposed high part (with two
+// parts the low one too), zeros in the padding of the contraction dimensions.
 template <bool BF16, bool MUON>
 __global__ __launch_bounds__(kThreads) void mat_spread_kernel(const MuonMat* __restrict__ mats,
                                                               const MatJob* __restrict__ jobs, const void* grad,

@@ -651,7 +651,8 @@ void lower_product(const std::vector<MuonMat>& mats, int list, ProductList* out)
 
 // The whole matrices of a plan: where their operands lie in the workspace and
 // the work lists of the passes over them (rs_orthogonalize, rs_muon_step).
-void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
+// parts: 2 for two parts of every matrix's operands.
+void lower_muon(const std::vector<Tensor>& t, MuonTables* mt, int parts) {
   std::vector<const Tensor*> ms;
   int64_t tiles = 0;
   for (const Tensor& x : t) {
@@ -700,13 +701,13 @@ void lower_muon(const std::vector<Tensor>& t, MuonTables* mt) {
     for (int64_t& o : q.xt) o = take(int64_t(2) * q.n * q.mp);
     q.a = take(int64_t(2) * q.m * q.mp);
     q.b = take(int64_t(2) * q.m * q.mp);
-    q.two_part = q.m <= kMatTwoPart;
+    q.two_part = parts == 2 || q.m <= kMatTwoPart;
     if (q.two_part) {
       for (int64_t& o : q.xtl) o = take(int64_t(2) * q.n * q.mp);
       q.al = take(int64_t(2) * q.m * q.mp);
       q.bl = take(int64_t(2) * q.m * q.mp);
     }
-    q.paired = mat_paired(q.m, q.n) || (forced_pairs() && !q.two_part);
+    q.paired = !q.two_part && (mat_paired(q.m, q.n) || forced_pairs());
     if (q.paired) {
       q.c = take(int64_t(2) * q.m * q.mp);
       q.t = take(int64_t(2) * q.m * q.mp);
@@ -766,11 +767,21 @@ static int init_table(PtrTable* tab, void** dev, int64_t n) {
 
 extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,
                             const int64_t* starts, int64_t R_mat, int32_t device, rs_plan** out) {
+  return rs_plan_load_with(specs, n, V, S, starts, R_mat, device, nullptr, out);
+}
+
+extern "C" int rs_plan_load_with(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,
+                                 const int64_t* starts, int64_t R_mat, int32_t device,
+                                 const rs_plan_options* options, rs_plan** out) {
   try {
     clear_error();
     if (!out) return fail(RS_EINVAL, "rs_plan_load: null output");
     *out = nullptr;
     if (device < 0) return fail(RS_EINVAL, "rs_plan_load: bad device");
+    const rs_plan_options opt = options ? *options : rs_plan_options{};
+    if (opt.muon_parts < 0 || opt.muon_parts > 2) return fail(RS_EINVAL, "rs_plan_load: muon_parts is 1 or 2");
+    for (int32_t r : opt.reserved)
+      if (r != 0) return fail(RS_EINVAL, "rs_plan_load: reserved options must be 0");
     std::vector<Tensor> t;
     int64_t R_used = 0;
     int st = validate_plan("rs_plan_load", specs, n, V, S, starts, R_mat, &t, &R_used);
@@ -779,7 +790,7 @@ extern "C" int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, i
     Tables tb;
     lower(t, S, R_mat, &tb);
     MuonTables mt;
-    lower_muon(t, &mt);
+    lower_muon(t, &mt, opt.muon_parts);
     // Every launch loops over its work items beyond kMaxGrid workgroups; item
     // and piece indices are 32-bit. Under the 2^39-element limit this holds
     // for any plan but one made of tiny tiles.

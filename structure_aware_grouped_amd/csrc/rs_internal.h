@@ -306,7 +306,8 @@ static_assert(kGatherMaxRun / 4 < 65536, "a run of several rows keeps its vector
 // product is stored with its contraction dimension contiguous and padded with
 // zeros to kMatK elements, so a product's inner loop has no tail.
 constexpr int64_t kMatK = 64;
-// Matrices of at most this many rows of X have high and low parts throughout.
+// Matrices of at most this many rows of X have high and low parts throughout,
+// as every matrix of a plan loaded with two parts has.
 constexpr int64_t kMatTwoPart = 64;
 // The first two steps of a matrix with n >= 1.5 m are applied to X together:
 // with r = n / m, 3 r + 5 instead of 6 r + 2 products of m^3 (halves of
@@ -359,7 +360,7 @@ struct MuonMat {
   int32_t tall;       // rows > cols: X is the transpose
   int32_t ex;         // X is stored times 2^ex
   int32_t n_part;
-  int32_t two_part;   // m <= kMatTwoPart: every operand has a low part
+  int32_t two_part;   // every operand has a low part
   int32_t paired;     // the first two steps may be applied to X as one
   int32_t unused;
 };
@@ -410,7 +411,7 @@ struct MuonTables {
   int64_t slabs = 0;                 // in the workspace
   bool too_large = false;            // beyond the limits above: the matrix calls return RS_ERANGE
 };
-void lower_muon(const std::vector<Tensor>& t, MuonTables* mt);
+void lower_muon(const std::vector<Tensor>& t, MuonTables* mt, int parts = 1);
 
 // Device copy of a per-tensor pointer table plus the host state that decides
 // when it must be uploaded again.

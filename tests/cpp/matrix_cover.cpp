@@ -9,7 +9,8 @@
 // per product the tile side, tiles, cut tiles, jobs, the end over the mean
 // share and how many steps it is behind it, or the first violation. With an argument 1-4 it
 // first plants a mistake (a job dropped, a step doubled, a slab shared, two
-// operands overlapping), which must be reported. Includes plan.cpp for
+// operands overlapping), which must be reported. A second argument is the
+// operands' parts of every matrix (1 or 2). Includes plan.cpp for
 // lower_muon(); link with planner.cpp.
 #include "plan.cpp"
 
@@ -41,7 +42,7 @@ int main(int argc, char** argv) {
     t.push_back(x);
   }
   MuonTables mt;
-  lower_muon(t, &mt);
+  lower_muon(t, &mt, argc > 2 ? std::atoi(argv[2]) : 1);
   if (plant == 1) mt.list[0].jobs.pop_back();
   if (plant == 2) mt.list[2].jobs[0].k1 += 1;
   if (plant == 3)

@@ -1,0 +1,48 @@
+"""Two-part operands for every matrix (rs_plan_load_with's muon_parts): the
+options that are refused, and the work lists and workspace that they give
+(tests/cpp/matrix_cover.cpp)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from tests.test_matrix_cover import LAYER, exe  # noqa: F401  (a fixture)
+from workloads import TensorSpec
+
+
+def _load(rs, specs, options):
+    from structure_aware_grouped_amd import binding as b
+    S, starts, _, _ = rs.rs_plan_build(specs, 1)
+    h = ctypes.c_void_p(7)
+    status = b.load().rs_plan_load_with(b.specs_array(specs), 1, 1, S, b._i64(starts), 1, 0, options, ctypes.byref(h))
+    return status, h.value
+
+
+@pytest.mark.parametrize("parts", [-1, 3, 1 << 30])
+def test_other_numbers_of_parts_are_refused(parts):
+    import structure_aware_grouped_amd as rs
+    from structure_aware_grouped_amd import binding as b
+    specs = [TensorSpec("w", 128, 128, "WHOLE")]
+    assert _load(rs, specs, ctypes.byref(b.PlanOptionsC(muon_parts=parts))) == (b.RS_EINVAL, None)
+    assert "muon_parts" in b.load().rs_last_error().decode()
+
+
+def test_reserved_options_are_refused():
+    import structure_aware_grouped_amd as rs
+    from structure_aware_grouped_amd import binding as b
+    for k in range(7):
+        options = b.PlanOptionsC()
+        options.reserved[k] = 1
+        assert _load(rs, [TensorSpec("w", 128, 128, "WHOLE")], ctypes.byref(options)) == (b.RS_EINVAL, None)
+
+
+@pytest.mark.parametrize("tile", [None, "64", "128", "256"])
+@pytest.mark.parametrize("shapes", [[(65, 65)], [(1024, 4096)], [(128, 2880), (333, 1001), (40, 900)], LAYER,
+                                    [(5760, 2880), (2880, 2880)] * 8])
+def test_every_step_once_with_two_parts(exe, shapes, tile, monkeypatch):  # noqa: F811
+    monkeypatch.setenv("RS_MUON_TILE", tile or "")
+    monkeypatch.setenv("RS_MUON_PAIRS", "1")       # two-part matrices have no paired steps, asked for or not
+    text = f"{len(shapes)}\n" + "".join(f"{r} {c}\n" for r, c in shapes)
+    r = subprocess.run([exe, "0", "2"], input=text, capture_output=True, text=True, timeout=120, env=dict(os.environ))
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
