@@ -367,8 +367,8 @@ int rs_adam8_step(rs_plan* plan, float* param, const float* grad, void* q_m, flo
  * n_ids signed integers of id_bytes (4 or 8) bytes. scale: finite. out:
  * device, n_ids x cols row-major of out_dt (RS_F32 or RS_BF16), overlapping
  * neither input. gathered and out 16-byte aligned. n_ids may be 0.
- * Limits (RS_ERANGE): rows under 2^27, rows * cols at most 2^34, n_ids under
- * 2^26, n_ids * cols at most 2^33.
+ * Limits (RS_ERANGE): rows at most 2^27 - 8, cols under 2^31, rows * cols at
+ * most 2^34, n_ids under 2^26, n_ids * cols at most 2^33.
  * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
 int rs_embed_rows(rs_plan* plan, int64_t tensor, const void* gathered, int32_t dt, const void* ids,
                   int32_t id_bytes, int64_t n_ids, float scale, void* out, int32_t out_dt, void* stream);

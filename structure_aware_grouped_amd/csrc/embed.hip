@@ -534,9 +534,12 @@ __global__ __launch_bounds__(kThreads) void embed_named_kernel(const uint32_t* _
 
 // ------------------------------------------------------------------ host
 
-// Limits that keep every launch under 2^32 work-items: 32 per row or token in
-// the gradient's passes, a quarter per element in the fill and the lookup.
-constexpr int64_t kEmbedMaxRows = int64_t(1) << 27, kEmbedMaxIds = int64_t(1) << 26;
+// Limits that keep every launch under 2^32 work-items: 32 per row (whole
+// groups of kGradRows) or token in the gradient's passes, a quarter per element
+// in the fill and the lookup. The lookup numbers a row's units in 32 bits.
+constexpr int64_t kEmbedMaxRows = (int64_t(1) << 27) - kGradRows, kEmbedMaxCols = int64_t(1) << 31;
+constexpr int64_t kEmbedMaxIds = int64_t(1) << 26;
+static_assert((kEmbedMaxRows + kGradRows - 1) / kGradRows * kThreads < int64_t(1) << 32, "the whole-table pass");
 constexpr int64_t kEmbedMaxTable = int64_t(1) << 34, kEmbedMaxElems = int64_t(1) << 33;
 
 // The table of an embedding call: a tensor of the plan in row-major order.
@@ -545,9 +548,10 @@ int check_table(const rs_plan* p, int64_t tensor, int64_t n_ids, const char* who
   const Tensor& t = p->t[tensor];
   if (t.kind == RS_TILEMAJOR) return fail(RS_EINVAL, std::string(who) + ": a TILEMAJOR tensor has no contiguous rows");
   if (n_ids < 0) return fail(RS_EINVAL, std::string(who) + ": negative number of tokens");
-  if (t.rows >= kEmbedMaxRows || t.n > kEmbedMaxTable || n_ids >= kEmbedMaxIds || n_ids * t.cols > kEmbedMaxElems)
-    return fail(RS_ERANGE, std::string(who) + ": rows under 2^27, tokens under 2^26, table at most 2^34 elements, "
-                               "tokens * columns at most 2^33");
+  if (t.rows > kEmbedMaxRows || t.cols >= kEmbedMaxCols || t.n > kEmbedMaxTable || n_ids >= kEmbedMaxIds ||
+      n_ids * t.cols > kEmbedMaxElems)
+    return fail(RS_ERANGE, std::string(who) + ": rows at most 2^27 - 8, columns under 2^31, table at most 2^34 "
+                               "elements, tokens under 2^26, tokens * columns at most 2^33");
   return RS_OK;
 }
 
