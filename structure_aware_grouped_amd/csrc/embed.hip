@@ -480,8 +480,10 @@ __global__ __launch_bounds__(kThreads) void embed_table_kernel(const uint32_t* _
   int64_t pos = lower_bound(srow, n_ids, static_cast<uint32_t>(r0), lane);
   Window w;
   for (int64_t r = r0; r < r0 + kGradRows && r < rows; ++r) {
+    const int64_t first = pos;
     const f32x4 sum = sum_row<BF16, VEC>(static_cast<uint32_t>(r), pos, w, srow, stok, n_ids, dy, part, c0, cols, lane);
-    store_row<OUT16, VEC>(packed, prev, r * cols, sum, sigma, c0, cols, lane);
+    // a row that no token names gets +0.0 or prev + 0.0, as from the fill: a negative sigma would make it -0.0
+    store_row<OUT16, VEC>(packed, prev, r * cols, sum, pos == first ? 0.0f : sigma, c0, cols, lane);
   }
 }
 
