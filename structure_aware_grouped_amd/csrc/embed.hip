@@ -249,23 +249,24 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const void* id
   }
 }
 
-// Sorted runs -> one sorted list: a token's place is its place in its own run
-// plus, in every other run, the number of smaller rows, or of smaller and
-// equal rows where that run's tokens come first. The runs' rows are searched
-// in LDS, kMergeRuns at a time (in memory the 11 dependent reads of one search
-// took 15 us).
+// Sorted runs -> one sorted list of each `span` neighbouring runs: a token's
+// place is its place in its own run plus, in every other run, the number of
+// smaller rows, or of smaller and equal rows where that run's tokens come
+// first. The runs' rows are searched in LDS, kMergeRuns at a time (in memory
+// the 11 dependent reads of one search took 15 us).
 constexpr int kMergeRuns = 8;
+constexpr int64_t kMergeAll = 16;   // runs merged in one launch (32: 94 us so, 80 in two passes; 16: 60 either way)
 
 __global__ __launch_bounds__(kThreads) void embed_merge_kernel(const uint32_t* __restrict__ rows,
                                                                const uint32_t* __restrict__ toks, int64_t n_ids,
-                                                               uint32_t* srow, uint32_t* stok) {
+                                                               int64_t span, uint32_t* srow, uint32_t* stok) {
   __shared__ __attribute__((aligned(16))) uint32_t s[kMergeRuns][kRun];
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const bool in = i < n_ids;
   const uint32_t row = in ? rows[i] : 0u, tok = in ? toks[i] : 0u;
-  const int64_t own = i / kRun;
-  int64_t place = i - own * kRun;
-  for (int64_t r0 = 0; r0 * kRun < n_ids; r0 += kMergeRuns) {
+  const int64_t own = i / kRun, begin = own / span * span, end = begin + span;
+  int64_t place = i - own * kRun + begin * kRun;
+  for (int64_t r0 = begin; r0 < end && r0 * kRun < n_ids; r0 += kMergeRuns) {
     __syncthreads();
     uint32_t* flat = &s[0][0];
     const int64_t at = r0 * kRun;
@@ -297,6 +298,41 @@ __global__ __launch_bounds__(kThreads) void embed_merge_kernel(const uint32_t* _
     srow[place] = row;
     stok[place] = tok;
   }
+}
+
+// One more pass over sorted lists of len = kRun * kMergeRuns^k tokens: each
+// kMergeRuns neighbouring ones -> one, as above, with the searches in memory.
+// A thread's searches in the other lists go step by step together, and a
+// wave's tokens, neighbours in a sorted list, read neighbouring places.
+__global__ __launch_bounds__(kThreads) void embed_merge_lists_kernel(const uint32_t* __restrict__ rows,
+                                                                     const uint32_t* __restrict__ toks, int n_ids,
+                                                                     int len, uint32_t* srow, uint32_t* stok) {
+  const int i = static_cast<int>(blockIdx.x) * kThreads + static_cast<int>(threadIdx.x);
+  if (i >= n_ids) return;
+  const uint32_t row = rows[i];
+  const int own = i / len, begin = own / kMergeRuns * kMergeRuns;
+  int lo[kMergeRuns], size[kMergeRuns];
+#pragma unroll
+  for (int r = 0; r < kMergeRuns; ++r) {
+    const int64_t first = static_cast<int64_t>(begin + r) * len;
+    lo[r] = 0;
+    size[r] = first >= n_ids || begin + r == own ? 0 : static_cast<int>(n_ids - first < len ? n_ids - first : len);
+  }
+  for (int step = len; step > 0; step /= 2) {
+#pragma unroll
+    for (int r = 0; r < kMergeRuns; ++r) {
+      const int next = lo[r] + step;
+      if (next <= size[r]) {
+        const uint32_t x = rows[static_cast<int64_t>(begin + r) * len + next - 1];
+        if (begin + r < own ? x <= row : x < row) lo[r] = next;
+      }
+    }
+  }
+  int place = i - own * len + begin * len;
+#pragma unroll
+  for (int r = 0; r < kMergeRuns; ++r) place += lo[r];
+  srow[place] = row;
+  stok[place] = toks[i];
 }
 
 // ------------------------------------------------------------------ gradient
@@ -636,14 +672,30 @@ void launch_grad(const Tensor& t, const GradCall& c, hipStream_t s) {
   // digits are all ones
   int passes = 1;
   while (passes * kDigitBits < 32 && t.rows >> (passes * kDigitBits) > 0) ++passes;
-  uint32_t* rrow = runs > 1 ? reinterpret_cast<uint32_t*>(c.work + w.rrow) : srow;
-  uint32_t* rtok = runs > 1 ? reinterpret_cast<uint32_t*>(c.work + w.rtok) : stok;
+  // Up to kMergeAll runs are merged at once, which reads all of them for every
+  // 256 tokens; more in passes of kMergeRuns, so that the time stays in
+  // proportion to the tokens (131072 of them at once 177 us the call, in passes
+  // 133; 2^20 5.5 ms and 0.91). The passes go to and fro between two lists and
+  // end in srow.
+  int merges = runs > 1 ? 1 : 0;
+  if (runs > kMergeAll)
+    for (int64_t lists = (runs + kMergeRuns - 1) / kMergeRuns; lists > 1; lists = (lists + kMergeRuns - 1) / kMergeRuns) ++merges;
+  uint32_t* list_row[2] = {srow, reinterpret_cast<uint32_t*>(c.work + w.rrow)};
+  uint32_t* list_tok[2] = {stok, reinterpret_cast<uint32_t*>(c.work + w.rtok)};
+  int from = merges % 2;
   if (runs + extra)
     hipLaunchKernelGGL(embed_sort_kernel, dim3(static_cast<unsigned>(runs) + extra), dim3(kSortThreads), 0, s, c.ids,
-                       c.wide, n, static_cast<uint32_t>(t.rows), passes, rrow, rtok, static_cast<unsigned>(runs), f);
-  if (runs > 1)
-    hipLaunchKernelGGL(embed_merge_kernel, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads),
-                       0, s, rrow, rtok, n, srow, stok);
+                       c.wide, n, static_cast<uint32_t>(t.rows), passes, list_row[from], list_tok[from],
+                       static_cast<unsigned>(runs), f);
+  const dim3 merge_grid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
+  for (int64_t m = 0, len = kRun; m < merges; ++m, len *= kMergeRuns, from ^= 1) {
+    if (m == 0)
+      hipLaunchKernelGGL(embed_merge_kernel, merge_grid, dim3(kThreads), 0, s, list_row[from], list_tok[from], n,
+                         merges == 1 ? runs : int64_t(kMergeRuns), list_row[from ^ 1], list_tok[from ^ 1]);
+    else
+      hipLaunchKernelGGL(embed_merge_lists_kernel, merge_grid, dim3(kThreads), 0, s, list_row[from], list_tok[from],
+                         static_cast<int>(n), static_cast<int>(len), list_row[from ^ 1], list_tok[from ^ 1]);
+  }
   const unsigned chunks = static_cast<unsigned>(n / kSumChunk);
   f = share(fill, kThreads, &extra);
   if (chunks + extra)
