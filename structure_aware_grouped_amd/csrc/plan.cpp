@@ -517,20 +517,35 @@ std::vector<int> deal(int from, int to, size_t at) {
   return order;
 }
 
+// When a launch ends whose jobs cost `costs`: each is taken, in order, by the
+// workgroup that is free first. `load`: what the workgroups have before.
+int64_t launch_end(std::vector<int64_t> load, const std::vector<int64_t>& costs) {
+  int64_t end = *std::max_element(load.begin(), load.end());
+  std::make_heap(load.begin(), load.end(), std::greater<int64_t>());
+  for (int64_t c : costs) {
+    std::pop_heap(load.begin(), load.end(), std::greater<int64_t>());
+    end = std::max(end, load.back() += c);
+    std::push_heap(load.begin(), load.end(), std::greater<int64_t>());
+  }
+  return end;
+}
+
 // The jobs of one product. Whole rounds of one tile per workgroup come first:
 // the workgroups of an XCD take neighbouring tiles and run in step, so that
 // they share operand rows in its L2 (out of step, with tiles cut at different
 // places ahead of them, an 8192 x 28672 product took 4.25 ms instead of 3.49).
 // The tiles left over (528 tiles of an 8192-row X X^T are 2.06 rounds) are laid
 // end to end into what room the workgroups have below a common end, and cut
-// where one workgroup's room ends and the next one's begins. A job starts
-// when a workgroup's place is free, so jobs are listed longest first within
-// the rounds' order.
-void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* out) {
+// where one workgroup's room ends and the next one's begins. Room of less than
+// kMatMinSteps is left empty, so the common end is raised until the launch ends
+// there; where that is not mat_join_steps ahead of the end of whole tiles, nothing
+// is cut. A job starts when a workgroup's place is free, so jobs are listed
+// longest first within the rounds' order.
+void schedule(const std::vector<ProductTile>& tiles, ProductList* out) {
+  const int groups = mat_places(out->side);
   struct Part {
     int tile, k0, k1;
   };
-  std::vector<Part> parts;
   auto cost = [&](int t, int steps) { return int64_t(steps) * tiles[t].weight; };
   const int n = static_cast<int>(tiles.size()), whole = n / groups * groups;
   auto give = [&](int t) {
@@ -556,6 +571,32 @@ void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* ou
     left += cost(t, tiles[t].steps);
     longest = std::max(longest, cost(t, tiles[t].steps));
   }
+  auto of = [&](const Part& p) { return cost(p.tile, p.k1 - p.k0); };
+  // the order of a list, longest first, and when the launch ends in an order
+  auto listed = [&](const std::vector<Part>& parts) {
+    std::vector<int> order(parts.size()), dealt;
+    for (size_t p = 0; p < parts.size(); ++p) order[p] = static_cast<int>(p);
+    std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return of(parts[a]) > of(parts[b]); });
+    for (int from = 0, to = 0; from < static_cast<int>(order.size()); from = to) {   // of about the same length
+      while (to < static_cast<int>(order.size()) && 4 * of(parts[order[to]]) >= 3 * of(parts[order[from]])) ++to;
+      for (int j : deal(from, to, out->jobs.size() + dealt.size())) dealt.push_back(order[j]);
+    }
+    return dealt;
+  };
+  auto ends = [&](const std::vector<Part>& parts, const std::vector<int>& order) {
+    std::vector<int64_t> costs;
+    for (int j : order) costs.push_back(of(parts[j]));
+    return launch_end(load, costs);
+  };
+  // whole tiles, as neighbours or longest first
+  std::vector<Part> parts;
+  for (int t = whole; t < n; ++t) parts.push_back({t, 0, tiles[t].steps});
+  std::vector<int> order = deal(0, n - whole, out->jobs.size()), other = listed(parts);
+  int64_t best = ends(parts, order);
+  if (const int64_t e = ends(parts, other); e < best) {
+    best = e;
+    order.swap(other);
+  }
   // the end at which the room below it holds what is left
   int64_t end = 0, below = 0;
   for (int c = 1; c <= groups; ++c) {
@@ -564,26 +605,40 @@ void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* ou
     if (c == groups || end <= load[c]) break;
   }
   const int64_t least = std::max<int64_t>(ceil_div(longest, kMatMaxParts - 1), kMatMinSteps);
-  // no cuts where they would save less than joining the parts costs
-  if (load[0] + longest - std::max(end, load[0] + least) <= kMatJoinSteps) {
-    for (int t : deal(whole, n, out->jobs.size())) give(t);
-    return;
-  }
-  int c = 0;
-  int64_t room = std::max(end - load[0], least);
-  for (int t = whole; t < n; ++t) {
-    for (int k = 0; k < tiles[t].steps;) {
-      const int rest = tiles[t].steps - k;
-      int take = static_cast<int>(std::min<int64_t>(rest, std::max<int64_t>(1, room / tiles[t].weight)));
-      if (rest - take < kMatMinSteps || c == groups - 1) take = rest;   // no short rest
-      parts.push_back({t, k, k + take});
-      k += take;
-      room -= cost(t, take);
-      if (room < kMatMinSteps * int64_t(tiles[t].weight) && c + 1 < groups) {
-        ++c;
-        room = std::max(end - load[c], least);
+  end = std::max(end, load[0] + least);
+  // the parts that fill the room below `end`
+  auto cut = [&](int64_t end) {
+    std::vector<Part> parts;
+    int c = 0;
+    int64_t room = std::max(end - load[0], least);
+    for (int t = whole; t < n; ++t) {
+      for (int k = 0; k < tiles[t].steps;) {
+        const int rest = tiles[t].steps - k;
+        int take = static_cast<int>(std::min<int64_t>(rest, std::max<int64_t>(1, room / tiles[t].weight)));
+        if (rest - take < kMatMinSteps || c == groups - 1) take = rest;   // no short rest
+        parts.push_back({t, k, k + take});
+        k += take;
+        room -= cost(t, take);
+        if (room < kMatMinSteps * int64_t(tiles[t].weight) && c + 1 < groups) {
+          ++c;
+          room = std::max(end - load[c], least);
+        }
       }
     }
+    return parts;
+  };
+  best -= mat_join_steps(out->side);   // an end to be ahead of
+  for (int tries = 0; tries < kMatTries && end < best; ++tries) {
+    std::vector<Part> p = cut(end);
+    std::vector<int> o = listed(p);
+    const int64_t e = ends(p, o);
+    if (e < best) {
+      best = e;
+      parts.swap(p);
+      order.swap(o);
+    }
+    if (e <= end) break;
+    end += std::max<int64_t>(1, (e - end) / 8);
   }
   std::vector<int> count(n, 0), slab(n, -1);
   for (const Part& p : parts) ++count[p.tile];
@@ -594,20 +649,14 @@ void schedule(const std::vector<ProductTile>& tiles, int groups, ProductList* ou
     const ProductTile& x = tiles[t];
     out->joins.push_back({x.mat, x.i, x.j, 0, static_cast<uint16_t>(x.steps), static_cast<uint16_t>(count[t]), 0, slab[t]});
   }
-  std::vector<std::pair<int64_t, ProductJob>> jobs;
-  for (size_t p = 0; p < parts.size(); ++p) {
+  std::vector<int> number(parts.size(), 0);
+  for (size_t p = 1; p < parts.size(); ++p)
+    if (parts[p - 1].tile == parts[p].tile) number[p] = number[p - 1] + 1;
+  for (int p : order) {
     const Part& a = parts[p];
     const ProductTile& x = tiles[a.tile];
-    const bool first = !p || parts[p - 1].tile != a.tile;
-    jobs.push_back({cost(a.tile, a.k1 - a.k0),
-                    {x.mat, x.i, x.j, static_cast<uint16_t>(a.k0), static_cast<uint16_t>(a.k1),
-                     static_cast<uint16_t>(count[a.tile]), 0,
-                     count[a.tile] < 2 ? -1 : first ? slab[a.tile] : jobs.back().second.slab + 1}});
-  }
-  std::stable_sort(jobs.begin(), jobs.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
-  for (int from = 0, to = 0; from < static_cast<int>(jobs.size()); from = to) {   // of about the same length
-    while (to < static_cast<int>(jobs.size()) && 4 * jobs[to].first >= 3 * jobs[from].first) ++to;
-    for (int j : deal(from, to, out->jobs.size())) out->jobs.push_back(jobs[j].second);
+    out->jobs.push_back({x.mat, x.i, x.j, static_cast<uint16_t>(a.k0), static_cast<uint16_t>(a.k1),
+                         static_cast<uint16_t>(count[a.tile]), 0, count[a.tile] < 2 ? -1 : slab[a.tile] + number[p]});
   }
 }
 
@@ -644,7 +693,7 @@ void lower_product(const std::vector<MuonMat>& mats, int list, ProductList* out)
             if (!sym || j <= i)
               tiles.push_back({k, static_cast<uint16_t>(i), static_cast<uint16_t>(j), steps, q.two_part ? 3 : 1});
   }
-  schedule(tiles, mat_places(out->side), out);
+  schedule(tiles, out);
 }
 
 }  // namespace

@@ -330,10 +330,17 @@ constexpr int mat_places(int side) { return side == 256 ? 256 : 512; }
 constexpr int kXcds = 8;
 constexpr int kMatMaxParts = 8;    // a tile's contraction is cut into at most this many parts
 constexpr int kMatMinSteps = 4;    // steps of kMatK in a part, at least
-// Tiles are cut only where that ends a launch this many steps earlier: the
-// join is a launch of its own (1024 x 4096: 303 us with 10, 267 with 16 and
-// 24; the Llama-3-8B layer 15.27 ms with 16, 14.95 with 24).
-constexpr int kMatJoinSteps = 24;
+// Tiles are cut only where that ends a launch more than this many steps
+// earlier: the join is a launch of its own, and costs more of the shorter steps
+// of smaller tiles. Whole calls with 24 / 30 / 36 for all: 5000 x 5000 (128-wide
+// m x m products 28 steps ahead) 3.20 / 3.08 / 3.03 ms, two MoE experts (256-wide
+// products 31 ahead) 3.37 / 3.44 / 3.48, 2880 x 2880 (128-wide, 37 ahead) 0.83
+// with any, 0.90 without cuts. What a join costs also grows with its tiles, which
+// this leaves out: 1024 x 4096 (136 of 136 tiles cut, 46 ahead) takes 242 us with
+// cuts and 227 without, 333 x 1001 beside 128 x 2880 (24 tiles, 37 ahead) 122
+// and 129.
+constexpr int mat_join_steps(int side) { return side == 256 ? 24 : 30; }
+constexpr int kMatTries = 24;      // common ends that are tried for the cuts of one launch
 // Matrices whose X is at most kMatTinyM x kMatTinyN run in one workgroup.
 constexpr int64_t kMatTinyM = 64, kMatTinyN = 256;
 // Elements per work item of the pass that updates momentum and sums squares.

@@ -7,7 +7,8 @@
 //
 // Reads "n" and n lines "rows cols" (WHOLE tensors) on stdin; prints "ok" and
 // per product the tile side, tiles, cut tiles, jobs, the end over the mean
-// share and how many steps it is behind it, or the first violation. With an argument 1-4 it
+// share, how many steps it is behind it and how many ahead of the end with
+// the cut tiles whole, longest first, or the first violation. With an argument 1-4 it
 // first plants a mistake (a job dropped, a step doubled, a slab shared, two
 // operands overlapping), which must be reported. A second argument is the
 // operands' parts of every matrix (1 or 2). Includes plan.cpp for
@@ -134,10 +135,18 @@ int main(int argc, char** argv) {
       if (js.size() > 1) ++cut;
     }
     if (joins.size() != cut) return bad("joins");
-    char line[200];
-    std::snprintf(line, sizeof line, " [%d tiles of %d, %zu cut, %zu jobs, share %.2f, behind %.1f]", static_cast<int>(need), l.side, cut,
+    // the same launch with its cut tiles whole
+    std::vector<double> uncut(mat_places(l.side), 0.0), cut_cost;
+    for (const ProductJob& p : l.jobs)
+      if (p.parts == 1) *std::min_element(uncut.begin(), uncut.end()) += (p.k1 - p.k0) * (mt.mats[p.mat].two_part ? 3 : 1);
+    for (const ProductJob& p : l.joins) cut_cost.push_back(p.k1 * (mt.mats[p.mat].two_part ? 3 : 1));
+    std::sort(cut_cost.begin(), cut_cost.end(), std::greater<double>());
+    for (double s : cut_cost) *std::min_element(uncut.begin(), uncut.end()) += s;
+    char line[240];
+    std::snprintf(line, sizeof line, " [%d tiles of %d, %zu cut, %zu jobs, share %.2f, behind %.1f, ahead %.1f]", static_cast<int>(need), l.side, cut,
                   l.jobs.size(), total ? *std::max_element(share.begin(), share.end()) / (total / share.size()) : 1.0,
-                  *std::max_element(share.begin(), share.end()) - total / share.size());
+                  *std::max_element(share.begin(), share.end()) - total / share.size(),
+                  *std::max_element(uncut.begin(), uncut.end()) - *std::max_element(share.begin(), share.end()));
     text += line;
   }
   std::printf("ok%s\n", text.c_str());
