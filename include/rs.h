@@ -176,7 +176,8 @@ int rs_plan_build(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t ali
  * identical results. RS_MUON_TILE=64|128|256 forces the output tile of the
  * matrix products (rs_orthogonalize, rs_muon_step), small matrices included;
  * RS_MUON_PAIRS=1 runs their first two steps together for every matrix whose
- * operands have one part (more than 64 rows and columns).
+ * operands have one part (more than 64 rows and columns); RS_MUON_CUTS=1 cuts
+ * every tile of their last, partial round along the contraction.
  * On success *out owns host memory and one device allocation, released by
  * rs_plan_free. Errors: the above, RS_ENOMEM, RS_EHIP. */
 int rs_plan_load(const rs_tensor_spec* specs, int64_t n, int64_t V, int64_t S,

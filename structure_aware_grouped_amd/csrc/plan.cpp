@@ -500,6 +500,13 @@ bool forced_pairs() {
   return e && std::strcmp(e, "1") == 0;
 }
 
+// RS_MUON_CUTS=1: every tile of a launch's last, partial round is cut where it
+// has the steps for it.
+bool forced_cuts() {
+  const char* e = std::getenv("RS_MUON_CUTS");
+  return e && std::strcmp(e, "1") == 0;
+}
+
 struct ProductTile {
   int32_t mat;
   uint16_t i, j;
@@ -628,6 +635,14 @@ void schedule(const std::vector<ProductTile>& tiles, ProductList* out) {
     return parts;
   };
   best -= mat_join_steps(out->side);   // an end to be ahead of
+  if (forced_cuts()) {
+    parts.clear();
+    for (int t = whole; t < n; ++t)
+      for (int k = 0, of = std::min(3, tiles[t].steps); k < of; ++k)
+        parts.push_back({t, tiles[t].steps * k / of, tiles[t].steps * (k + 1) / of});
+    order = listed(parts);
+    best = 0;
+  }
   for (int tries = 0; tries < kMatTries && end < best; ++tries) {
     std::vector<Part> p = cut(end);
     std::vector<int> o = listed(p);
