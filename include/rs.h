@@ -471,8 +471,16 @@ int rs_muon_step(rs_plan* plan, float* param, const void* grad, int32_t grad_dt,
                  const rs_muon_hparams* hp, const float* coeffs, void* work, int64_t work_bytes, void* stream);
 
 /* Bytes of workspace that rs_orthogonalize and rs_muon_step need for this
- * plan (about 8 per element of its matrices and 4 per element of their smaller
- * Gram matrices; half as much again for sides of at most 64). Errors: RS_EINVAL. */
+ * plan. All its matrices advance together, so it is a sum over them (a group
+ * split over several plans needs the largest of theirs). With m and n a
+ * matrix's shorter and longer side, each padded to a multiple of 64:
+ *   one part                     8 m n + 4 m^2
+ *   one part, m >= 1024 and n >= 1.5 m (the first two steps together)
+ *                                8 m n + 8 m^2
+ *   two parts                    12 m n + 8 m^2
+ *   m <= 64 and n <= 256         nothing
+ * and up to 1% and 8 KiB a matrix more for norms, diagonals and alignment, and
+ * at most 128 MiB in all for the parts of cut tiles. Errors: RS_EINVAL. */
 int rs_muon_workspace(const rs_plan* plan, int64_t* bytes);
 
 /* Message for the calling thread's last failed call ("" if none). The

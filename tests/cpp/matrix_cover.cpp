@@ -8,7 +8,8 @@
 // Reads "n" and n lines "rows cols" (WHOLE tensors) on stdin; prints "ok" and
 // per product the tile side, tiles, cut tiles, jobs, the end over the mean
 // share, how many steps it is behind it and how many ahead of the end with
-// the cut tiles whole, longest first, or the first violation. With an argument 1-4 it
+// the cut tiles whole, longest first, and at last the workspace's bytes and those
+// of the cut tiles' parts; or the first violation. With an argument 1-4 it
 // first plants a mistake (a job dropped, a step doubled, a slab shared, two
 // operands overlapping), which must be reported. A second argument is the
 // operands' parts of every matrix (1 or 2). Includes plan.cpp for
@@ -149,6 +150,6 @@ int main(int argc, char** argv) {
                   *std::max_element(uncut.begin(), uncut.end()) - *std::max_element(share.begin(), share.end()));
     text += line;
   }
-  std::printf("ok%s\n", text.c_str());
+  std::printf("ok%s work %lld parts %lld\n", text.c_str(), static_cast<long long>(mt.work_bytes), static_cast<long long>(slabs));
   return 0;
 }

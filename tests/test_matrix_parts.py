@@ -3,6 +3,8 @@ options that are refused, and the work lists and workspace that they give
 (tests/cpp/matrix_cover.cpp)."""
 import ctypes
 import os
+import random
+import re
 import subprocess
 
 import pytest
@@ -46,3 +48,28 @@ def test_every_step_once_with_two_parts(exe, shapes, tile, monkeypatch):  # noqa
     text = f"{len(shapes)}\n" + "".join(f"{r} {c}\n" for r, c in shapes)
     r = subprocess.run([exe, "0", "2"], input=text, capture_output=True, text=True, timeout=120, env=dict(os.environ))
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
+
+
+def _stated(rows, cols, parts):
+    """The workspace that rs.h states for one matrix."""
+    m, n = (-(-v // 64) * 64 for v in (min(rows, cols), max(rows, cols)))
+    if min(rows, cols) < 2 or (min(rows, cols) <= 64 and max(rows, cols) <= 256):
+        return 0
+    if parts == 2 or min(rows, cols) <= 64:
+        return 12 * m * n + 8 * m * m
+    paired = min(rows, cols) >= 1024 and 2 * max(rows, cols) >= 3 * min(rows, cols)
+    return 8 * m * n + (8 if paired else 4) * m * m
+
+
+@pytest.mark.parametrize("parts", [1, 2])
+@pytest.mark.parametrize("seed", range(25))
+def test_workspace_is_as_stated(exe, seed, parts):  # noqa: F811
+    rng = random.Random(seed)
+    shapes = [(rng.choice([2, 17, 64, 65, 300, 1000, 1024, 1100, 2049, 5000, 8192]), rng.choice([2, 33, 64, 129, 300, 777, 2880, 6000, 20000]))
+              for _ in range(rng.randint(1, 6))] if seed else [(2880, 5760)] * 16
+    text = f"{len(shapes)}\n" + "".join(f"{r} {c}\n" for r, c in shapes)
+    r = subprocess.run([exe, "0", str(parts)], input=text, capture_output=True, text=True, timeout=120)
+    work, cut = (int(v) for v in re.search(r"work (\d+) parts (\d+)", r.stdout).groups())
+    stated = sum(_stated(*s, parts) for s in shapes)
+    assert cut <= 128 << 20
+    assert stated <= work - cut <= 1.01 * stated + 8192 * len(shapes), (shapes, work, cut, stated)
