@@ -473,7 +473,7 @@ int rs_muon_step(rs_plan* plan, float* param, const void* grad, int32_t grad_dt,
 /* Bytes of workspace that rs_orthogonalize and rs_muon_step need for this
  * plan. All its matrices advance together, so it is a sum over them (a group
  * split over several plans needs the largest of theirs). With m and n a
- * matrix's shorter and longer side, each padded to a multiple of 64:
+ * matrix's shorter and longer side, each padded to a multiple of 64, at most:
  *   one part                     8 m n + 4 m^2
  *   one part, m >= 1024 and n >= 1.5 m (the first two steps together)
  *                                8 m n + 8 m^2
