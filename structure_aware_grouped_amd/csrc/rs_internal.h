@@ -321,8 +321,12 @@ constexpr int64_t kMatMaxSide = int64_t(1) << 20;
 constexpr int64_t kMatMaxMin = int64_t(1) << 16;
 constexpr int64_t kMatMaxTiles = int64_t(1) << 22;   // 64 x 64 tiles of all matrices: launches under 2^32 work-items
 // A product takes 256 x 256 output tiles where the plan's matrices give at
-// least kMatMinTiles of them, else 128 x 128 by the same rule, else 64 x 64
-// (four MoE matrices, 312 tiles of 256: 3.83 ms with them, 3.70 with 128).
+// least kMatMinTiles of them, else 128 x 128 by the same rule, else 64 x 64. No
+// one number is best for all (a rule on the padded area and the rounds would be
+// nearer): whole calls with 200 / 320 / 400 took 1.61 / 1.69 / 1.69 ms for 4096 x
+// 4096, 2.91 / 3.09 / 3.10 for 5000 x 5000, 0.98 / 0.98 / 1.06 for 3200 x 3200,
+// 2.57 / 2.56 / 2.66 for 4500 x 4500, 1.12 / 1.12 / 1.04 for 2048 x 10240, 2.31 /
+// 2.31 / 2.22 for 5300 x 4100, 3.68 / 3.47 / 3.47 for two MoE experts (312 tiles).
 constexpr int64_t kMatMinTiles = 320;
 // Workgroups of a product that run at once: one per CU with 256-wide tiles
 // (128 KiB of LDS each), two with the others (64 KiB).
