@@ -39,16 +39,19 @@
 // and more. Two parts for every matrix give 4e-7 to 1.2e-6 on the card (one:
 // 2.3e-4 to 9.6e-4), 1.4e-5 where most directions are 100 times weaker than a
 // few (fp32 products give 2.8e-5 there), at 1.4 (100 x 110) to 2.9
-// (4096 x 14336: 4.0 -> 11.8 ms) times the time, so one is the default: its error is below the bf16 rounding of
-// rs_orthogonalize's result, and in rs_muon_step it comes times the rate.
+// (4096 x 14336: 4.0 -> 11.8 ms) times the time, so one is the default: its
+// error is below the bf16 rounding of rs_orthogonalize's result (where it moves
+// 16 to 22% of the values to their bf16 neighbour), and in rs_muon_step it comes
+// times the rate.
 //
 // What bounds it. The products: with 256-wide tiles the matrix cores are busy
-// 63 to 75% of the time at the 1.66 GHz that the card holds under them
-// (8192 x 28672: polynomial times X 3.54 ms, 1087 TFLOP/s, X X^T 1185; a
-// library fp16 product of that size reaches 1373). Small matrices: the latency
-// of about 17 launches. The passes around the products move bytes: momentum
-// and norm 5.8 TB/s, the split into operands 5.1 TB/s on the Llama-3-8B layer's
-// 218 M elements, 7% of its 14.5 ms.
+// 61 to 73% of the time for 8192 x 28672, at the 1.6 to 1.7 GHz that the card
+// holds under them (polynomial times X 3.41 ms, 1128 TFLOP/s, X X^T 1204; a
+// library fp16 product of that size reaches 1373 to 1427), and 42 to 58% at 1.8
+// GHz for the Llama-3-8B layer. Small matrices: the latency of about 17
+// launches. The passes around the products move bytes: momentum and norm 5.7
+// TB/s, the split into operands 4.8 TB/s on that layer's 218 M elements, 8% of
+// its 14.4 ms.
 #include "host_common.h"
 
 namespace rs {
@@ -340,8 +343,8 @@ __device__ __forceinline__ Where where(const MuonMat& m, int turn, int pair) {
 //   256: 64 KiB a stage, one workgroup per CU; what large products take. 128
 // and 64: two workgroups per CU, for products of few tiles; 64 keeps three
 // stages on their way, since few workgroups wait for memory. Whole calls, 64 /
-// 128 / 256 wide: 1024 x 4096 266 / 323 / 543 us, 4096 x 4096 2.25 / 1.62 /
-// 1.86 ms, 4096 x 14336 6.67 / 4.56 / 4.81 ms (4.37 with the rule: 128 for the
+// 128 / 256 wide: 1024 x 4096 248 / 339 / 569 us, 4096 x 4096 2.27 / 1.60 /
+// 1.75 ms, 4096 x 14336 5.84 / 4.00 / 4.01 ms (3.85 with the rule: 128 for the
 // m x m products, 256 for the m x n ones).
 template <int BM>
 struct Tile {
