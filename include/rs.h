@@ -480,7 +480,8 @@ int rs_muon_step(rs_plan* plan, float* param, const void* grad, int32_t grad_dt,
  *   two parts                    12 m n + 8 m^2
  *   m <= 64 and n <= 256         nothing
  * and up to 1% and 8 KiB a matrix more for norms, diagonals and alignment, and
- * at most 128 MiB in all for the parts of cut tiles. Errors: RS_EINVAL. */
+ * at most 128 MiB in all for the parts of cut tiles (192 with RS_MUON_CUTS=1).
+ * Errors: RS_EINVAL. */
 int rs_muon_workspace(const rs_plan* plan, int64_t* bytes);
 
 /* Message for the calling thread's last failed call ("" if none). The

@@ -245,7 +245,8 @@ def rs_plan_load(specs, V: int, S: int, starts: Sequence[int], R_mat: Optional[i
                  device: int = 0, muon_parts: int = 1) -> Plan:
     """Validate a plan and build its work lists on `device`. muon_parts: fp16 parts of the operands
     of rs_orthogonalize and rs_muon_step; 2 brings their results as near as fp32 products', at
-    1.4 to 2.9 times the time and up to 1.7 times the workspace."""
+    1.4 to 2.9 times the time and up to 1.7 times the workspace (an option of the loaded plan: a
+    plan's JSON does not hold it)."""
     lib = load()
     n = len(specs)
     if R_mat is None:
