@@ -7,12 +7,9 @@
 //
 // Reads "n" and n lines "rows cols" (WHOLE tensors) on stdin; prints "ok" and
 // per product the tile side, tiles, cut tiles, jobs, the end over the mean
-// share, how many steps it is behind it and how many ahead of the end with
-// the cut tiles whole, longest first, and at last the workspace's bytes and those
-// of the cut tiles' parts; or the first violation. With an argument 1-4 it
+// share and how many steps it is behind it, or the first violation. With an argument 1-4 it
 // first plants a mistake (a job dropped, a step doubled, a slab shared, two
-// operands overlapping), which must be reported. A second argument is the
-// operands' parts of every matrix (1 or 2). Includes plan.cpp for
+// operands overlapping), which must be reported. Includes plan.cpp for
 // lower_muon(); link with planner.cpp.
 #include "plan.cpp"
 
@@ -44,7 +41,7 @@ int main(int argc, char** argv) {
     t.push_back(x);
   }
   MuonTables mt;
-  lower_muon(t, &mt, argc > 2 ? std::atoi(argv[2]) : 1);
+  lower_muon(t, &mt);
   if (plant == 1) mt.list[0].jobs.pop_back();
   if (plant == 2) mt.list[2].jobs[0].k1 += 1;
   if (plant == 3)
@@ -136,20 +133,12 @@ int main(int argc, char** argv) {
       if (js.size() > 1) ++cut;
     }
     if (joins.size() != cut) return bad("joins");
-    // the same launch with its cut tiles whole
-    std::vector<double> uncut(mat_places(l.side), 0.0), cut_cost;
-    for (const ProductJob& p : l.jobs)
-      if (p.parts == 1) *std::min_element(uncut.begin(), uncut.end()) += (p.k1 - p.k0) * (mt.mats[p.mat].two_part ? 3 : 1);
-    for (const ProductJob& p : l.joins) cut_cost.push_back(p.k1 * (mt.mats[p.mat].two_part ? 3 : 1));
-    std::sort(cut_cost.begin(), cut_cost.end(), std::greater<double>());
-    for (double s : cut_cost) *std::min_element(uncut.begin(), uncut.end()) += s;
-    char line[240];
-    std::snprintf(line, sizeof line, " [%d tiles of %d, %zu cut, %zu jobs, share %.2f, behind %.1f, ahead %.1f]", static_cast<int>(need), l.side, cut,
+    char line[200];
+    std::snprintf(line, sizeof line, " [%d tiles of %d, %zu cut, %zu jobs, share %.2f, behind %.1f]", static_cast<int>(need), l.side, cut,
                   l.jobs.size(), total ? *std::max_element(share.begin(), share.end()) / (total / share.size()) : 1.0,
-                  *std::max_element(share.begin(), share.end()) - total / share.size(),
-                  *std::max_element(uncut.begin(), uncut.end()) - *std::max_element(share.begin(), share.end()));
+                  *std::max_element(share.begin(), share.end()) - total / share.size());
     text += line;
   }
-  std::printf("ok%s work %lld parts %lld\n", text.c_str(), static_cast<long long>(mt.work_bytes), static_cast<long long>(slabs));
+  std::printf("ok%s\n", text.c_str());
   return 0;
 }

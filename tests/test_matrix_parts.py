@@ -1,16 +1,18 @@
 """Two-part operands for every matrix (rs_plan_load_with's muon_parts): the
 options that are refused, and the work lists and workspace that they give
-(tests/cpp/matrix_cover.cpp)."""
+(tests/cpp/matrix_lists.cpp)."""
 import ctypes
-import os
 import random
-import re
-import subprocess
 
 import pytest
 
-from tests.test_matrix_cover import LAYER, exe  # noqa: F401  (a fixture)
+from tests.matrix_lists import LAYER, build, lists
 from workloads import TensorSpec
+
+
+@pytest.fixture(scope="module")
+def exe(tmp_path_factory):
+    return build(tmp_path_factory.mktemp("lists"))
 
 
 def _load(rs, specs, options):
@@ -39,15 +41,11 @@ def test_reserved_options_are_refused():
         assert _load(rs, [TensorSpec("w", 128, 128, "WHOLE")], ctypes.byref(options)) == (b.RS_EINVAL, None)
 
 
-@pytest.mark.parametrize("tile", [None, "64", "128", "256"])
+@pytest.mark.parametrize("tile", [None, 64, 128, 256])
 @pytest.mark.parametrize("shapes", [[(65, 65)], [(1024, 4096)], [(128, 2880), (333, 1001), (40, 900)], LAYER,
                                     [(5760, 2880), (2880, 2880)] * 8])
-def test_every_step_once_with_two_parts(exe, shapes, tile, monkeypatch):  # noqa: F811
-    monkeypatch.setenv("RS_MUON_TILE", tile or "")
-    monkeypatch.setenv("RS_MUON_PAIRS", "1")       # two-part matrices have no paired steps, asked for or not
-    text = f"{len(shapes)}\n" + "".join(f"{r} {c}\n" for r, c in shapes)
-    r = subprocess.run([exe, "0", "2"], input=text, capture_output=True, text=True, timeout=120, env=dict(os.environ))
-    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
+def test_every_step_once_with_two_parts(exe, shapes, tile):
+    lists(exe, shapes, 2, tile, pairs=True)       # two-part matrices have no paired steps, asked for or not
 
 
 def _stated(rows, cols, parts, pad=64):
@@ -63,13 +61,12 @@ def _stated(rows, cols, parts, pad=64):
 
 @pytest.mark.parametrize("parts", [1, 2])
 @pytest.mark.parametrize("seed", range(25))
-def test_workspace_is_as_stated(exe, seed, parts):  # noqa: F811
+def test_workspace_is_as_stated(exe, seed, parts):
     rng = random.Random(seed)
     shapes = [(rng.choice([2, 17, 64, 65, 300, 1000, 1024, 1100, 2049, 5000, 8192]), rng.choice([2, 33, 64, 129, 300, 777, 2880, 6000, 20000]))
               for _ in range(rng.randint(1, 6))] if seed else [(2880, 5760)] * 16
-    text = f"{len(shapes)}\n" + "".join(f"{r} {c}\n" for r, c in shapes)
-    r = subprocess.run([exe, "0", str(parts)], input=text, capture_output=True, text=True, timeout=120)
-    work, cut = (int(v) for v in re.search(r"work (\d+) parts (\d+)", r.stdout).groups())
+    found = lists(exe, shapes, parts)
+    work, cut = found.work, found.parts
     stated, bare = (sum(_stated(*s, parts, pad) for s in shapes) for pad in (64, 1))
     assert cut <= 128 << 20
     assert bare <= work - cut <= 1.01 * stated + 8192 * len(shapes), (shapes, work, cut, stated)
