@@ -26,6 +26,11 @@
  *   rs_embed_rows       embedding lookup straight from the gathered buffer
  *   rs_embed_grad       its gradient straight into the packed buffer
  *   rs_embed_workspace  bytes of workspace rs_embed_grad needs
+ *   rs_layer_norm       layer norm (or RMS norm) with its weight and bias in
+ *                       the gathered buffer
+ *   rs_layer_norm_grad  its gradient, the parameters' straight into the
+ *                       packed buffer
+ *   rs_layer_norm_workspace  bytes of workspace rs_layer_norm_grad needs
  *   rs_orthogonalize    Newton-Schulz orthogonalisation of the WHOLE matrices
  *   rs_muon_step        one Muon step on the WHOLE matrices
  *   rs_muon_workspace   bytes of workspace the two need
@@ -401,6 +406,51 @@ int rs_embed_grad(rs_plan* plan, int64_t tensor, const void* ids, int32_t id_byt
 /* Bytes of workspace for rs_embed_grad on this tensor with n_ids tokens; it
  * grows with n_ids. Errors: RS_EINVAL, RS_ERANGE. */
 int rs_embed_workspace(const rs_plan* plan, int64_t tensor, int64_t n_ids, int64_t* bytes);
+
+/* Layer norm of each row of x with its parameters where the gather left them
+ * (feynmanwiki walkthrough, DBuffer paragraphs: a tensor is its planned
+ * slice). With C the number of elements of tensor `weight`, w its elements and
+ * b those of tensor `bias` (0 where bias is -1), per row:
+ *   m = center ? sum(x) / C : 0
+ *   r = 1 / sqrt(sum((x - m)^2) / C + eps)
+ *   y = (x - m) r w + b
+ * center 0 is the RMS norm. Sums and all steps are fp32, in an order that
+ * depends on C alone; a bf16 y is rounded once, to nearest even. A row of zeros
+ * gives b (NaN with eps = 0); a NaN or an infinity in a row, or a sum past
+ * fp32's range, stays in its row.
+ * weight, bias: numbers of two tensors of the plan with the same number of
+ * elements, any kind but RS_TILEMAJOR. gathered: device, R_mat*S elements of
+ * dt. x: device, n_rows x C row-major of x_dt. y: device, n_rows x C of y_dt,
+ * overlapping neither input. All RS_F32 or RS_BF16, 16-byte aligned. n_rows may
+ * be 0. eps: finite, >= 0. Limits (RS_ERANGE): C at most 16384, n_rows under
+ * 2^31. Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
+int rs_layer_norm(rs_plan* plan, int64_t weight, int64_t bias, const void* gathered, int32_t dt, const void* x,
+                  int32_t x_dt, int64_t n_rows, float eps, int32_t center, void* y, int32_t y_dt, void* stream);
+
+/* Gradients of rs_layer_norm from that of y; nothing is kept from the forward
+ * call. With h = (x - m) r and g = dy w, per row:
+ *   dx = r (g - (center ? sum(g) / C : 0) - h sum(g h) / C)
+ * and on the intervals of the two tensors in the packed buffer
+ *   weight:  packed = [prev +] sigma * sum over the rows of dy h
+ *   bias:    packed = [prev +] sigma * sum over the rows of dy
+ * with sigma = scale (RS_SCALE_GIVEN) or fl32(scale / V) (RS_SCALE_INV_V). The
+ * sums are fp32, in an order that depends on n_rows and C alone. Both intervals
+ * are written whole (also for n_rows = 0); other positions are left alone.
+ * x, x_dt, dy (n_rows x C of dy_dt): inputs. dx: device, n_rows x C of x_dt.
+ * prev: device fp32 R_mat*S or NULL; it may equal packed (fp32 only) to add in
+ * place, and must not overlap it in any other way. packed: device R_mat*S of
+ * packed_dt (RS_F32 or RS_BF16). work: device memory of
+ * rs_layer_norm_workspace bytes, contents not kept between calls; calls that
+ * may overlap need a workspace each. All 16-byte aligned; outputs overlap
+ * neither inputs nor each other. Limits and errors as in rs_layer_norm. */
+int rs_layer_norm_grad(rs_plan* plan, int64_t weight, int64_t bias, const void* gathered, int32_t dt, const void* x,
+                       int32_t x_dt, const void* dy, int32_t dy_dt, int64_t n_rows, float eps, int32_t center, void* dx,
+                       const float* prev, void* packed, int32_t packed_dt, int32_t scale_mode, float scale, void* work,
+                       int64_t work_bytes, void* stream);
+
+/* Bytes of workspace for rs_layer_norm_grad on n_rows rows, or fewer. Errors:
+ * RS_EINVAL, RS_ERANGE. */
+int rs_layer_norm_workspace(const rs_plan* plan, int64_t weight, int64_t n_rows, int64_t* bytes);
 
 /* Orthogonalisation of every matrix of the plan by Newton-Schulz products
  * (feynmanwiki walkthrough, Muon paragraphs: the rank that holds a matrix

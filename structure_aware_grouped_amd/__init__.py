@@ -18,6 +18,9 @@ from .binding import (  # noqa: F401
     rs_embed_grad,
     rs_embed_rows,
     rs_embed_workspace,
+    rs_layer_norm,
+    rs_layer_norm_grad,
+    rs_layer_norm_workspace,
     rs_muon_step,
     rs_muon_workspace,
     rs_orthogonalize,

@@ -28,7 +28,8 @@ CODE_FORMATS = {"e4m3": RS_E4M3, "i8": RS_I8, "u8": RS_U8}
 EXPORTS = ("rs_plan_build", "rs_plan_load", "rs_plan_load_with", "rs_plan_info", "rs_plan_free", "rs_unpack_gathered",
            "rs_pack_scatter", "rs_block_quant", "rs_block_dequant", "rs_unpack_dequant", "rs_adam8_step",
            "rs_last_error", "rs_block_quant_noalloc", "rs_orthogonalize", "rs_muon_step", "rs_muon_workspace",
-           "rs_embed_rows", "rs_embed_grad", "rs_embed_workspace")
+           "rs_embed_rows", "rs_embed_grad", "rs_embed_workspace", "rs_layer_norm", "rs_layer_norm_grad",
+           "rs_layer_norm_workspace")
 
 
 class RsError(RuntimeError):
@@ -96,6 +97,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rs_embed_rows.argtypes = [P, I64, P, I32, P, I32, I64, F, P, I32, P]
     lib.rs_embed_grad.argtypes = [P, I64, P, I32, I64, P, I32, P, P, I32, I32, F, P, I64, P]
     lib.rs_embed_workspace.argtypes = [P, I64, I64, PI64]
+    lib.rs_layer_norm.argtypes = [P, I64, I64, P, I32, P, I32, I64, F, I32, P, I32, P]
+    lib.rs_layer_norm_grad.argtypes = [P, I64, I64, P, I32, P, I32, P, I32, I64, F, I32, P, P, P, I32, I32, F, P, I64, P]
+    lib.rs_layer_norm_workspace.argtypes = [P, I64, I64, PI64]
     lib.rs_last_error.argtypes = []
     lib.rs_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -451,6 +455,94 @@ def rs_embed_grad(plan: Plan, tensor: int, ids: torch.Tensor, dy: torch.Tensor, 
                                 _code(dy), prev.data_ptr() if prev is not None else None, packed.data_ptr(),
                                 _code(packed), 0 if inv_v else 1, float(scale), work.data_ptr(), work.numel(),
                                 _stream(plan.device)))
+
+
+# ---------------------------------------------------------------- layer norm
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _tensor_number(plan: Plan, tensor: int, what: str) -> int:
+    if not 0 <= int(tensor) < len(plan.specs):
+        raise ValueError(f"{what}: no tensor {tensor} in a plan of {len(plan.specs)}")
+    return int(tensor)
+
+
+def _norm_rows(plan: Plan, weight: int, bias: Optional[int], **rows: torch.Tensor) -> int:
+    """(rows) of a layer norm call: every named buffer holds the same number of rows of the weight's size."""
+    cols = plan.numels[_tensor_number(plan, weight, "weight")]
+    if bias is not None:
+        _tensor_number(plan, bias, "bias")
+    sizes = set()
+    for name, t in rows.items():
+        if t.dtype not in _FLOATS:
+            raise ValueError(f"{name}: fp32 or bf16")
+        if t.numel() % cols:
+            raise ValueError(f"{name}: rows of {cols} columns")
+        sizes.add(t.numel() // cols)
+    if len(sizes) != 1:
+        raise ValueError(f"{', '.join(rows)}: different numbers of rows")
+    return sizes.pop()
+
+
+def rs_layer_norm(plan: Plan, weight: int, gathered: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                  bias: Optional[int] = None, eps: float = 1e-5, center: bool = True):
+    """y <- the layer norm of x's rows, with tensor number `weight` of the gathered flat buffer (fp32
+    or bf16) as its weight and tensor number `bias`, if any, added; center=False: the RMS norm."""
+    n = _norm_rows(plan, weight, bias, x=x, y=y)
+    _dev_check(plan, gathered, x, y)
+    _flat_check(plan, gathered, _FLOATS, "gathered")
+    _apart_check(gathered=gathered, y=y)
+    _apart_check(x=x, y=y)
+    _check(load().rs_layer_norm(plan.handle, int(weight), -1 if bias is None else int(bias), gathered.data_ptr(),
+                                _code(gathered), x.data_ptr(), _code(x), n, float(eps), int(bool(center)), y.data_ptr(),
+                                _code(y), _stream(plan.device)))
+
+
+def rs_layer_norm_workspace(plan: Plan, weight: int, n_rows: int) -> torch.Tensor:
+    """Workspace for rs_layer_norm_grad with up to n_rows rows (uint8, on the plan's device). Calls
+    that may overlap need a workspace each."""
+    n = ctypes.c_int64()
+    _check(load().rs_layer_norm_workspace(plan.handle, int(weight), int(n_rows), ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=f"cuda:{plan.device}")
+
+
+def _gradient_check(plan: Plan, inputs, outputs, packed, work, prev):
+    """The buffers of a call that writes gradients: outputs apart from each other and from the inputs,
+    which may share memory; prev may be packed (fp32)."""
+    _flat_check(plan, packed, _FLOATS, "packed")
+    if work.dtype != torch.uint8:      # its size is checked by the call itself
+        raise ValueError("work: uint8")
+    outputs = dict(outputs, packed=packed, work=work)
+    if prev is not None:
+        _flat_check(plan, prev, (torch.float32,), "prev")
+        if prev.data_ptr() != packed.data_ptr() or packed.dtype != torch.float32:
+            inputs = dict(inputs, prev=prev)
+        else:      # in place, and of the same length as far as the call is concerned
+            outputs["packed"] = prev if prev.numel() > packed.numel() else packed
+    _apart_check(**outputs)
+    for name, t in inputs.items():
+        _apart_check(**outputs, **{name: t})
+
+
+def rs_layer_norm_grad(plan: Plan, weight: int, gathered: torch.Tensor, x: torch.Tensor, dy: torch.Tensor,
+                       dx: torch.Tensor, packed: torch.Tensor, work: torch.Tensor, bias: Optional[int] = None,
+                       eps: float = 1e-5, center: bool = True, prev: Optional[torch.Tensor] = None, scale: float = 1.0,
+                       inv_v: bool = False):
+    """Gradients of rs_layer_norm: dx (x's dtype), and on the intervals of the weight (and bias)
+    packed <- [prev +] sigma * their gradients, sigma = scale, or scale / V with inv_v. prev=packed
+    (fp32) adds in place."""
+    n = _norm_rows(plan, weight, bias, x=x, dy=dy, dx=dx)
+    if dx.dtype != x.dtype:
+        raise ValueError("dx has x's dtype")
+    _dev_check(plan, gathered, x, dy, dx, packed, work, prev)
+    _flat_check(plan, gathered, _FLOATS, "gathered")
+    _gradient_check(plan, {"gathered": gathered, "x": x, "dy": dy}, {"dx": dx}, packed, work, prev)
+    _check(load().rs_layer_norm_grad(plan.handle, int(weight), -1 if bias is None else int(bias), gathered.data_ptr(),
+                                     _code(gathered), x.data_ptr(), _code(x), dy.data_ptr(), _code(dy), n, float(eps),
+                                     int(bool(center)), dx.data_ptr(), prev.data_ptr() if prev is not None else None,
+                                     packed.data_ptr(), _code(packed), 0 if inv_v else 1, float(scale), work.data_ptr(),
+                                     work.numel(), _stream(plan.device)))
 
 
 # ---------------------------------------------------------------- whole matrices
