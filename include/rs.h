@@ -31,6 +31,13 @@
  *   rs_layer_norm_grad  its gradient, the parameters' straight into the
  *                       packed buffer
  *   rs_layer_norm_workspace  bytes of workspace rs_layer_norm_grad needs
+ *   rs_head_loss        softmax cross entropy of a vocabulary head whose table
+ *                       is in the gathered buffer, without handing out logits
+ *   rs_head_grad        the same with its gradients, the table's straight into
+ *                       the packed buffer
+ *   rs_distill_loss     divergence of that head from a teacher's top logits
+ *   rs_distill_grad     the same with its gradients
+ *   rs_head_workspace   bytes of workspace these four need
  *   rs_orthogonalize    Newton-Schulz orthogonalisation of the WHOLE matrices
  *   rs_muon_step        one Muon step on the WHOLE matrices
  *   rs_muon_workspace   bytes of workspace the two need
@@ -451,6 +458,87 @@ int rs_layer_norm_grad(rs_plan* plan, int64_t weight, int64_t bias, const void* 
 /* Bytes of workspace for rs_layer_norm_grad on n_rows rows, or fewer. Errors:
  * RS_EINVAL, RS_ERANGE. */
 int rs_layer_norm_workspace(const rs_plan* plan, int64_t weight, int64_t n_rows, int64_t* bytes);
+
+/* Softmax cross entropy of a vocabulary head, straight from the gathered
+ * buffer (feynmanwiki walkthrough, DBuffer paragraphs: a tensor is its planned
+ * slice). With W = tensor `tensor` of the plan, rows x cols, and y = targets[t]:
+ *   l = scale * (W x_t),   loss[t] = log(sum over r of exp(l_r)) - l_y
+ * A target outside [0, rows) (e.g. -100) is none: its loss is +0.0, its x is
+ * not read, and it costs next to nothing. The logits live in the workspace at
+ * most. Products of bf16 values with fp32 sums; everything else is fp32. Sums
+ * have a fixed order: the same call gives the same bits. A NaN or an infinity
+ * in x_t makes loss[t] NaN (one in W may make all of them NaN).
+ * Any block kind but RS_TILEMAJOR. gathered: device, R_mat*S bf16 elements. x:
+ * device, n_tokens x cols bf16, row-major. targets: device, n_tokens signed
+ * integers of id_bytes (4 or 8) bytes, aligned to their size. scale: finite.
+ * loss: device, n_tokens fp32. piece: tokens worked on at a time, a multiple of
+ * 256 up to 65536, or 0 for up to 4096; it bounds the workspace, and results
+ * may differ in the last bits with it. work: device memory of rs_head_workspace
+ * bytes, contents not kept between calls; calls that may overlap need a
+ * workspace each. All but targets 16-byte aligned; outputs and workspace
+ * overlap neither inputs nor each other. n_tokens may be 0.
+ * Limits (RS_ERANGE): n_tokens at most 2^20, rows 2^21, cols 2^16, rows * cols
+ * and n_tokens * cols 2^33, n_tokens * top 2^28.
+ * Errors: RS_EINVAL, RS_EALIGN, RS_EDTYPE, RS_ERANGE, RS_EHIP. */
+int rs_head_loss(rs_plan* plan, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens,
+                 const void* targets, int32_t id_bytes, float scale, float* loss, int64_t piece, void* work,
+                 int64_t work_bytes, void* stream);
+
+/* The losses of rs_head_loss and the gradients of sum over t of w_t * loss[t],
+ * w_t = weights[t] (1 where weights is NULL). With p the softmax of l, e_y the
+ * unit vector of the target and a_t = w_t * scale:
+ *   dx_t = a_t * W^T (p - e_y), rounded once to bf16
+ *   packed = [prev +] sigma * sum over t of a_t * (p - e_y) x_t^T
+ * on W's interval, sigma = grad_scale (RS_SCALE_GIVEN) or fl32(grad_scale / V)
+ * (RS_SCALE_INV_V). A token without a target gets a dx of +0.0 and adds nothing,
+ * and neither does one of weight 0, whatever its x holds. p - e_y is computed in
+ * fp32; for dx it is rounded to bf16, for the table's gradient to fp16 (a bf16
+ * packed buffer) or to 22 bits (fp32), below a few 2^-24 of the largest
+ * a_t it loses bits, as x does below 2^-28 of the largest |x|. Sums are fp32.
+ * W's interval is written whole (with n_tokens = 0 too; with prev = packed and
+ * no targets it is left alone); other positions are left alone.
+ * weights: device, n_tokens fp32, or NULL. dx: device, n_tokens x cols bf16.
+ * prev: device fp32 R_mat*S or NULL; it may equal packed (fp32 only) to add in
+ * place, and must not overlap it in any other way. packed: device R_mat*S of
+ * packed_dt (RS_F32 or RS_BF16). The rest, limits and errors as above. */
+int rs_head_grad(rs_plan* plan, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens,
+                 const void* targets, int32_t id_bytes, const float* weights, float scale, float* loss, void* dx,
+                 const float* prev, void* packed, int32_t packed_dt, int32_t scale_mode, float grad_scale, int64_t piece,
+                 void* work, int64_t work_bytes, void* stream);
+
+/* Distillation of the same head from the `top` (1 to 256) largest logits that
+ * a teacher gave each token: teacher[t, k] for row ids[t, k] of the table. With
+ * T = temperature, l as above and q the softmax of teacher[t] / T over the
+ * token's places:
+ *   loss[t] = T^2 * sum over k of q_k * (log q_k - log softmax(l / T)[ids[t, k]])
+ * Places whose id is outside [0, rows) or whose logit is -inf are empty; a token
+ * with none left is one without a target, as above. A row named twice counts
+ * with both its shares. A teacher's logit of NaN or +inf makes the token's loss
+ * NaN. ids: device, n_tokens x top integers of id_bytes; teacher: device,
+ * n_tokens x top of teacher_dt (RS_F32 or RS_BF16), 16-byte aligned.
+ * temperature: finite, above 0, as is its square. The rest as in rs_head_loss. */
+int rs_distill_loss(rs_plan* plan, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* ids,
+                    int32_t id_bytes, const void* teacher, int32_t teacher_dt, int64_t top, float temperature, float scale,
+                    float* loss, int64_t piece, void* work, int64_t work_bytes, void* stream);
+
+/* The losses of rs_distill_loss and the gradients of their weighted sum as in
+ * rs_head_grad, with p = softmax(l / T), q in e_y's place and
+ * a_t = w_t * T * scale. The teacher's logits get no gradient. */
+int rs_distill_grad(rs_plan* plan, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* ids,
+                    int32_t id_bytes, const void* teacher, int32_t teacher_dt, int64_t top, const float* weights,
+                    float temperature, float scale, float* loss, void* dx, const float* prev, void* packed,
+                    int32_t packed_dt, int32_t scale_mode, float grad_scale, int64_t piece, void* work, int64_t work_bytes,
+                    void* stream);
+
+/* Bytes of workspace for the four calls on this tensor: n_tokens, piece and
+ * top (0 for labels) as in the call; grad 1 for the gradients (a workspace that
+ * also serves the losses), packed_dt the packed buffer's type. About
+ * 4 n cols + 8 n top for the tokens; rows * cols * 2 more where cols is no
+ * multiple of 64; for gradients piece * rows * 6, at most 256 MiB for parts of
+ * dx, and rows * cols * 4 more for a bf16 packed buffer and more than one piece.
+ * Errors: RS_EINVAL, RS_EDTYPE, RS_ERANGE. */
+int rs_head_workspace(const rs_plan* plan, int64_t tensor, int64_t n_tokens, int64_t top, int32_t grad, int32_t packed_dt,
+                      int64_t piece, int64_t* bytes);
 
 /* Orthogonalisation of every matrix of the plan by Newton-Schulz products
  * (feynmanwiki walkthrough, Muon paragraphs: the rank that holds a matrix

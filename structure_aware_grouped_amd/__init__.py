@@ -15,9 +15,14 @@ from .binding import (  # noqa: F401
     rs_block_dequant,
     rs_block_quant,
     rs_block_quant_noalloc,
+    rs_distill_grad,
+    rs_distill_loss,
     rs_embed_grad,
     rs_embed_rows,
     rs_embed_workspace,
+    rs_head_grad,
+    rs_head_loss,
+    rs_head_workspace,
     rs_layer_norm,
     rs_layer_norm_grad,
     rs_layer_norm_workspace,

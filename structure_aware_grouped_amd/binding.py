@@ -29,7 +29,8 @@ EXPORTS = ("rs_plan_build", "rs_plan_load", "rs_plan_load_with", "rs_plan_info",
            "rs_pack_scatter", "rs_block_quant", "rs_block_dequant", "rs_unpack_dequant", "rs_adam8_step",
            "rs_last_error", "rs_block_quant_noalloc", "rs_orthogonalize", "rs_muon_step", "rs_muon_workspace",
            "rs_embed_rows", "rs_embed_grad", "rs_embed_workspace", "rs_layer_norm", "rs_layer_norm_grad",
-           "rs_layer_norm_workspace")
+           "rs_layer_norm_workspace", "rs_head_loss", "rs_head_grad", "rs_distill_loss", "rs_distill_grad",
+           "rs_head_workspace")
 
 
 class RsError(RuntimeError):
@@ -100,6 +101,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rs_layer_norm.argtypes = [P, I64, I64, P, I32, P, I32, I64, F, I32, P, I32, P]
     lib.rs_layer_norm_grad.argtypes = [P, I64, I64, P, I32, P, I32, P, I32, I64, F, I32, P, P, P, I32, I32, F, P, I64, P]
     lib.rs_layer_norm_workspace.argtypes = [P, I64, I64, PI64]
+    lib.rs_head_loss.argtypes = [P, I64, P, P, I64, P, I32, F, P, I64, P, I64, P]
+    lib.rs_head_grad.argtypes = [P, I64, P, P, I64, P, I32, P, F, P, P, P, P, I32, I32, F, I64, P, I64, P]
+    lib.rs_distill_loss.argtypes = [P, I64, P, P, I64, P, I32, P, I32, I64, F, F, P, I64, P, I64, P]
+    lib.rs_distill_grad.argtypes = [P, I64, P, P, I64, P, I32, P, I32, I64, P, F, F, P, P, P, P, I32, I32, F, I64, P, I64, P]
+    lib.rs_head_workspace.argtypes = [P, I64, I64, I64, I32, I32, I64, PI64]
     lib.rs_last_error.argtypes = []
     lib.rs_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -543,6 +549,119 @@ def rs_layer_norm_grad(plan: Plan, weight: int, gathered: torch.Tensor, x: torch
                                      int(bool(center)), dx.data_ptr(), prev.data_ptr() if prev is not None else None,
                                      packed.data_ptr(), _code(packed), 0 if inv_v else 1, float(scale), work.data_ptr(),
                                      work.numel(), _stream(plan.device)))
+
+
+# ---------------------------------------------------------------- the vocabulary head
+
+def rs_head_workspace(plan: Plan, tensor: int, n_tokens: int, top: int = 0, packed=None, piece: int = 0) -> torch.Tensor:
+    """Workspace (uint8, on the plan's device) for the head's calls with n_tokens tokens: for the
+    losses, or with packed (the packed buffer, or its dtype) for the gradients too. top: logits of
+    the teacher per token, 0 for labels. piece: tokens whose logits are held at a time (a multiple
+    of 256; 0: up to 4096), the same as in the call. Calls that may overlap need a workspace each."""
+    dt = packed.dtype if isinstance(packed, torch.Tensor) else packed
+    if dt not in (None,) + _FLOATS:
+        raise ValueError("packed: fp32 or bf16")
+    n = ctypes.c_int64()
+    _check(load().rs_head_workspace(plan.handle, int(tensor), int(n_tokens), int(top), int(dt is not None),
+                                    RS_BF16 if dt == torch.bfloat16 else RS_F32, int(piece), ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=f"cuda:{plan.device}")
+
+
+def _head_tokens(plan: Plan, tensor: int, gathered, x, ids, logits, loss, work) -> int:
+    """(tokens) of a call on the head: x has one row of the table's width per token."""
+    cols = int(plan.specs[_tensor_number(plan, tensor, "tensor")].cols)
+    _flat_check(plan, gathered, (torch.bfloat16,), "gathered")
+    if x.dtype != torch.bfloat16 or x.numel() % cols:
+        raise ValueError(f"x: bf16 rows of {cols} columns")
+    n = x.numel() // cols
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("targets: int32 or int64")
+    if logits is None:
+        if ids.numel() != n:
+            raise ValueError("targets: one per row of x")
+    elif logits.dtype not in _FLOATS or logits.shape != ids.shape or logits.dim() < 2 or ids.numel() != n * ids.shape[-1]:
+        raise ValueError("ids and logits: tokens x top, fp32 or bf16 logits")
+    if loss.dtype != torch.float32 or loss.numel() != n:
+        raise ValueError("loss: fp32, one per row of x")
+    if work.dtype != torch.uint8:      # its size is checked by the call itself
+        raise ValueError("work: uint8")
+    return n
+
+
+def _head_loss(plan, tensor, gathered, x, ids, logits, loss, work):
+    n = _head_tokens(plan, tensor, gathered, x, ids, logits, loss, work)
+    _dev_check(plan, gathered, x, ids, logits, loss, work)
+    for t in (gathered, x, ids, logits):
+        if t is not None:
+            _apart_check(input=t, loss=loss, work=work)
+    return n
+
+
+def _head_grad(plan, tensor, gathered, x, ids, logits, loss, dx, packed, work, weights, prev):
+    n = _head_tokens(plan, tensor, gathered, x, ids, logits, loss, work)
+    if dx.dtype != torch.bfloat16 or dx.numel() != x.numel():
+        raise ValueError("dx: bf16, of x's size")
+    if weights is not None and (weights.dtype != torch.float32 or weights.numel() != n):
+        raise ValueError("weights: fp32, one per row of x")
+    _dev_check(plan, gathered, x, ids, logits, loss, dx, packed, work, weights, prev)
+    inputs = {"gathered": gathered, "x": x, "ids": ids, "logits": logits, "weights": weights}
+    _gradient_check(plan, {k: t for k, t in inputs.items() if t is not None}, {"loss": loss, "dx": dx}, packed, work, prev)
+    return n
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+def rs_head_loss(plan: Plan, tensor: int, gathered: torch.Tensor, x: torch.Tensor, targets: torch.Tensor,
+                 loss: torch.Tensor, work: torch.Tensor, scale: float = 1.0, piece: int = 0):
+    """loss[t] <- the softmax cross entropy of scale * (table x_t) at targets[t], with tensor number
+    `tensor` of the gathered flat buffer (bf16) as the table; 0 where the target is outside the table."""
+    n = _head_loss(plan, tensor, gathered, x, targets, None, loss, work)
+    _check(load().rs_head_loss(plan.handle, int(tensor), gathered.data_ptr(), x.data_ptr(), n, targets.data_ptr(),
+                               targets.element_size(), float(scale), loss.data_ptr(), int(piece), work.data_ptr(),
+                               work.numel(), _stream(plan.device)))
+
+
+def rs_head_grad(plan: Plan, tensor: int, gathered: torch.Tensor, x: torch.Tensor, targets: torch.Tensor,
+                 loss: torch.Tensor, dx: torch.Tensor, packed: torch.Tensor, work: torch.Tensor,
+                 weights: Optional[torch.Tensor] = None, prev: Optional[torch.Tensor] = None, scale: float = 1.0,
+                 grad_scale: float = 1.0, inv_v: bool = False, piece: int = 0):
+    """The losses of rs_head_loss, and the gradients of sum weights[t] * loss[t] (weights: fp32, None
+    for ones): dx (bf16), and on the table's interval packed <- [prev +] sigma * the table's, sigma =
+    grad_scale, or grad_scale / V with inv_v. prev=packed (fp32) adds in place."""
+    n = _head_grad(plan, tensor, gathered, x, targets, None, loss, dx, packed, work, weights, prev)
+    _check(load().rs_head_grad(plan.handle, int(tensor), gathered.data_ptr(), x.data_ptr(), n, targets.data_ptr(),
+                               targets.element_size(), _ptr(weights), float(scale), loss.data_ptr(), dx.data_ptr(),
+                               _ptr(prev), packed.data_ptr(), _code(packed), 0 if inv_v else 1, float(grad_scale), int(piece),
+                               work.data_ptr(), work.numel(), _stream(plan.device)))
+
+
+def rs_distill_loss(plan: Plan, tensor: int, gathered: torch.Tensor, x: torch.Tensor, ids: torch.Tensor,
+                    logits: torch.Tensor, loss: torch.Tensor, work: torch.Tensor, temperature: float = 1.0,
+                    scale: float = 1.0, piece: int = 0):
+    """loss[t] <- temperature^2 * the divergence of the head's softmax from a teacher's, both at
+    `temperature`, the teacher's over its top logits alone: logits[t, k] (fp32 or bf16) at rows
+    ids[t, k] of the table; ids outside the table and logits of -inf are empty places."""
+    n = _head_loss(plan, tensor, gathered, x, ids, logits, loss, work)
+    _check(load().rs_distill_loss(plan.handle, int(tensor), gathered.data_ptr(), x.data_ptr(), n, ids.data_ptr(),
+                                  ids.element_size(), logits.data_ptr(), _code(logits), int(ids.shape[-1]),
+                                  float(temperature), float(scale), loss.data_ptr(), int(piece), work.data_ptr(),
+                                  work.numel(), _stream(plan.device)))
+
+
+def rs_distill_grad(plan: Plan, tensor: int, gathered: torch.Tensor, x: torch.Tensor, ids: torch.Tensor,
+                    logits: torch.Tensor, loss: torch.Tensor, dx: torch.Tensor, packed: torch.Tensor, work: torch.Tensor,
+                    weights: Optional[torch.Tensor] = None, prev: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                    scale: float = 1.0, grad_scale: float = 1.0, inv_v: bool = False, piece: int = 0):
+    """The losses of rs_distill_loss, and the gradients of their weighted sum as rs_head_grad gives
+    them (the teacher's logits get none)."""
+    n = _head_grad(plan, tensor, gathered, x, ids, logits, loss, dx, packed, work, weights, prev)
+    _check(load().rs_distill_grad(plan.handle, int(tensor), gathered.data_ptr(), x.data_ptr(), n, ids.data_ptr(),
+                                  ids.element_size(), logits.data_ptr(), _code(logits), int(ids.shape[-1]), _ptr(weights),
+                                  float(temperature), float(scale), loss.data_ptr(), dx.data_ptr(), _ptr(prev),
+                                  packed.data_ptr(), _code(packed), 0 if inv_v else 1, float(grad_scale), int(piece),
+                                  work.data_ptr(), work.numel(), _stream(plan.device)))
 
 
 # ---------------------------------------------------------------- whole matrices

@@ -1,0 +1,1180 @@
+// The vocabulary head's losses with the head's table read from the gathered
+// flat buffer and its gradient written into the packed one, on gfx950: kernels
+// and the rs_head_loss / rs_head_grad / rs_distill_loss / rs_distill_grad /
+// rs_head_workspace entry points ("veScale-FSDP: flexible, structure-aware
+// sharding at 10K-GPU scale", feynmanwiki walkthrough, DBuffer paragraphs: a
+// tensor is its planned slice, and scale / add / zero ahead of the reduction).
+//
+// Mathematics. With W the table (V rows of H columns), x_t a token's hidden
+// state, c the factor on the logits and q_t the wanted distribution (one row of
+// the table, or the softmax of a teacher's top logits):
+//   l_t = c W x_t,  Z_t = log sum exp l_t,  p_t = exp(l_t - Z_t)
+//   loss_t = f (sum_k q_k log q_k + Z_t - sum_k q_k l_k)
+// and with d_t = p_t - q_t and a_t = weight_t f c, the gradients of
+// sum weight_t loss_t:
+//   dx_t = a_t W^T d_t,   dW = sum_t a_t d_t x_t^T.
+// These are three products; nothing is computed twice. Tokens are taken in
+// pieces: a piece's logits are stored (fp32) with each row's running maximum
+// and sum per 128 columns, become d in place, and are used up by the piece's two
+// gradient products. Tokens without a target take part in none of them: the
+// others are brought together first.
+//
+// Number formats. The logits' product takes the bf16 operands as they are, with
+// fp32 sums. d is computed in fp32 and rounded once for each of the two
+// products that read it: to bf16 for dx, whose result is bf16 too and whose
+// other operand is the table as gathered (range of bf16, no copy); to fp16,
+// eight times finer, for dW, with x scaled to fp16 by a power of two. Where the
+// packed buffer is fp32, d has a second fp16 part that holds the rest of the
+// first, and its product comes ahead of the first's: the result is then as
+// near as fp32 products'.
+#include "host_common.h"
+#include "mfma.h"
+
+#include <type_traits>
+
+namespace rs {
+namespace {
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kTileM = 256;          // rows of an output tile: its contiguous dimension in memory
+constexpr int kStepK = 64;           // of the contraction, per stage
+constexpr int kProductThreads = 512;
+constexpr int kProductWaves = kProductThreads / kWave;
+constexpr int kPart = 128;           // columns of d whose fp16 parts lie beside each other
+constexpr float kLog2e = 1.44269504088896341f;
+
+// ------------------------------------------------------------------ products
+
+// C[m, n] = sum_k P[m, k] Q[n, k] on one 256 x BN tile by 8 waves, 32 x 32
+// accumulators. Either operand may lie with k contiguous (plain) or with its
+// other index contiguous (TR): a TR operand is read out of LDS transposed
+// (ds_read_b64_tr_b16), so the table and d are used as they lie in memory.
+template <int BN>
+struct HeadTile {
+  static constexpr int WR = BN == 256 ? 2 : 4;              // wave rows
+  static constexpr int WC = kProductWaves / WR;
+  static constexpr int NI = kTileM / 32 / WR, NJ = BN / 32 / WC;
+  static constexpr int kStages = BN == 256 ? 2 : 3;
+  static constexpr int kLds = kStages * (kTileM + BN) * kStepK * 2;
+};
+
+// One operand's tile: from `base` on, `left` bytes may be read. Plain: `rows`
+// rows exist (those past them repeat the last), and the contraction is padded.
+// TR: `rows` values of k exist, at least one (those past them repeat the last:
+// the other operand holds zeros there). PARTS: see Fetch.
+struct Operand {
+  const char* base;
+  int64_t left;
+  int pitch, rows;
+};
+
+// Memory to LDS, 16 bytes per lane and load. Plain: 128-byte rows, piece c of
+// row r at place c ^ (r / 2 % 8). TR: rows of SIDE * 2 bytes, one per k, piece c
+// of row k at place c ^ (4 * (k % 4)), so that the four rows that 32 lanes of a
+// transposed read touch fall into banks of their own.
+//   PARTS: the operand is the fp16 parts of d, kPart columns of each beside each
+// other.
+template <int SIDE, bool TR, bool PARTS>
+struct Fetch {
+  static constexpr int kBytes = SIDE * kStepK * 2;
+  static constexpr int kLoads = kBytes / 1024 / kProductWaves;
+  static constexpr int kRowLanes = TR ? SIDE / 8 : 8;        // lanes that load one row
+  int off[kLoads];
+
+  __device__ static __forceinline__ int row(int t, int wave, int lane) {
+    return (t * kProductWaves + wave) * (kWave / kRowLanes) + lane / kRowLanes;
+  }
+  __device__ static __forceinline__ int piece(int r, int lane) {
+    const int c = (lane % kRowLanes) ^ (TR ? 4 * (r % 4) : r / 2 % 8);
+    return PARTS ? c / 16 * 512 + c % 16 * 16 : c * 16;
+  }
+  __device__ __forceinline__ void init(const Operand& o, int wave, int lane) {
+#pragma unroll
+    for (int t = 0; t < kLoads; ++t) {
+      const int r = row(t, wave, lane);
+      off[t] = (TR ? r : min(r, o.rows - 1)) * o.pitch + piece(r, lane);
+    }
+  }
+  // Stage k of the contraction; `more`: bytes that all of it lies further on.
+  __device__ __forceinline__ void load(const Operand& o, int k, int64_t more, lds_char* dst, int wave, int lane) const {
+    const int first = TR ? min(k * kStepK, o.rows - 1) : 0;
+    const int64_t at = more + (TR ? static_cast<int64_t>(first) * o.pitch : static_cast<int64_t>(k) * (kStepK * 2));
+    const int64_t left = o.left - at;
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(o.base + at), 0,
+                                          static_cast<int>(left < 0x7fffffff ? left : 0x7fffffff), kRawBufferWord3);
+    const int rows = o.rows - first;
+    const bool whole = !TR || (first == k * kStepK && rows >= kStepK);
+#pragma unroll
+    for (int t = 0; t < kLoads; ++t) {
+      int mine = off[t];
+      if (!whole) {
+        const int r = row(t, wave, lane);
+        mine = min(r, rows - 1) * o.pitch + piece(r, lane);
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst + (t * kProductWaves + wave) * 1024, 16, mine, 0, 0, 0);
+    }
+  }
+};
+
+// LDS to fragments: 32 rows (m or n) by 16 k, lane l has row l % 32 and the 8
+// values of k from 8 * (l / 32) on. A transposed read gives each lane of 16 the
+// column of its number of a 4 x 16 block, so a fragment takes two.
+template <int SIDE, bool TR, int N>
+struct Fragments {
+  static constexpr int kBytes = SIDE * kStepK * 2;
+  const char* at[TR ? N : 4];
+
+  __device__ __forceinline__ void init(const char* lds, int first, int lane) {   // first: the wave's first 32-row block
+    if constexpr (TR) {
+      const int i = lane % 16, g = lane / 16, k = g / 2 * 8 + i / 4;
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        const int piece = (first + b) * 4 + g % 2 * 2 + i % 4 / 2;
+        at[b] = lds + k * SIDE * 2 + (piece ^ (4 * (k % 4))) * 16 + i % 2 * 8;
+      }
+    } else {
+      const int r = lane % 32;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        at[kk] = lds + first * 4096 + r * 128 + ((kk * 2 + lane / 32) ^ (r / 2 % 8)) * 16;
+    }
+  }
+  __device__ __forceinline__ u32x4 read(int b, int kk, int stage) const {
+    if constexpr (TR) {
+      const char* p = at[b] + stage * kBytes + kk * 16 * SIDE * 2;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(p + 4 * SIDE * 2));
+      const u32x2 a = __builtin_bit_cast(u32x2, lo), c = __builtin_bit_cast(u32x2, hi);
+      return u32x4{a.x, a.y, c.x, c.y};
+    } else {
+      return *reinterpret_cast<const u32x4*>(at[kk] + stage * kBytes + b * 4096);
+    }
+  }
+};
+
+template <int BN>
+struct HeadAcc {
+  f32x16 v[HeadTile<BN>::NI][HeadTile<BN>::NJ];
+};
+
+// The contraction, in `ksteps` stages. With `two`, after the first half of them
+// P starts over and Q starts over at its other part, `second` bytes further on.
+template <int BN, bool F16, bool PT, bool QT, bool PARTS>
+__device__ __forceinline__ void multiply(const Operand& p, const Operand& q, int ksteps, bool two, int64_t second, char* lds, HeadAcc<BN>& c) {
+  using T = HeadTile<BN>;
+  const int tid = fresh_thread(), lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  Fetch<kTileM, PT, false> fp;
+  Fetch<BN, QT, PARTS> fq;
+  constexpr int kPBytes = decltype(fp)::kBytes, kQBytes = decltype(fq)::kBytes, S = T::kStages;
+  constexpr int kLoads = decltype(fp)::kLoads + decltype(fq)::kLoads;
+  fp.init(p, wave, lane);
+  fq.init(q, wave, lane);
+  const int turn = two ? ksteps / 2 : ksteps;
+  lds_char* base = (lds_char*)lds;
+  auto load = [&](int s, int stage) {
+    const int k = s < turn ? s : s - turn;
+    fp.load(p, k, 0, base + stage * kPBytes, wave, lane);
+    fq.load(q, k, s < turn ? 0 : second, base + S * kPBytes + stage * kQBytes, wave, lane);
+  };
+  Fragments<kTileM, PT, T::NI> rp;
+  Fragments<BN, QT, T::NJ> rq;
+  rp.init(lds, wave / T::WC * T::NI, lane);
+  rq.init(lds + S * kPBytes, wave % T::WC * T::NJ, lane);
+  u32x4 fa[2][T::NI], fb[2][T::NJ];
+  auto fetch = [&](int stage, int kk, int to) {
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j) fb[to][j] = rq.read(j, kk, stage);
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i) fa[to][i] = rp.read(i, kk, stage);
+  };
+  auto mma = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+      for (int j = 0; j < T::NJ; ++j) {
+        if constexpr (F16)
+          c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, fa[from][i]), __builtin_bit_cast(h8, fb[from][j]),
+                                                             c.v[i][j], 0, 0, 0);
+        else
+          c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, fa[from][i]), __builtin_bit_cast(b8, fb[from][j]),
+                                                              c.v[i][j], 0, 0, 0);
+      }
+  };
+  // fragment reads spread over the multiplications, so that none of them waits
+  constexpr int kReads = T::NI * (PT ? 2 : 1) + T::NJ * (QT ? 2 : 1), kMuls = T::NI * T::NJ;
+  constexpr int kEach = (kReads + kMuls - 1) / kMuls;
+  auto interleave = [&]() {
+#pragma unroll
+    for (int i = 0; i < kMuls; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);   // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // one multiplication
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // One stage: three sixteen-column multiplications, each while the next
+  // fragment is read; then, with every wave done reading this stage and the
+  // next one arrived (full: later ones may still be on their way), the loads
+  // into this stage and the next stage's first fragment, under the fourth.
+  auto step = [&](int s, int stage, int next, bool full, bool more_loads, bool more) {
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      fetch(stage, kk + 1, (kk + 1) & 1);
+      mma(kk & 1);
+      interleave();
+    }
+    if (full) wait<(S - 2) * kLoads, true>();
+    else wait<0, true>();
+    barrier();
+    if (more) fetch(next, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (more_loads) load(s + S, stage);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(1);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (ksteps == 0) return;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < ksteps) load(s, s);
+  if (ksteps >= S) wait<(S - 1) * kLoads, false>();
+  else wait<0, false>();
+  barrier();
+  fetch(0, 0, 0);
+  int s = 0;
+  for (; s + 2 * S - 1 < ksteps; s += S) {
+#pragma unroll
+    for (int u = 0; u < S; ++u) step(s + u, u, (u + 1) % S, true, true, true);
+  }
+  for (; s < ksteps; ++s) step(s, s % S, (s + 1) % S, s + S <= ksteps, s + S < ksteps, s + 1 < ksteps);
+}
+
+// Tile number `o` of m_tiles x n_tiles, eight m tiles beside each other within
+// a band, so that the 32 neighbours that an XCD's CUs work on at a time share
+// operands in its L2.
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int o, int across, int along, bool m_across) {
+  constexpr int kBand = 8;
+  const int band = o / (kBand * along), rest = o - band * kBand * along;
+  const int wide = min(kBand, across - band * kBand);
+  const int a = band * kBand + rest % wide, b = rest / wide;
+  return m_across ? TileAt{a, b} : TileAt{b, a};
+}
+
+// Work item of this workgroup out of n: workgroup b runs on XCD b % 8, and each
+// XCD takes a contiguous eighth. -1: none.
+__device__ __forceinline__ int xcd_item(int n) {
+  const int per = (n + 7) / 8, slot = static_cast<int>(blockIdx.x) / 8;
+  const int o = static_cast<int>(blockIdx.x) % 8 * per + slot;
+  return slot < per && o < n ? o : -1;
+}
+
+// ------------------------------------------------------------------ call
+
+// What the tokens of a call come to, known on the device only.
+struct HeadInfo {
+  int32_t count;     // tokens with a target
+  int32_t ex, ec;    // |x| < 2^ex and |a_t| < 2^ec over them
+  int32_t pad;
+};
+struct HeadPiece {
+  int32_t count;     // of this piece's tokens
+  int32_t splits;    // of the contraction of dx
+};
+
+// A call as the kernels see it. Kept tokens are numbered 0.. count-1 in their
+// own order; arrays "by token" have n entries, arrays "by place" have npad.
+struct Head {
+  int32_t n, npad, rows, cols, vp, hp, top, piece;   // vp, hp: rows and columns padded
+  const char* table;      // bf16, pitch bytes a row
+  int32_t pitch;
+  int64_t table_bytes;
+  HeadInfo* info;
+  HeadPiece* pieces;
+  uint32_t* keep;         // by token: has a target
+  float *xmax, *ent;      // by token: largest finite |x|, sum q log q
+  int32_t* idx;           // by token, top each: row of the table or -1
+  float* q;
+  int32_t* kept;          // by place: the token
+  float *pent, *a, *lse;  // by place
+  int32_t* pidx;          // top rows of npad
+  float *pq, *picked;     // the same: q and the logit there
+  char *xb, *xh;          // by place: x in bf16 and scaled in fp16, hp columns
+  float2* stat;           // of one piece: per 32 * NI rows of the table, `piece` maxima and sums
+  float* logits;          // of one piece: piece x vp, then the fp16 parts of d
+  uint16_t* d;            // of one piece: bf16
+  char* slabs;
+};
+
+// ------------------------------------------------------------------ targets
+
+constexpr int kMaxTop = 256;
+
+// One token a wave: its rows of the table and their share q, whether it has
+// any, and the largest finite |x| (GRAD). A token without a target gets its
+// loss (and dx) of zero here.
+template <bool GRAD>
+__global__ __launch_bounds__(kThreads) void head_targets_kernel(Head h, const void* ids, bool wide, const void* teacher,
+                                                                bool teacher16, float temperature, const uint16_t* x, float* loss,
+                                                                uint16_t* dx) {
+  const int lane = threadIdx.x % kWave;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / kWave) + threadIdx.x / kWave;
+  if (t >= h.n) return;
+  constexpr int kSlots = kMaxTop / kWave;
+  int row[kSlots];
+  float z[kSlots], top = -INFINITY;
+  const int k = max(h.top, 1);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int s = i * kWave + lane;
+    row[i] = -1;
+    z[i] = -INFINITY;
+    if (s < k) {
+      const int64_t at = t * k + s;
+      const int64_t v = wide ? static_cast<const int64_t*>(ids)[at] : static_cast<const int32_t*>(ids)[at];
+      if (v >= 0 && v < h.rows) {
+        row[i] = static_cast<int>(v);
+        z[i] = !teacher ? 0.0f : teacher16 ? In<true>::elem(teacher, at) : In<false>::elem(teacher, at);
+      }
+    }
+    top = fmaxf(top, z[i]);
+  }
+  bool some = false;   // a teacher's logit of -inf is no target, one of NaN is
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) some |= row[i] >= 0 && !(z[i] == -INFINITY);
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
+  some = __any(some);
+  float sum = 0.0f, ent = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    z[i] = row[i] >= 0 && some ? expf((z[i] - top) / temperature) : 0.0f;
+    sum += z[i];
+  }
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int s = i * kWave + lane;
+    z[i] = some ? z[i] / sum : 0.0f;
+    if (!(z[i] == 0.0f)) ent += z[i] * logf(z[i]);
+    if (s < k) {
+      h.idx[t * k + s] = row[i];
+      h.q[t * k + s] = z[i];
+    }
+  }
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) ent += __shfl_xor(ent, o, kWave);
+  float most = 0.0f;
+  if constexpr (GRAD) {
+    const uint16_t* from = x + t * h.cols;
+    if (h.cols % 8 == 0) {
+      for (int c = lane * 8; c < h.cols; c += kWave * 8) {
+        float v[8];
+        In<true>::widen(*reinterpret_cast<const u32x4*>(from + c), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fabsf(v[e]) <= FLT_MAX ? fmaxf(most, fabsf(v[e])) : most;
+      }
+    } else {
+      for (int c = lane; c < h.cols; c += kWave) {
+        const float v = fabsf(In<true>::elem(from, c));
+        most = v <= FLT_MAX ? fmaxf(most, v) : most;
+      }
+    }
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, kWave));
+    if (!some) {
+      if (h.cols % 8 == 0)
+        for (int c = lane * 8; c < h.cols; c += kWave * 8) *reinterpret_cast<u32x4*>(dx + t * h.cols + c) = u32x4{};
+      else
+        for (int c = lane; c < h.cols; c += kWave) dx[t * h.cols + c] = 0;
+    }
+  }
+  if (lane == 0) {
+    h.keep[t] = some;
+    h.ent[t] = ent;
+    h.xmax[t] = most;
+    if (!some) loss[t] = 0.0f;
+  }
+}
+
+// Parts of the contraction of dx: none, or as many as fill one to four rounds of
+// the 256 CUs, whichever makes the launch shortest, counted in stages, with six
+// for a part's ends; at least four stages a part. At most kMaxSlabs workgroups
+// have a part each, which bounds the slabs.
+constexpr int kMaxSlabs = 1024;
+__host__ __device__ inline int dx_splits(int tiles, int ksteps) {
+  if (tiles <= 0) return 1;
+  int best = 1, least = (tiles + 255) / 256 * (ksteps + 6);
+  for (int round = 1; round <= kMaxSlabs / 256; ++round) {
+    int s = 256 * round / tiles;
+    s = s < ksteps / 4 ? s : ksteps / 4;
+    if (s < 2) continue;
+    const int cost = (s * tiles + 255) / 256 * ((ksteps + s - 1) / s + 6);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// The tokens with a target, in their order, by one workgroup; the exponents
+// that bound x and a; and the pieces.
+constexpr int kKeepThreads = 1024;
+__global__ __launch_bounds__(kKeepThreads) void head_keep_kernel(Head h, const float* weights, float factor, int n_pieces,
+                                                                 int dx_tiles_m, int tile_n) {
+  __shared__ int wave_sum[kKeepThreads / kWave];
+  __shared__ float wave_x[kKeepThreads / kWave], wave_a[kKeepThreads / kWave];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  int base = 0;
+  float most_x = 0.0f, most_a = 0.0f;
+  for (int t0 = 0; t0 < h.n; t0 += kKeepThreads) {
+    const int t = t0 + tid;
+    const bool mine = t < h.n && h.keep[t];
+    const uint64_t set = __ballot(mine);
+    if (lane == 0) wave_sum[wave] = __popcll(set);
+    __syncthreads();
+    int before = base, all = 0;
+    for (int w = 0; w < kKeepThreads / kWave; ++w) {
+      before += w < wave ? wave_sum[w] : 0;
+      all += wave_sum[w];
+    }
+    __syncthreads();
+    base += all;
+    if (mine) {
+      h.kept[before + __popcll(set & ((1ull << lane) - 1))] = t;
+      most_x = fmaxf(most_x, h.xmax[t]);
+      const float a = fabsf((weights ? weights[t] : 1.0f) * factor);
+      if (a <= FLT_MAX) most_a = fmaxf(most_a, a);
+    }
+  }
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) {
+    most_x = fmaxf(most_x, __shfl_xor(most_x, o, kWave));
+    most_a = fmaxf(most_a, __shfl_xor(most_a, o, kWave));
+  }
+  if (lane == 0) {
+    wave_x[wave] = most_x;
+    wave_a[wave] = most_a;
+  }
+  __syncthreads();
+  for (int w = 0; w < kKeepThreads / kWave; ++w) {
+    most_x = fmaxf(most_x, wave_x[w]);
+    most_a = fmaxf(most_a, wave_a[w]);
+  }
+  if (tid == 0) {
+    int ex = 0, ec = 0;
+    frexpf(most_x, &ex);   // 0 for 0
+    frexpf(most_a, &ec);
+    *h.info = HeadInfo{base, ex, ec, 0};
+  }
+  for (int p = tid; p < n_pieces; p += kKeepThreads) {
+    const int count = min(max(base - p * h.piece, 0), h.piece);
+    h.pieces[p] = HeadPiece{count, dx_splits(dx_tiles_m * ((count + tile_n - 1) / tile_n), h.vp / kStepK)};
+  }
+}
+
+// x of the kept tokens beside each other, as bf16 and (GRAD) scaled as fp16,
+// zeros in the padding of their columns and in the places up to the next
+// multiple of kStepK; and their targets. A token whose gradient has no weight
+// has zeros as fp16, whatever x holds.
+template <bool GRAD>
+__global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uint16_t* x, const float* weights, float factor) {
+  const int p = blockIdx.x, count = h.info->count;
+  if (p >= (count + kStepK - 1) / kStepK * kStepK) return;
+  const bool live = p < count;
+  const int64_t t = live ? h.kept[p] : 0;
+  const float a = live ? (weights ? weights[t] : 1.0f) * factor : 0.0f;
+  const int shift = 14 - h.info->ex;
+  if (live) {
+    const int k = max(h.top, 1);
+    for (int s = threadIdx.x; s < k; s += kThreads) {
+      h.pidx[static_cast<int64_t>(s) * h.npad + p] = h.idx[t * k + s];
+      h.pq[static_cast<int64_t>(s) * h.npad + p] = h.q[t * k + s];
+    }
+    if (threadIdx.x == 0) {
+      h.pent[p] = h.ent[t];
+      h.a[p] = a;
+    }
+  }
+  uint16_t* xb = reinterpret_cast<uint16_t*>(h.xb) + static_cast<int64_t>(p) * h.hp;
+  _Float16* xh = reinterpret_cast<_Float16*>(h.xh) + static_cast<int64_t>(p) * h.hp;
+  const bool vec = h.cols % 8 == 0;
+  for (int c = threadIdx.x * 8; c < h.hp; c += kThreads * 8) {
+    float v[8] = {};
+    u32x4 raw = {};
+    if (live && vec) {
+      if (c < h.cols) raw = *reinterpret_cast<const u32x4*>(x + t * h.cols + c);
+    } else if (live) {
+      uint32_t e16[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) e16[e] = c + e < h.cols ? x[t * h.cols + c + e] : 0u;
+      raw = u32x4{e16[0] | e16[1] << 16, e16[2] | e16[3] << 16, e16[4] | e16[5] << 16, e16[6] | e16[7] << 16};
+    }
+    *reinterpret_cast<u32x4*>(xb + c) = raw;
+    if constexpr (GRAD) {
+      In<true>::widen(raw, v);
+      h8 y;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = a == 0.0f ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(ldexpf(v[e], shift));
+      *reinterpret_cast<h8*>(xh + c) = y;
+    }
+  }
+}
+
+// The table with its rows padded, where their width is no multiple of kStepK.
+__global__ __launch_bounds__(kThreads) void head_widen_kernel(const uint16_t* table, int rows, int cols, int hp, uint16_t* out) {
+  const int per = hp / 8;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (u >= static_cast<int64_t>(rows) * per) return;
+  const int64_t r = u / per;
+  const int c = static_cast<int>(u - r * per) * 8;
+  const uint16_t* from = table + r * cols + c;
+  uint32_t v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? from[e] : 0u;
+  *reinterpret_cast<u32x4*>(out + r * hp + c) = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+}
+
+// ------------------------------------------------------------------ logits
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// One tile of the logits of a piece, 256 rows of the table by BN tokens: the
+// largest and the sum of exponentials over the wave's rows for each token, the
+// logits at its targets, and (STORE) the logits themselves, -inf behind the
+// table's end. A lane holds one token's logits, so the sums are its own and
+// the other half wave's.
+template <int BN, bool STORE>
+__global__ __launch_bounds__(kProductThreads) void head_logits_kernel(Head h, int piece, float factor) {
+  using T = HeadTile<BN>;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const int count = h.pieces[piece].count, m_tiles = h.vp / kTileM, n_tiles = (count + BN - 1) / BN;
+  const int o = xcd_item(m_tiles * n_tiles);
+  if (o < 0) return;
+  const TileAt at = tile_at(o, n_tiles, m_tiles, false);
+  const int v0 = at.m * kTileM, p0 = piece * h.piece + at.n * BN;
+  const int64_t row_bytes = static_cast<int64_t>(h.hp) * 2;
+  const int64_t from = static_cast<int64_t>(v0) * h.pitch;
+  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - v0};
+  const Operand q = {h.xb + p0 * row_bytes, BN * row_bytes, static_cast<int>(row_bytes), BN};
+  HeadAcc<BN> acc = {};
+  multiply<BN, false, false, false, false>(p, q, h.hp / kStepK, false, 0, lds, acc);
+  const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave, half = lane / 32;
+  const int first = v0 + wave / T::WC * T::NI * 32;   // the wave's first row of the table
+  const int k = max(h.top, 1);
+#pragma unroll
+  for (int j = 0; j < T::NJ; ++j) {
+    const int place = at.n * BN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;   // in the piece
+    const bool live = place < count;
+    const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int v = first + i * 32 + e / 4 * 8 + half * 4 + e % 4;
+        const float l = v < h.rows ? acc.v[i][j][e] * factor : -INFINITY;
+        acc.v[i][j][e] = l;
+        top = fmaxf(top, l);
+      }
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    const float base = top == -INFINITY ? 0.0f : top;   // only -inf and NaN: the sum says which
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum += exp_of(acc.v[i][j][e] - base);
+    sum += __shfl_xor(sum, 32, kWave);
+    if (live && half == 0) h.stat[static_cast<int64_t>(first / (32 * T::NI)) * h.piece + place] = float2{top, sum};
+    if (live) {
+      constexpr int kAhead = 8;   // targets looked at together: their loads do not wait for each other
+      for (int s0 = 0; s0 < k; s0 += kAhead) {
+        int r[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) r[u] = s0 + u < k ? h.pidx[static_cast<int64_t>(s0 + u) * h.npad + mine] - first : -1;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (r[u] < 0 || r[u] >= T::NI * 32 || r[u] / 4 % 2 != half) continue;
+          float l = 0.0f;
+#pragma unroll
+          for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) l = r[u] == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
+          h.picked[static_cast<int64_t>(s0 + u) * h.npad + mine] = l;
+        }
+      }
+    }
+    if constexpr (STORE) {
+      if (live) {
+        float* out = h.logits + static_cast<int64_t>(place) * h.vp + first + half * 4;
+#pragma unroll
+        for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<f32x4*>(out + i * 32 + e * 2) =
+                f32x4{acc.v[i][j][e], acc.v[i][j][e + 1], acc.v[i][j][e + 2], acc.v[i][j][e + 3]};
+      }
+    }
+  }
+}
+
+// Log-sum-exp and loss of kLossTokens tokens, 32 threads each.
+constexpr int kLossTokens = kThreads / 32;
+__global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, int stats, float factor, float* loss) {
+  __shared__ float tops[kLossTokens][33], sums[kLossTokens][33];
+  const int tok = threadIdx.x % kLossTokens, part = threadIdx.x / kLossTokens;
+  const int place = blockIdx.x * kLossTokens + tok, count = h.pieces[piece].count;
+  const bool live = place < count;
+  const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
+  float top = -INFINITY, sum = 0.0f;
+  bool broken = false;
+  auto add = [&](float t, float s) {
+    const float both = fmaxf(top, t), base = both == -INFINITY ? 0.0f : both;
+    broken |= !(s >= 0.0f);
+    sum = sum * exp_of(top - base) + s * exp_of(t - base);
+    top = both;
+  };
+  if (live)
+    for (int i = part; i < stats; i += 32) {
+      const float2 s = h.stat[static_cast<int64_t>(i) * h.piece + place];
+      add(s.x, s.y);
+    }
+  tops[tok][part] = top;
+  sums[tok][part] = broken ? NAN : sum;
+  __syncthreads();
+  if (part == 0 && live) {
+    top = -INFINITY;
+    sum = 0.0f;
+    for (int i = 0; i < 32; ++i) add(tops[tok][i], sums[tok][i]);
+    tops[tok][32] = h.lse[mine] = broken ? NAN : top + logf(sum);
+  }
+  __syncthreads();
+  const float z = tops[tok][32];
+  float l = 0.0f;
+  const int k = max(h.top, 1);
+  if (live)
+    for (int s = part; s < k; s += 32) {
+      const int64_t at = static_cast<int64_t>(s) * h.npad + mine;
+      const float q = h.pq[at];
+      if (h.pidx[at] >= 0 && !(q == 0.0f)) l += q * (z - h.picked[at]);
+    }
+  __syncthreads();
+  sums[tok][part] = l;
+  __syncthreads();
+  if (part || !live) return;
+  l = 0.0f;
+  for (int i = 0; i < min(k, 32); ++i) l += sums[tok][i];
+  loss[h.kept[mine]] = factor * (h.pent[mine] + l);
+}
+
+// ------------------------------------------------------------------ gradients
+
+// d = p - q of one token and kDeltaCols columns: bf16 for dx, and times the
+// token's share of the gradient, scaled, in fp16 parts for dW, where the logits
+// lay: 128 logits give way to 128 values of each part, and those that a wave
+// overwrites are its own, read before.
+constexpr int kDeltaCols = 8192;
+template <bool TWO>
+__global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece) {
+  __shared__ int row[kMaxTop];
+  __shared__ float share[kMaxTop];
+  const int count = h.pieces[piece].count, place = blockIdx.x;
+  if (place >= (count + kStepK - 1) / kStepK * kStepK) return;
+  const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
+  const bool live = place < count;
+  const float a = live ? h.a[mine] : 0.0f, z = live ? h.lse[mine] : 0.0f;
+  const bool zero = a == 0.0f;
+  const float g = ldexpf(a, 15 - h.info->ec);
+  float* logits = h.logits + static_cast<int64_t>(place) * h.vp;
+  uint16_t* d16 = h.d + static_cast<int64_t>(place) * h.vp;
+  const int k = max(h.top, 1), c0 = blockIdx.y * kDeltaCols, c1 = min(c0 + kDeltaCols, h.vp);
+  const int slot = threadIdx.x;
+  if (live && slot < k) {
+    row[slot] = h.pidx[static_cast<int64_t>(slot) * h.npad + mine];
+    share[slot] = h.pq[static_cast<int64_t>(slot) * h.npad + mine];
+  }
+  auto part = [&](int c) { return reinterpret_cast<_Float16*>(logits) + c / kPart * (2 * kPart) + c % kPart; };
+  for (int c = c0 + slot * 8; c < c1; c += kThreads * 8) {
+    u32x4 out = {};
+    h8 hi = {}, lo = {};
+    if (!zero) {
+      const f32x4 l0 = *reinterpret_cast<const f32x4*>(logits + c), l1 = *reinterpret_cast<const f32x4*>(logits + c + 4);
+      uint32_t b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p = exp_of((e < 4 ? l0[e] : l1[e - 4]) - z), y = p * g;
+        b[e] = bf16_rne(p);
+        hi[e] = static_cast<_Float16>(y);
+        lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
+      }
+      out = u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16};
+    }
+    *reinterpret_cast<u32x4*>(d16 + c) = out;
+    *reinterpret_cast<h8*>(part(c)) = hi;
+    if constexpr (TWO) *reinterpret_cast<h8*>(part(c) + kPart) = lo;
+  }
+  if (zero) return;
+  __syncthreads();   // the targets' columns again, with their share; the first of equal rows has all of it
+  if (slot >= k) return;
+  const int c = row[slot];
+  if (c < c0 || c >= c1) return;
+  float q = 0.0f;
+  for (int s = 0; s < k; ++s) {
+    if (row[s] != c) continue;
+    if (s < slot) return;
+    q += share[s];
+  }
+  const float p = exp_of(h.picked[static_cast<int64_t>(slot) * h.npad + mine] - z) - q, y = p * g;
+  d16[c] = static_cast<uint16_t>(bf16_rne(p));
+  const _Float16 hi = static_cast<_Float16>(y);
+  *part(c) = hi;
+  if constexpr (TWO) part(c)[kPart] = static_cast<_Float16>(y - static_cast<float>(hi));
+}
+
+// dx of a piece: 256 columns by BN tokens, one part of the contraction over the
+// table's rows. Sums go to the part's slab, in the registers' order.
+template <int BN>
+__global__ __launch_bounds__(kProductThreads) void head_dx_kernel(Head h, int piece) {
+  using T = HeadTile<BN>;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const HeadPiece info = h.pieces[piece];
+  const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = (info.count + BN - 1) / BN, tiles = m_tiles * n_tiles;
+  const int o = xcd_item(tiles * info.splits);
+  if (o < 0) return;
+  const int split = o / tiles;
+  const TileAt at = tile_at(o - split * tiles, m_tiles, n_tiles, true);
+  const int ksteps = h.vp / kStepK;
+  const int k0 = static_cast<int>(static_cast<int64_t>(ksteps) * split / info.splits);
+  const int k1 = static_cast<int>(static_cast<int64_t>(ksteps) * (split + 1) / info.splits);
+  // stages behind the table's last row repeat it; d is zero there
+  const int row = min(k0 * kStepK, h.rows - 1);
+  const int64_t from = static_cast<int64_t>(row) * h.pitch + at.m * (kTileM * 2);
+  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - row};
+  const int64_t row_bytes = static_cast<int64_t>(h.vp) * 2;
+  const Operand q = {reinterpret_cast<const char*>(h.d) + at.n * BN * row_bytes + k0 * (kStepK * 2), BN * row_bytes - k0 * (kStepK * 2),
+                     static_cast<int>(row_bytes), BN};
+  HeadAcc<BN> acc = {};
+  multiply<BN, false, true, false, false>(p, q, k1 - k0, false, 0, lds, acc);
+  char* out = h.slabs + static_cast<int64_t>(o) * (kTileM * BN * 4) + fresh_thread() * 16;
+#pragma unroll
+  for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<f32x4*>(out + ((i * T::NJ + j) * 4 + e / 4) * (kProductThreads * 16)) =
+            f32x4{acc.v[i][j][e], acc.v[i][j][e + 1], acc.v[i][j][e + 2], acc.v[i][j][e + 3]};
+}
+
+// dx of one 32-column block of a tile for each of its waves: the parts added in
+// their order, times a, rounded to bf16, to the tokens' own rows.
+template <int BN>
+__global__ __launch_bounds__(kProductThreads) void head_dx_sum_kernel(Head h, int piece, uint16_t* dx) {
+  using T = HeadTile<BN>;
+  constexpr int kBlocks = T::NI * T::NJ * 4;
+  const HeadPiece info = h.pieces[piece];
+  const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = (info.count + BN - 1) / BN, tiles = m_tiles * n_tiles;
+  const int tile = blockIdx.x / kBlocks, block = blockIdx.x % kBlocks;
+  if (tile >= tiles) return;
+  const TileAt at = tile_at(tile, m_tiles, n_tiles, true);
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int i = block / 4 / T::NJ, j = block / 4 % T::NJ, e4 = block % 4;
+  const int place = at.n * BN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;
+  const int c = at.m * kTileM + (wave / T::WC * T::NI + i) * 32 + e4 * 8 + lane / 32 * 4;
+  if (place >= info.count || c >= h.cols) return;
+  const char* from = h.slabs + static_cast<int64_t>(tile) * (kTileM * BN * 4) + block * (kProductThreads * 16) + tid * 16;
+  f32x4 sum = {};
+#pragma unroll 4
+  for (int s = 0; s < info.splits; ++s) sum += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(s) * tiles * (kTileM * BN * 4));
+  const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
+  const float a = h.a[mine];
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = bf16_rne(a == 0.0f ? 0.0f : sum[e] * a);
+  uint16_t* out = dx + static_cast<int64_t>(h.kept[mine]) * h.cols + c;
+  if (h.cols % 4 == 0) {
+    *reinterpret_cast<u32x2*>(out) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < h.cols) out[e] = static_cast<uint16_t>(b[e]);
+  }
+}
+
+// dW of a piece, 256 columns by 256 rows of the table: out <- [in +] sigma * sum.
+template <bool TWO, bool OUT16>
+__global__ __launch_bounds__(kProductThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
+  constexpr int BN = 256;
+  using T = HeadTile<BN>;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = h.vp / BN;
+  const int o = xcd_item(m_tiles * n_tiles);
+  if (o < 0) return;
+  const TileAt at = tile_at(o, m_tiles, n_tiles, true);
+  const HeadInfo info = *h.info;
+  const int count = h.pieces[piece].count, ksteps = (count + kStepK - 1) / kStepK;
+  if (count == 0 && in == out) return;   // nothing to add
+  const int64_t row_bytes = static_cast<int64_t>(h.hp) * 2, d_bytes = static_cast<int64_t>(h.vp) * 4;
+  const int64_t from = static_cast<int64_t>(piece) * h.piece * row_bytes + at.m * (kTileM * 2);
+  const int c0 = at.n * BN;
+  const Operand p = {h.xh + from, h.npad * row_bytes - from, static_cast<int>(row_bytes), ksteps * kStepK};
+  const Operand q = {reinterpret_cast<const char*>(h.logits) + static_cast<int64_t>(c0) * 4 + (TWO ? kPart * 2 : 0),
+                     h.piece * d_bytes - static_cast<int64_t>(c0) * 4 - (TWO ? kPart * 2 : 0), static_cast<int>(d_bytes), ksteps * kStepK};
+  HeadAcc<BN> acc = {};
+  multiply<BN, true, true, true, true>(p, q, TWO ? 2 * ksteps : ksteps, TWO, -(kPart * 2), lds, acc);
+  const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
+  const int up = info.ec + info.ex - 29;
+  const bool vec = h.cols % 4 == 0;
+#pragma unroll
+  for (int j = 0; j < T::NJ; ++j) {
+    const int v = c0 + (wave % T::WC * T::NJ + j) * 32 + lane % 32;
+    if (v >= h.rows) continue;
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int c = at.m * kTileM + (wave / T::WC * T::NI + i) * 32 + e * 2 + lane / 32 * 4;
+        if (c >= h.cols) continue;
+        const int64_t to = static_cast<int64_t>(v) * h.cols + c;
+        float y[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) y[t] = __builtin_ldexpf(acc.v[i][j][e + t], up) * sigma + 0.0f;   // never -0.0
+        if (vec) {
+          if (in) {
+            const f32x4 before = *reinterpret_cast<const f32x4*>(in + to);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) y[t] = before[t] + y[t];
+          }
+          if constexpr (OUT16)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + to) =
+                u32x2{bf16_rne(y[0]) | bf16_rne(y[1]) << 16, bf16_rne(y[2]) | bf16_rne(y[3]) << 16};
+          else
+            *reinterpret_cast<f32x4*>(static_cast<float*>(out) + to) = f32x4{y[0], y[1], y[2], y[3]};
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (c + t >= h.cols) continue;
+            if (in) y[t] = in[to + t] + y[t];
+            if constexpr (OUT16) static_cast<uint16_t*>(out)[to + t] = static_cast<uint16_t>(bf16_rne(y[t]));
+            else static_cast<float*>(out)[to + t] = y[t];
+          }
+        }
+      }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxRows = int64_t(1) << 21, kHeadMaxCols = int64_t(1) << 16;
+constexpr int64_t kHeadMaxElems = int64_t(1) << 33;
+constexpr int64_t kPieceTokens = 4096;   // tokens of a piece, unless the call says another number
+constexpr int64_t kPieceMax = 65536;
+
+int64_t up_to(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// A call's sizes, its workspace laid out, and how it is launched.
+struct HeadShape {
+  int64_t n = 0, npad = 0, rows = 0, cols = 0, vp = 0, hp = 0, top = 0, piece = 0, n_pieces = 0;
+  int tile_n = 256;            // tokens of a tile
+  int64_t dx_groups = 0;       // workgroups of the dx product
+  bool grad = false, widen = false, sums = false;   // sums: dW adds up in the workspace
+  int64_t info, pieces, keep, xmax, ent, idx, q, kept, pent, a, lse, pidx, pq, picked, xb, xh, stat, logits, d, slabs, table, acc;
+  int64_t bytes = 0;
+};
+
+int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool grad, int32_t packed_dt, int64_t piece, const char* who,
+               HeadShape* s) {
+  if (tensor < 0 || tensor >= p->n) return fail(RS_EINVAL, std::string(who) + ": no such tensor");
+  const Tensor& t = p->t[tensor];
+  if (t.kind == RS_TILEMAJOR) return fail(RS_EINVAL, std::string(who) + ": a TILEMAJOR tensor has no contiguous rows");
+  if (n < 0 || top < 0 || top > kMaxTop || piece < 0 || piece % 256 || piece > kPieceMax)
+    return fail(RS_EINVAL, std::string(who) + ": tokens >= 0, 0 to 256 top logits, pieces of a multiple of 256 tokens up to 65536 (or 0)");
+  if (n > kHeadMaxTokens || t.rows > kHeadMaxRows || t.cols > kHeadMaxCols || t.n > kHeadMaxElems || n * t.cols > kHeadMaxElems ||
+      n * std::max<int64_t>(top, 1) > (int64_t(1) << 28))
+    return fail(RS_ERANGE, std::string(who) + ": at most 2^20 tokens, 2^21 rows, 2^16 columns, table and tokens * columns at most 2^33 "
+                               "elements, tokens * top at most 2^28");
+  s->n = n;
+  s->rows = t.rows;
+  s->cols = t.cols;
+  s->top = top;
+  s->grad = grad;
+  s->npad = up_to(n, 256);
+  s->vp = up_to(t.rows, kTileM);
+  s->hp = up_to(t.cols, kStepK);
+  s->widen = s->hp != t.cols;
+  // pieces of equal size, of at most the tokens asked for
+  const int64_t most = std::min(s->npad, piece ? piece : kPieceTokens);
+  s->n_pieces = most ? (s->npad + most - 1) / most : 0;
+  s->piece = s->n_pieces ? up_to((s->npad + s->n_pieces - 1) / s->n_pieces, 256) : 256;
+  s->tile_n = n <= 64 ? 64 : n <= 128 ? 128 : 256;
+  s->sums = grad && packed_dt == RS_BF16 && s->n_pieces > 1;
+  const int64_t k = std::max<int64_t>(top, 1), dx_m = (t.cols + kTileM - 1) / kTileM;
+  for (int64_t tt = 1; tt <= (std::min(s->piece, n) + s->tile_n - 1) / s->tile_n; ++tt)
+    s->dx_groups = std::max(s->dx_groups, dx_m * tt * dx_splits(static_cast<int>(dx_m * tt), static_cast<int>(s->vp / kStepK)));
+  int64_t at = 0;
+  auto room = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up_to(bytes, 256);
+    return here;
+  };
+  s->info = room(sizeof(HeadInfo));
+  s->pieces = room(s->n_pieces * sizeof(HeadPiece));
+  s->keep = room(n * 4);
+  s->xmax = room(n * 4);
+  s->ent = room(n * 4);
+  s->idx = room(n * k * 4);
+  s->q = room(n * k * 4);
+  s->kept = room(s->npad * 4);
+  s->pent = room(s->npad * 4);
+  s->a = room(s->npad * 4);
+  s->lse = room(s->npad * 4);
+  s->pidx = room(s->npad * k * 4);
+  s->pq = room(s->npad * k * 4);
+  s->picked = room(s->npad * k * 4);
+  s->xb = room(s->npad * s->hp * 2);
+  s->stat = room(s->piece * (s->vp / 64) * 8);
+  s->table = room(s->widen ? s->rows * s->hp * 2 : 0);
+  s->xh = room(grad ? s->npad * s->hp * 2 : 0);
+  s->logits = room(grad ? s->piece * s->vp * 4 : 0);
+  s->d = room(grad ? s->piece * s->vp * 2 : 0);
+  s->slabs = room(grad ? s->dx_groups * kTileM * s->tile_n * 4 : 0);
+  s->acc = room(s->sums ? s->rows * s->cols * 4 : 0);
+  s->bytes = n ? at : 0;
+  return RS_OK;
+}
+
+// What the four calls have in common.
+struct HeadArgs {
+  int64_t tensor;
+  const void *gathered, *x;
+  int64_t n;
+  const void* ids;
+  int32_t id_bytes;
+  const void* teacher;    // null: ids are labels
+  int32_t teacher_dt;
+  int64_t top;
+  float temperature, scale;
+  float* loss;
+  const float* weights;
+  void* dx;
+  const float* prev;
+  void* packed;
+  int32_t packed_dt, scale_mode;
+  float grad_scale;
+  int64_t piece;
+  void* work;
+  int64_t work_bytes;
+};
+
+template <int BN>
+void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sigma, bool grad, float factor, hipStream_t q) {
+  const float c = a.scale / a.temperature, f = a.temperature * a.temperature;
+  for (int64_t i = 0; i < s.n_pieces; ++i) {
+    const int piece = static_cast<int>(i);
+    const int64_t tokens = std::min(s.piece, s.n - i * s.piece);
+    const int64_t n_tiles = (tokens + BN - 1) / BN, m_tiles = s.vp / kTileM;
+    const dim3 tiles(static_cast<unsigned>(up_to(m_tiles * n_tiles, 8))), threads(kProductThreads);
+    if (grad) hipLaunchKernelGGL((head_logits_kernel<BN, true>), tiles, threads, 0, q, h, piece, c);
+    else hipLaunchKernelGGL((head_logits_kernel<BN, false>), tiles, threads, 0, q, h, piece, c);
+    hipLaunchKernelGGL(head_loss_kernel, dim3(static_cast<unsigned>((tokens + kLossTokens - 1) / kLossTokens)), dim3(kThreads), 0, q, h,
+                       piece, static_cast<int>(s.vp / (32 * HeadTile<BN>::NI)), f, a.loss);
+    if (!grad) continue;
+    const bool two = a.packed_dt == RS_F32;
+    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStepK)), static_cast<unsigned>((s.vp + kDeltaCols - 1) / kDeltaCols));
+    if (two) hipLaunchKernelGGL(head_delta_kernel<true>, delta, dim3(kThreads), 0, q, h, piece);
+    else hipLaunchKernelGGL(head_delta_kernel<false>, delta, dim3(kThreads), 0, q, h, piece);
+    const int64_t dx_m = (s.cols + kTileM - 1) / kTileM;
+    hipLaunchKernelGGL(head_dx_kernel<BN>, dim3(static_cast<unsigned>(up_to(s.dx_groups, 8))), threads, 0, q, h, piece);
+    hipLaunchKernelGGL(head_dx_sum_kernel<BN>, dim3(static_cast<unsigned>(dx_m * n_tiles * HeadTile<BN>::NI * HeadTile<BN>::NJ * 4)),
+                       threads, 0, q, h, piece, static_cast<uint16_t*>(a.dx));
+    // dW: into the packed buffer, or with more than one piece into fp32 sums that the last piece rounds
+    const dim3 dw(static_cast<unsigned>(up_to(dx_m * (s.vp / 256), 8)));
+    const int64_t start = a.tensor;
+    float* sums = reinterpret_cast<float*>(static_cast<char*>(a.work) + s.acc);
+    const float* in = i ? (s.sums ? sums : static_cast<const float*>(a.packed) + start) : a.prev ? a.prev + start : nullptr;
+    if (two)
+      hipLaunchKernelGGL((head_dw_kernel<true, false>), dw, threads, 0, q, h, piece, sigma, in, static_cast<void*>(static_cast<float*>(a.packed) + start));
+    else if (s.sums && i + 1 < s.n_pieces)
+      hipLaunchKernelGGL((head_dw_kernel<false, false>), dw, threads, 0, q, h, piece, sigma, in, static_cast<void*>(sums));
+    else
+      hipLaunchKernelGGL((head_dw_kernel<false, true>), dw, threads, 0, q, h, piece, sigma, in,
+                         static_cast<void*>(static_cast<uint16_t*>(a.packed) + start));
+  }
+}
+
+// No tokens: the gradient of the table is zero. Four elements a thread.
+template <bool OUT16>
+__global__ __launch_bounds__(kThreads) void head_none_kernel(const float* prev, void* packed, int64_t n) {
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 4;
+  for (int64_t i = first; i < n && i < first + 4; ++i) {
+    const float y = prev ? prev[i] + 0.0f : 0.0f;
+    if constexpr (OUT16) static_cast<uint16_t*>(packed)[i] = static_cast<uint16_t>(bf16_rne(y));
+    else static_cast<float*>(packed)[i] = y;
+  }
+}
+
+int run_head(rs_plan* p, HeadArgs a, bool grad, void* stream, const char* who) {
+  clear_error();
+  int st = check_call(p, who);
+  HeadShape s;
+  if (st == RS_OK) st = head_shape(p, a.tensor, a.n, a.top, grad, grad ? a.packed_dt : RS_F32, a.piece, who, &s);
+  if (st != RS_OK) return st;
+  if (!a.gathered || (a.n && (!a.x || !a.ids || !a.loss || !a.work)) || (grad && (!a.packed || (a.n && !a.dx))))
+    return fail(RS_EINVAL, std::string(who) + ": null argument");
+  if (a.id_bytes != 4 && a.id_bytes != 8) return fail(RS_EINVAL, std::string(who) + ": token ids have 4 or 8 bytes");
+  if (reinterpret_cast<uintptr_t>(a.ids) % static_cast<uintptr_t>(a.id_bytes))
+    return fail(RS_EALIGN, std::string(who) + ": token ids must be aligned to their size");
+  if ((a.teacher_dt != RS_F32 && a.teacher_dt != RS_BF16) || (grad && a.packed_dt != RS_F32 && a.packed_dt != RS_BF16))
+    return fail(RS_EDTYPE, std::string(who) + ": fp32 or bf16");
+  if (!std::isfinite(a.scale) || !(a.temperature > 0.0f) || !std::isfinite(a.temperature) || !std::isfinite(a.scale / a.temperature) ||
+      !std::isfinite(a.temperature * a.temperature))
+    return fail(RS_EINVAL, std::string(who) + ": scale must be finite, temperature finite and above 0");
+  if (grad && a.prev == a.packed && a.packed_dt != RS_F32)
+    return fail(RS_EINVAL, std::string(who) + ": prev may be packed only when packed is fp32");
+  if (grad && ((a.scale_mode != RS_SCALE_INV_V && a.scale_mode != RS_SCALE_GIVEN) || !std::isfinite(a.grad_scale)))
+    return fail(RS_EINVAL, std::string(who) + ": bad scale");
+  for (const void* b : {a.gathered, a.x, static_cast<const void*>(a.loss), static_cast<const void*>(a.weights), static_cast<const void*>(a.dx),
+                        static_cast<const void*>(a.prev), static_cast<const void*>(a.packed), static_cast<const void*>(a.work), a.teacher})
+    if (!aligned16(b)) return fail(RS_EALIGN, std::string(who) + ": buffers must be 16-byte aligned");
+  if (a.work_bytes < s.bytes)
+    return fail(RS_EINVAL, std::string(who) + ": workspace of " + std::to_string(a.work_bytes) + " bytes, " + std::to_string(s.bytes) +
+                               " needed");
+  hipStream_t q = static_cast<hipStream_t>(stream);
+  const Tensor& t = p->t[a.tensor];
+  const float sigma = a.scale_mode == RS_SCALE_INV_V ? static_cast<float>(static_cast<double>(a.grad_scale) / static_cast<double>(p->V))
+                                                     : a.grad_scale;
+  if (a.n == 0) {
+    if (!grad || a.prev == a.packed) return RS_OK;
+    const dim3 grid(static_cast<unsigned>((t.n + kThreads * 4 - 1) / (kThreads * 4)));
+    const float* prev = a.prev ? a.prev + t.start : nullptr;
+    if (a.packed_dt == RS_BF16)
+      hipLaunchKernelGGL(head_none_kernel<true>, grid, dim3(kThreads), 0, q, prev, static_cast<void*>(static_cast<uint16_t*>(a.packed) + t.start), t.n);
+    else
+      hipLaunchKernelGGL(head_none_kernel<false>, grid, dim3(kThreads), 0, q, prev, static_cast<void*>(static_cast<float*>(a.packed) + t.start), t.n);
+    return launched(who);
+  }
+  char* w = static_cast<char*>(a.work);
+  const char* table = static_cast<const char*>(a.gathered) + t.start * 2;
+  Head h{};
+  h.n = static_cast<int32_t>(s.n);
+  h.npad = static_cast<int32_t>(s.npad);
+  h.rows = static_cast<int32_t>(s.rows);
+  h.cols = static_cast<int32_t>(s.cols);
+  h.vp = static_cast<int32_t>(s.vp);
+  h.hp = static_cast<int32_t>(s.hp);
+  h.top = static_cast<int32_t>(s.top);
+  h.piece = static_cast<int32_t>(s.piece);
+  h.table = s.widen ? w + s.table : table;
+  h.pitch = static_cast<int32_t>(s.hp * 2);
+  h.table_bytes = s.rows * s.hp * 2;
+  h.info = reinterpret_cast<HeadInfo*>(w + s.info);
+  h.pieces = reinterpret_cast<HeadPiece*>(w + s.pieces);
+  h.keep = reinterpret_cast<uint32_t*>(w + s.keep);
+  h.xmax = reinterpret_cast<float*>(w + s.xmax);
+  h.ent = reinterpret_cast<float*>(w + s.ent);
+  h.idx = reinterpret_cast<int32_t*>(w + s.idx);
+  h.q = reinterpret_cast<float*>(w + s.q);
+  h.kept = reinterpret_cast<int32_t*>(w + s.kept);
+  h.pent = reinterpret_cast<float*>(w + s.pent);
+  h.a = reinterpret_cast<float*>(w + s.a);
+  h.lse = reinterpret_cast<float*>(w + s.lse);
+  h.pidx = reinterpret_cast<int32_t*>(w + s.pidx);
+  h.pq = reinterpret_cast<float*>(w + s.pq);
+  h.picked = reinterpret_cast<float*>(w + s.picked);
+  h.xb = w + s.xb;
+  h.xh = w + s.xh;
+  h.stat = reinterpret_cast<float2*>(w + s.stat);
+  h.logits = reinterpret_cast<float*>(w + s.logits);
+  h.d = reinterpret_cast<uint16_t*>(w + s.d);
+  h.slabs = w + s.slabs;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  const float factor = a.temperature * a.scale;   // f c
+  const dim3 targets(static_cast<unsigned>((s.n + kThreads / kWave - 1) / (kThreads / kWave)));
+  if (grad)
+    hipLaunchKernelGGL(head_targets_kernel<true>, targets, dim3(kThreads), 0, q, h, a.ids, a.id_bytes == 8, a.teacher, a.teacher_dt == RS_BF16,
+                       a.temperature, x, a.loss, static_cast<uint16_t*>(a.dx));
+  else
+    hipLaunchKernelGGL(head_targets_kernel<false>, targets, dim3(kThreads), 0, q, h, a.ids, a.id_bytes == 8, a.teacher, a.teacher_dt == RS_BF16,
+                       a.temperature, x, a.loss, static_cast<uint16_t*>(nullptr));
+  hipLaunchKernelGGL(head_keep_kernel, dim3(1), dim3(kKeepThreads), 0, q, h, a.weights, factor, static_cast<int>(s.n_pieces),
+                     static_cast<int>((s.cols + kTileM - 1) / kTileM), s.tile_n);
+  if (grad)
+    hipLaunchKernelGGL(head_gather_kernel<true>, dim3(static_cast<unsigned>(s.npad)), dim3(kThreads), 0, q, h, x, a.weights, factor);
+  else
+    hipLaunchKernelGGL(head_gather_kernel<false>, dim3(static_cast<unsigned>(s.npad)), dim3(kThreads), 0, q, h, x, a.weights, factor);
+  if (s.widen)
+    hipLaunchKernelGGL(head_widen_kernel, dim3(static_cast<unsigned>((s.rows * (s.hp / 8) + kThreads - 1) / kThreads)), dim3(kThreads), 0, q,
+                       reinterpret_cast<const uint16_t*>(table), static_cast<int>(s.rows), static_cast<int>(s.cols), static_cast<int>(s.hp),
+                       reinterpret_cast<uint16_t*>(w + s.table));
+  a.tensor = t.start;   // elements from here on
+  if (s.tile_n == 64) launch_head<64>(s, h, a, sigma, grad, factor, q);
+  else if (s.tile_n == 128) launch_head<128>(s, h, a, sigma, grad, factor, q);
+  else launch_head<256>(s, h, a, sigma, grad, factor, q);
+  return launched(who);
+}
+
+}  // namespace
+}  // namespace rs
+
+using namespace rs;
+
+extern "C" int rs_head_workspace(const rs_plan* p, int64_t tensor, int64_t n_tokens, int64_t top, int32_t grad, int32_t packed_dt,
+                                 int64_t piece, int64_t* bytes) {
+  const char* who = "rs_head_workspace";
+  clear_error();
+  if (!p || !bytes) return fail(RS_EINVAL, std::string(who) + ": null argument");
+  if (grad != 0 && grad != 1) return fail(RS_EINVAL, std::string(who) + ": grad is 0 or 1");
+  if (packed_dt != RS_F32 && packed_dt != RS_BF16) return fail(RS_EDTYPE, std::string(who) + ": fp32 or bf16");
+  HeadShape s;
+  const int st = head_shape(p, tensor, n_tokens, top, grad == 1, packed_dt, piece, who, &s);
+  if (st != RS_OK) return st;
+  *bytes = s.bytes;
+  return RS_OK;
+}
+
+extern "C" int rs_head_loss(rs_plan* p, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* targets,
+                            int32_t id_bytes, float scale, float* loss, int64_t piece, void* work, int64_t work_bytes, void* stream) {
+  const HeadArgs a = {tensor, gathered, x, n_tokens, targets, id_bytes, nullptr, RS_F32, 0, 1.0f, scale, loss, nullptr, nullptr, nullptr,
+                      nullptr, RS_F32, RS_SCALE_GIVEN, 1.0f, piece, work, work_bytes};
+  return run_head(p, a, false, stream, "rs_head_loss");
+}
+
+extern "C" int rs_head_grad(rs_plan* p, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* targets,
+                            int32_t id_bytes, const float* weights, float scale, float* loss, void* dx, const float* prev, void* packed,
+                            int32_t packed_dt, int32_t scale_mode, float grad_scale, int64_t piece, void* work, int64_t work_bytes,
+                            void* stream) {
+  const HeadArgs a = {tensor, gathered, x, n_tokens, targets, id_bytes, nullptr, RS_F32, 0, 1.0f, scale, loss, weights, dx, prev,
+                      packed, packed_dt, scale_mode, grad_scale, piece, work, work_bytes};
+  return run_head(p, a, true, stream, "rs_head_grad");
+}
+
+extern "C" int rs_distill_loss(rs_plan* p, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* ids,
+                               int32_t id_bytes, const void* teacher, int32_t teacher_dt, int64_t top, float temperature, float scale,
+                               float* loss, int64_t piece, void* work, int64_t work_bytes, void* stream) {
+  const char* who = "rs_distill_loss";
+  clear_error();
+  if (top < 1 || (n_tokens && !teacher)) return fail(RS_EINVAL, std::string(who) + ": 1 to 256 top logits of a teacher");
+  const HeadArgs a = {tensor, gathered, x, n_tokens, ids, id_bytes, teacher, teacher_dt, top, temperature, scale, loss, nullptr, nullptr,
+                      nullptr, nullptr, RS_F32, RS_SCALE_GIVEN, 1.0f, piece, work, work_bytes};
+  return run_head(p, a, false, stream, who);
+}
+
+extern "C" int rs_distill_grad(rs_plan* p, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* ids,
+                               int32_t id_bytes, const void* teacher, int32_t teacher_dt, int64_t top, const float* weights,
+                               float temperature, float scale, float* loss, void* dx, const float* prev, void* packed, int32_t packed_dt,
+                               int32_t scale_mode, float grad_scale, int64_t piece, void* work, int64_t work_bytes, void* stream) {
+  const char* who = "rs_distill_grad";
+  clear_error();
+  if (top < 1 || (n_tokens && !teacher)) return fail(RS_EINVAL, std::string(who) + ": 1 to 256 top logits of a teacher");
+  const HeadArgs a = {tensor, gathered, x, n_tokens, ids, id_bytes, teacher, teacher_dt, top, temperature, scale, loss, weights, dx, prev,
+                      packed, packed_dt, scale_mode, grad_scale, piece, work, work_bytes};
+  return run_head(p, a, true, stream, who);
+}
