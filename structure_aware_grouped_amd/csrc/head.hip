@@ -40,25 +40,23 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kTileM = 256;          // rows of an output tile: its contiguous dimension in memory
-constexpr int kStepK = 64;           // of the contraction, per stage
-constexpr int kProductThreads = 512;
-constexpr int kProductWaves = kProductThreads / kWave;
+constexpr int kStep = 64;            // of the contraction, per stage; what it is padded to
 constexpr int kPart = 128;           // columns of d whose fp16 parts lie beside each other
 constexpr float kLog2e = 1.44269504088896341f;
 
 // ------------------------------------------------------------------ products
 
-// C[m, n] = sum_k P[m, k] Q[n, k] on one 256 x BN tile by 8 waves, 32 x 32
-// accumulators. Either operand may lie with k contiguous (plain) or with its
+// C[m, n] = sum_k P[m, k] Q[n, k] on one 256 x BN tile, 32 x 32 accumulators. Either operand may lie with k contiguous (plain) or with its
 // other index contiguous (TR): a TR operand is read out of LDS transposed
 // (ds_read_b64_tr_b16), so the table and d are used as they lie in memory.
 template <int BN>
 struct HeadTile {
+  static constexpr int kWaves = 8, kThreads = kWaves * kWave;
   static constexpr int WR = BN == 256 ? 2 : 4;              // wave rows
-  static constexpr int WC = kProductWaves / WR;
+  static constexpr int WC = kWaves / WR;
   static constexpr int NI = kTileM / 32 / WR, NJ = BN / 32 / WC;
-  static constexpr int kStages = BN == 256 ? 2 : 3;
-  static constexpr int kLds = kStages * (kTileM + BN) * kStepK * 2;
+  static constexpr int kStages = BN == 256 ? 2 : BN == 128 ? 3 : 4, kStagesQ = BN == 256 ? 3 : kStages;
+  static constexpr int kLds = (kStages * kTileM + kStagesQ * BN) * kStep * 2;
 };
 
 // One operand's tile: from `base` on, `left` bytes may be read. Plain: `rows`
@@ -72,61 +70,69 @@ struct Operand {
 };
 
 // Memory to LDS, 16 bytes per lane and load. Plain: 128-byte rows, piece c of
-// row r at place c ^ (r / 2 % 8). TR: rows of SIDE * 2 bytes, one per k, piece c
-// of row k at place c ^ (4 * (k % 4)), so that the four rows that 32 lanes of a
+// row r at place c ^ (r / 2 % 8). TR: rows of SIDE values, one per k, piece c of
+// row k at place c ^ (4 * (k % 4)), so that the four rows that 32 lanes of a
 // transposed read touch fall into banks of their own.
+//   RAGGED: a TR operand's rows may end within a stage, or ahead of one.
 //   PARTS: the operand is the fp16 parts of d, kPart columns of each beside each
 // other.
-template <int SIDE, bool TR, bool PARTS>
+template <int SIDE, bool TR, bool RAGGED, bool PARTS, int WAVES>
 struct Fetch {
-  static constexpr int kBytes = SIDE * kStepK * 2;
-  static constexpr int kLoads = kBytes / 1024 / kProductWaves;
+  static constexpr int kBytes = SIDE * kStep * 2;
+  static constexpr int kLoads = kBytes / 1024 / WAVES;
   static constexpr int kRowLanes = TR ? SIDE / 8 : 8;        // lanes that load one row
-  int off[kLoads];
+  static_assert(kLoads * 1024 * WAVES == kBytes, "whole loads");
+  int off[kLoads], wave, lane;
 
-  __device__ static __forceinline__ int row(int t, int wave, int lane) {
-    return (t * kProductWaves + wave) * (kWave / kRowLanes) + lane / kRowLanes;
-  }
-  __device__ static __forceinline__ int piece(int r, int lane) {
+  __device__ __forceinline__ int row(int t) const { return (t * WAVES + wave) * (kWave / kRowLanes) + lane / kRowLanes; }
+  __device__ __forceinline__ int piece(int r) const {
     const int c = (lane % kRowLanes) ^ (TR ? 4 * (r % 4) : r / 2 % 8);
     return PARTS ? c / 16 * 512 + c % 16 * 16 : c * 16;
   }
-  __device__ __forceinline__ void init(const Operand& o, int wave, int lane) {
+  __device__ __forceinline__ void init(const Operand& o, int wave_, int lane_) {
+    wave = wave_;
+    lane = lane_;
 #pragma unroll
     for (int t = 0; t < kLoads; ++t) {
-      const int r = row(t, wave, lane);
-      off[t] = (TR ? r : min(r, o.rows - 1)) * o.pitch + piece(r, lane);
+      const int r = row(t);
+      off[t] = (TR ? r : min(r, o.rows - 1)) * o.pitch + piece(r);
     }
   }
-  // Stage k of the contraction; `more`: bytes that all of it lies further on.
-  __device__ __forceinline__ void load(const Operand& o, int k, int64_t more, lds_char* dst, int wave, int lane) const {
-    const int first = TR ? min(k * kStepK, o.rows - 1) : 0;
-    const int64_t at = more + (TR ? static_cast<int64_t>(first) * o.pitch : static_cast<int64_t>(k) * (kStepK * 2));
-    const int64_t left = o.left - at;
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(o.base + at), 0,
-                                          static_cast<int>(left < 0x7fffffff ? left : 0x7fffffff), kRawBufferWord3);
-    const int rows = o.rows - first;
-    const bool whole = !TR || (first == k * kStepK && rows >= kStepK);
+  // Stage k of the contraction: loads [first, last) of this wave. `more`: bytes
+  // that all of the operand lies further on.
+  template <int FIRST, int LAST>
+  __device__ __forceinline__ void load(const Operand& o, int k, int64_t more, lds_char* dst) const {
+    if constexpr (FIRST < LAST) {
+      const int first = RAGGED ? min(k * kStep, o.rows - 1) : k * kStep;
+      const int64_t at = more + (TR ? static_cast<int64_t>(first) * o.pitch : static_cast<int64_t>(k) * (kStep * 2));
+      const int64_t left = o.left - at;
+      const __amdgpu_buffer_rsrc_t rsrc =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(o.base + at), 0,
+                                            static_cast<int>(left < 0x7fffffff ? left : 0x7fffffff), kRawBufferWord3);
 #pragma unroll
-    for (int t = 0; t < kLoads; ++t) {
-      int mine = off[t];
-      if (!whole) {
-        const int r = row(t, wave, lane);
-        mine = min(r, rows - 1) * o.pitch + piece(r, lane);
+      for (int t = FIRST; t < LAST; ++t) {
+        const int r = row(t);
+        const int mine = RAGGED ? min(r, o.rows - 1 - first) * o.pitch + piece(r) : off[t];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst + (t * WAVES + wave) * 1024, 16, mine, 0, 0, 0);
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst + (t * kProductWaves + wave) * 1024, 16, mine, 0, 0, 0);
     }
   }
 };
+
+// A transposed read. The pointer is marked as aliasing nothing else: otherwise
+// the compiler waits for every load into LDS on its way ahead of each read,
+// where the contraction waits for the one stage that it reads.
+__device__ __forceinline__ u32x2 read_tr(const lds_s16x4* __restrict__ p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_s16x4*>(p)));
+}
 
 // LDS to fragments: 32 rows (m or n) by 16 k, lane l has row l % 32 and the 8
 // values of k from 8 * (l / 32) on. A transposed read gives each lane of 16 the
 // column of its number of a 4 x 16 block, so a fragment takes two.
 template <int SIDE, bool TR, int N>
 struct Fragments {
-  static constexpr int kBytes = SIDE * kStepK * 2;
-  const char* at[TR ? N : 4];
+  static constexpr int kBytes = SIDE * kStep * 2;
+  const char* at[TR ? N : kStep / 16];
 
   __device__ __forceinline__ void init(const char* lds, int first, int lane) {   // first: the wave's first 32-row block
     if constexpr (TR) {
@@ -139,16 +145,13 @@ struct Fragments {
     } else {
       const int r = lane % 32;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        at[kk] = lds + first * 4096 + r * 128 + ((kk * 2 + lane / 32) ^ (r / 2 % 8)) * 16;
+      for (int kk = 0; kk < kStep / 16; ++kk) at[kk] = lds + first * 4096 + r * 128 + ((kk * 2 + lane / 32) ^ (r / 2 % 8)) * 16;
     }
   }
   __device__ __forceinline__ u32x4 read(int b, int kk, int stage) const {
     if constexpr (TR) {
       const char* p = at[b] + stage * kBytes + kk * 16 * SIDE * 2;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(p + 4 * SIDE * 2));
-      const u32x2 a = __builtin_bit_cast(u32x2, lo), c = __builtin_bit_cast(u32x2, hi);
+      const u32x2 a = read_tr((const lds_s16x4*)(const lds_char*)p), c = read_tr((const lds_s16x4*)(const lds_char*)(p + 4 * SIDE * 2));
       return u32x4{a.x, a.y, c.x, c.y};
     } else {
       return *reinterpret_cast<const u32x4*>(at[kk] + stage * kBytes + b * 4096);
@@ -163,95 +166,136 @@ struct HeadAcc {
 
 // The contraction, in `ksteps` stages. With `two`, after the first half of them
 // P starts over and Q starts over at its other part, `second` bytes further on.
-template <int BN, bool F16, bool PT, bool QT, bool PARTS>
-__device__ __forceinline__ void multiply(const Operand& p, const Operand& q, int ksteps, bool two, int64_t second, char* lds, HeadAcc<BN>& c) {
-  using T = HeadTile<BN>;
+//   One stage: three sixteen-column multiplications, each while the next
+// fragment is read; then, with every wave done reading this stage and the next
+// one arrived, the fourth under the first reads of the next stage. From there
+// on, spread over a whole stage, the places that this stage leaves are loaded
+// again, P's for kStages stages later and behind them Q's for kStagesQ later.
+// A load into LDS holds its wave up while others are on their way, so loads in
+// one burst stop the multiplications: 8 of them after each turn took 4096 x
+// 131072 x 4096 from 2.85 (loads left out) to 3.33 ms.
+template <int BN, bool F16, bool PT, bool QT, bool RAGGED, bool PARTS>
+struct Contract {
+using T = HeadTile<BN>;
+using FP = Fetch<kTileM, PT, RAGGED, false, T::kWaves>;
+using FQ = Fetch<BN, QT, false, PARTS, T::kWaves>;
+static constexpr int SP = T::kStages, SQ = T::kStagesQ, U = SP == SQ ? SP : SP * SQ;
+static constexpr int LP = FP::kLoads, LQ = FQ::kLoads, kLoads = LP + LQ;
+static constexpr int kReads = T::NI * (PT ? 2 : 1) + T::NJ * (QT ? 2 : 1), kMuls = T::NI * T::NJ;
+static_assert(SQ == SP || SQ == SP + 1, "the counts of loads on their way below");
+
+Operand p, q;
+int ksteps, turn;
+int64_t second;
+lds_char* base;
+FP fp;
+FQ fq;
+Fragments<kTileM, PT, T::NI> rp;
+Fragments<BN, QT, T::NJ> rq;
+u32x4 fa[2][T::NI], fb[2][T::NJ];
+HeadAcc<BN>& c;
+
+template <int FIRST, int LAST>
+__device__ __forceinline__ void load_p(int s, int place) {
+  fp.template load<FIRST, LAST>(p, s < turn ? s : s - turn, 0, base + place * FP::kBytes);
+}
+template <int FIRST, int LAST>
+__device__ __forceinline__ void load_q(int s, int place) {
+  fq.template load<FIRST, LAST>(q, s < turn ? s : s - turn, s < turn ? 0 : second, base + SP * FP::kBytes + place * FQ::kBytes);
+}
+// Quarter Q4 of what is loaded into the places of stage s.
+template <int Q4>
+__device__ __forceinline__ void load_quarter(int s, int pp, int qp, bool whole) {
+  constexpr int a = kLoads * Q4 / 4, b = kLoads * (Q4 + 1) / 4;
+  if (whole || s + SP < ksteps) load_p<(a < LP ? a : LP), (b < LP ? b : LP)>(s + SP, pp);
+  if (whole || s + SQ < ksteps) load_q<(a > LP ? a - LP : 0), (b > LP ? b - LP : 0)>(s + SQ, qp);
+}
+__device__ __forceinline__ void fetch(int pp, int qp, int kk, int to) {
+#pragma unroll
+  for (int j = 0; j < T::NJ; ++j) fb[to][j] = rq.read(j, kk, qp);
+#pragma unroll
+  for (int i = 0; i < T::NI; ++i) fa[to][i] = rp.read(i, kk, pp);
+}
+__device__ __forceinline__ void mma(int from) {
+#pragma unroll
+  for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j) {
+      if constexpr (F16)
+        c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, fa[from][i]), __builtin_bit_cast(h8, fb[from][j]),
+                                                           c.v[i][j], 0, 0, 0);
+      else
+        c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, fa[from][i]), __builtin_bit_cast(b8, fb[from][j]),
+                                                            c.v[i][j], 0, 0, 0);
+    }
+}
+// Multiplications with the fragment reads between them, and behind the reads
+// the LOADS loads.
+template <int LOADS>
+__device__ static __forceinline__ void interleave() {
+  constexpr int kEach = (kReads + kMuls - 1) / kMuls, kRead = (kReads + kEach - 1) / kEach;
+  constexpr int kRest = kMuls > kRead ? kMuls - kRead : 1, kLoadEach = (LOADS + kRest - 1) / kRest;
+#pragma unroll
+  for (int i = 0; i < kMuls; ++i) {
+    if (i < kRead) __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);   // LDS reads
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // one multiplication
+    if (LOADS && (i >= kRead || i == kMuls - 1)) __builtin_amdgcn_sched_group_barrier(0x020, kLoadEach, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int KK>
+__device__ __forceinline__ void sixteen(int s, int pp, int qp, int before_p, int before_q, bool whole) {
+  fetch(pp, qp, KK + 1, (KK + 1) & 1);
+  if (whole || s > 0) load_quarter<KK + 1>(s - 1, before_p, before_q, whole);
+  mma(KK & 1);
+  interleave<kLoads * (KK + 2) / 4 - kLoads * (KK + 1) / 4>();
+}
+// Stage s, in places pp and qp; before_p, before_q: those of stage s - 1.
+// whole: everything that a stage loads exists, and stages ahead of this one.
+__device__ __forceinline__ void step(int s, int pp, int qp, int next_p, int next_q, int before_p, int before_q, bool whole) {
+  sixteen<0>(s, pp, qp, before_p, before_q, whole);
+  sixteen<1>(s, pp, qp, before_p, before_q, whole);
+  sixteen<2>(s, pp, qp, before_p, before_q, whole);
+  // newer than the next stage's loads: SP - 2 turns' and Q's of one stage more
+  if (whole || s + SQ <= ksteps) wait<(SP - 2) * kLoads + (SQ - SP) * LQ, true>();
+  else wait<0, true>();
+  barrier();
+  if (whole || s + 1 < ksteps) fetch(next_p, next_q, 0, 0);
+  load_quarter<0>(s, pp, qp, whole);
+  mma(1);
+  interleave<kLoads / 4>();
+}
+
+__device__ __forceinline__ Contract(const Operand& p_, const Operand& q_, int ksteps_, bool two, int64_t second_, char* lds, HeadAcc<BN>& c_)
+    : p(p_), q(q_), ksteps(ksteps_), turn(two ? ksteps_ / 2 : ksteps_), second(second_), base((lds_char*)lds), c(c_) {
   const int tid = fresh_thread(), lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  Fetch<kTileM, PT, false> fp;
-  Fetch<BN, QT, PARTS> fq;
-  constexpr int kPBytes = decltype(fp)::kBytes, kQBytes = decltype(fq)::kBytes, S = T::kStages;
-  constexpr int kLoads = decltype(fp)::kLoads + decltype(fq)::kLoads;
   fp.init(p, wave, lane);
   fq.init(q, wave, lane);
-  const int turn = two ? ksteps / 2 : ksteps;
-  lds_char* base = (lds_char*)lds;
-  auto load = [&](int s, int stage) {
-    const int k = s < turn ? s : s - turn;
-    fp.load(p, k, 0, base + stage * kPBytes, wave, lane);
-    fq.load(q, k, s < turn ? 0 : second, base + S * kPBytes + stage * kQBytes, wave, lane);
-  };
-  Fragments<kTileM, PT, T::NI> rp;
-  Fragments<BN, QT, T::NJ> rq;
   rp.init(lds, wave / T::WC * T::NI, lane);
-  rq.init(lds + S * kPBytes, wave % T::WC * T::NJ, lane);
-  u32x4 fa[2][T::NI], fb[2][T::NJ];
-  auto fetch = [&](int stage, int kk, int to) {
-#pragma unroll
-    for (int j = 0; j < T::NJ; ++j) fb[to][j] = rq.read(j, kk, stage);
-#pragma unroll
-    for (int i = 0; i < T::NI; ++i) fa[to][i] = rp.read(i, kk, stage);
-  };
-  auto mma = [&](int from) {
-#pragma unroll
-    for (int i = 0; i < T::NI; ++i)
-#pragma unroll
-      for (int j = 0; j < T::NJ; ++j) {
-        if constexpr (F16)
-          c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, fa[from][i]), __builtin_bit_cast(h8, fb[from][j]),
-                                                             c.v[i][j], 0, 0, 0);
-        else
-          c.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, fa[from][i]), __builtin_bit_cast(b8, fb[from][j]),
-                                                              c.v[i][j], 0, 0, 0);
-      }
-  };
-  // fragment reads spread over the multiplications, so that none of them waits
-  constexpr int kReads = T::NI * (PT ? 2 : 1) + T::NJ * (QT ? 2 : 1), kMuls = T::NI * T::NJ;
-  constexpr int kEach = (kReads + kMuls - 1) / kMuls;
-  auto interleave = [&]() {
-#pragma unroll
-    for (int i = 0; i < kMuls; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);   // LDS reads
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // one multiplication
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  // One stage: three sixteen-column multiplications, each while the next
-  // fragment is read; then, with every wave done reading this stage and the
-  // next one arrived (full: later ones may still be on their way), the loads
-  // into this stage and the next stage's first fragment, under the fourth.
-  auto step = [&](int s, int stage, int next, bool full, bool more_loads, bool more) {
-#pragma unroll
-    for (int kk = 0; kk < 3; ++kk) {
-      fetch(stage, kk + 1, (kk + 1) & 1);
-      mma(kk & 1);
-      interleave();
-    }
-    if (full) wait<(S - 2) * kLoads, true>();
-    else wait<0, true>();
-    barrier();
-    if (more) fetch(next, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (more_loads) load(s + S, stage);
-    __builtin_amdgcn_sched_barrier(0);
-    mma(1);
-    __builtin_amdgcn_sched_barrier(0);
-  };
+  rq.init(lds + SP * FP::kBytes, wave % T::WC * T::NJ, lane);
   if (ksteps == 0) return;
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (s < ksteps) load(s, s);
-  if (ksteps >= S) wait<(S - 1) * kLoads, false>();
+  for (int s = 0; s < SQ; ++s) {
+    if (s < SP && s < ksteps) load_p<0, LP>(s, s);
+    if (s < ksteps) load_q<0, LQ>(s, s);
+  }
+  if (ksteps >= SQ) wait<(SP - 1) * kLoads + (SQ - SP) * LQ, false>();
   else wait<0, false>();
   barrier();
-  fetch(0, 0, 0);
+  fetch(0, 0, 0, 0);
   int s = 0;
-  for (; s + 2 * S - 1 < ksteps; s += S) {
+  if (ksteps > 2 * U) {   // the first has no stage ahead of it
+    step(0, 0, 0, 1 % SP, 1 % SQ, 0, 0, false);
+    for (s = 1; s + U - 1 + SQ < ksteps; s += U) {
 #pragma unroll
-    for (int u = 0; u < S; ++u) step(s + u, u, (u + 1) % S, true, true, true);
+      for (int u = 1; u <= U; ++u)
+        step(s + u - 1, u % SP, u % SQ, (u + 1) % SP, (u + 1) % SQ, (u - 1) % SP, (u - 1) % SQ, true);
+    }
   }
-  for (; s < ksteps; ++s) step(s, s % S, (s + 1) % S, s + S <= ksteps, s + S < ksteps, s + 1 < ksteps);
+  for (; s < ksteps; ++s) step(s, s % SP, s % SQ, (s + 1) % SP, (s + 1) % SQ, (s + SP - 1) % SP, (s + SQ - 1) % SQ, false);
 }
+};
 
 // Tile number `o` of m_tiles x n_tiles, eight m tiles beside each other within
 // a band, so that the 32 neighbours that an XCD's CUs work on at a time share
@@ -477,18 +521,18 @@ __global__ __launch_bounds__(kKeepThreads) void head_keep_kernel(Head h, const f
   }
   for (int p = tid; p < n_pieces; p += kKeepThreads) {
     const int count = min(max(base - p * h.piece, 0), h.piece);
-    h.pieces[p] = HeadPiece{count, dx_splits(dx_tiles_m * ((count + tile_n - 1) / tile_n), h.vp / kStepK)};
+    h.pieces[p] = HeadPiece{count, dx_splits(dx_tiles_m * ((count + tile_n - 1) / tile_n), h.vp / kStep)};
   }
 }
 
 // x of the kept tokens beside each other, as bf16 and (GRAD) scaled as fp16,
 // zeros in the padding of their columns and in the places up to the next
-// multiple of kStepK; and their targets. A token whose gradient has no weight
+// multiple of kStep; and their targets. A token whose gradient has no weight
 // has zeros as fp16, whatever x holds.
 template <bool GRAD>
 __global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uint16_t* x, const float* weights, float factor) {
   const int p = blockIdx.x, count = h.info->count;
-  if (p >= (count + kStepK - 1) / kStepK * kStepK) return;
+  if (p >= (count + kStep - 1) / kStep * kStep) return;
   const bool live = p < count;
   const int64_t t = live ? h.kept[p] : 0;
   const float a = live ? (weights ? weights[t] : 1.0f) * factor : 0.0f;
@@ -529,7 +573,7 @@ __global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uin
   }
 }
 
-// The table with its rows padded, where their width is no multiple of kStepK.
+// The table with its rows padded, where their width is no multiple of kStep.
 __global__ __launch_bounds__(kThreads) void head_widen_kernel(const uint16_t* table, int rows, int cols, int hp, uint16_t* out) {
   const int per = hp / 8;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -553,7 +597,7 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // table's end. A lane holds one token's logits, so the sums are its own and
 // the other half wave's.
 template <int BN, bool STORE>
-__global__ __launch_bounds__(kProductThreads) void head_logits_kernel(Head h, int piece, float factor) {
+__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Head h, int piece, float factor) {
   using T = HeadTile<BN>;
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   const int count = h.pieces[piece].count, m_tiles = h.vp / kTileM, n_tiles = (count + BN - 1) / BN;
@@ -566,7 +610,7 @@ __global__ __launch_bounds__(kProductThreads) void head_logits_kernel(Head h, in
   const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - v0};
   const Operand q = {h.xb + p0 * row_bytes, BN * row_bytes, static_cast<int>(row_bytes), BN};
   HeadAcc<BN> acc = {};
-  multiply<BN, false, false, false, false>(p, q, h.hp / kStepK, false, 0, lds, acc);
+  Contract<BN, false, false, false, false, false>(p, q, h.hp / kStep, false, 0, lds, acc);
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave, half = lane / 32;
   const int first = v0 + wave / T::WC * T::NI * 32;   // the wave's first row of the table
   const int k = max(h.top, 1);
@@ -600,14 +644,17 @@ __global__ __launch_bounds__(kProductThreads) void head_logits_kernel(Head h, in
         int r[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) r[u] = s0 + u < k ? h.pidx[static_cast<int64_t>(s0 + u) * h.npad + mine] - first : -1;
+#pragma unroll 1
+        for (int u = 0; u < kAhead; ++u) {   // one body for all: hits are rare
+          int mine_r = -1;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (r[u] < 0 || r[u] >= T::NI * 32 || r[u] / 4 % 2 != half) continue;
+          for (int w = 0; w < kAhead; ++w) mine_r = u == w ? r[w] : mine_r;
+          if (mine_r < 0 || mine_r >= T::NI * 32 || mine_r / 4 % 2 != half) continue;
           float l = 0.0f;
 #pragma unroll
           for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) l = r[u] == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
+            for (int e = 0; e < 16; ++e) l = mine_r == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
           h.picked[static_cast<int64_t>(s0 + u) * h.npad + mine] = l;
         }
       }
@@ -687,7 +734,7 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
   __shared__ int row[kMaxTop];
   __shared__ float share[kMaxTop];
   const int count = h.pieces[piece].count, place = blockIdx.x;
-  if (place >= (count + kStepK - 1) / kStepK * kStepK) return;
+  if (place >= (count + kStep - 1) / kStep * kStep) return;
   const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
   const bool live = place < count;
   const float a = live ? h.a[mine] : 0.0f, z = live ? h.lse[mine] : 0.0f;
@@ -742,7 +789,7 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
 // dx of a piece: 256 columns by BN tokens, one part of the contraction over the
 // table's rows. Sums go to the part's slab, in the registers' order.
 template <int BN>
-__global__ __launch_bounds__(kProductThreads) void head_dx_kernel(Head h, int piece) {
+__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_kernel(Head h, int piece) {
   using T = HeadTile<BN>;
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   const HeadPiece info = h.pieces[piece];
@@ -751,18 +798,18 @@ __global__ __launch_bounds__(kProductThreads) void head_dx_kernel(Head h, int pi
   if (o < 0) return;
   const int split = o / tiles;
   const TileAt at = tile_at(o - split * tiles, m_tiles, n_tiles, true);
-  const int ksteps = h.vp / kStepK;
+  const int ksteps = h.vp / kStep;
   const int k0 = static_cast<int>(static_cast<int64_t>(ksteps) * split / info.splits);
   const int k1 = static_cast<int>(static_cast<int64_t>(ksteps) * (split + 1) / info.splits);
   // stages behind the table's last row repeat it; d is zero there
-  const int row = min(k0 * kStepK, h.rows - 1);
+  const int row = min(k0 * kStep, h.rows - 1);
   const int64_t from = static_cast<int64_t>(row) * h.pitch + at.m * (kTileM * 2);
   const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - row};
   const int64_t row_bytes = static_cast<int64_t>(h.vp) * 2;
-  const Operand q = {reinterpret_cast<const char*>(h.d) + at.n * BN * row_bytes + k0 * (kStepK * 2), BN * row_bytes - k0 * (kStepK * 2),
+  const Operand q = {reinterpret_cast<const char*>(h.d) + at.n * BN * row_bytes + k0 * (kStep * 2), BN * row_bytes - k0 * (kStep * 2),
                      static_cast<int>(row_bytes), BN};
   HeadAcc<BN> acc = {};
-  multiply<BN, false, true, false, false>(p, q, k1 - k0, false, 0, lds, acc);
+  Contract<BN, false, true, false, true, false>(p, q, k1 - k0, false, 0, lds, acc);
   char* out = h.slabs + static_cast<int64_t>(o) * (kTileM * BN * 4) + fresh_thread() * 16;
 #pragma unroll
   for (int i = 0; i < T::NI; ++i)
@@ -770,14 +817,14 @@ __global__ __launch_bounds__(kProductThreads) void head_dx_kernel(Head h, int pi
     for (int j = 0; j < T::NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<f32x4*>(out + ((i * T::NJ + j) * 4 + e / 4) * (kProductThreads * 16)) =
+        *reinterpret_cast<f32x4*>(out + ((i * T::NJ + j) * 4 + e / 4) * (T::kThreads * 16)) =
             f32x4{acc.v[i][j][e], acc.v[i][j][e + 1], acc.v[i][j][e + 2], acc.v[i][j][e + 3]};
 }
 
 // dx of one 32-column block of a tile for each of its waves: the parts added in
 // their order, times a, rounded to bf16, to the tokens' own rows.
 template <int BN>
-__global__ __launch_bounds__(kProductThreads) void head_dx_sum_kernel(Head h, int piece, uint16_t* dx) {
+__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_sum_kernel(Head h, int piece, uint16_t* dx) {
   using T = HeadTile<BN>;
   constexpr int kBlocks = T::NI * T::NJ * 4;
   const HeadPiece info = h.pieces[piece];
@@ -790,7 +837,7 @@ __global__ __launch_bounds__(kProductThreads) void head_dx_sum_kernel(Head h, in
   const int place = at.n * BN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;
   const int c = at.m * kTileM + (wave / T::WC * T::NI + i) * 32 + e4 * 8 + lane / 32 * 4;
   if (place >= info.count || c >= h.cols) return;
-  const char* from = h.slabs + static_cast<int64_t>(tile) * (kTileM * BN * 4) + block * (kProductThreads * 16) + tid * 16;
+  const char* from = h.slabs + static_cast<int64_t>(tile) * (kTileM * BN * 4) + block * (T::kThreads * 16) + tid * 16;
   f32x4 sum = {};
 #pragma unroll 4
   for (int s = 0; s < info.splits; ++s) sum += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(s) * tiles * (kTileM * BN * 4));
@@ -811,7 +858,7 @@ __global__ __launch_bounds__(kProductThreads) void head_dx_sum_kernel(Head h, in
 
 // dW of a piece, 256 columns by 256 rows of the table: out <- [in +] sigma * sum.
 template <bool TWO, bool OUT16>
-__global__ __launch_bounds__(kProductThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
+__global__ __launch_bounds__(HeadTile<256>::kThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
   constexpr int BN = 256;
   using T = HeadTile<BN>;
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
@@ -820,16 +867,16 @@ __global__ __launch_bounds__(kProductThreads) void head_dw_kernel(Head h, int pi
   if (o < 0) return;
   const TileAt at = tile_at(o, m_tiles, n_tiles, true);
   const HeadInfo info = *h.info;
-  const int count = h.pieces[piece].count, ksteps = (count + kStepK - 1) / kStepK;
+  const int count = h.pieces[piece].count, depth = (count + kStep - 1) / kStep * kStep;
   if (count == 0 && in == out) return;   // nothing to add
   const int64_t row_bytes = static_cast<int64_t>(h.hp) * 2, d_bytes = static_cast<int64_t>(h.vp) * 4;
   const int64_t from = static_cast<int64_t>(piece) * h.piece * row_bytes + at.m * (kTileM * 2);
   const int c0 = at.n * BN;
-  const Operand p = {h.xh + from, h.npad * row_bytes - from, static_cast<int>(row_bytes), ksteps * kStepK};
+  const Operand p = {h.xh + from, h.npad * row_bytes - from, static_cast<int>(row_bytes), depth};
   const Operand q = {reinterpret_cast<const char*>(h.logits) + static_cast<int64_t>(c0) * 4 + (TWO ? kPart * 2 : 0),
-                     h.piece * d_bytes - static_cast<int64_t>(c0) * 4 - (TWO ? kPart * 2 : 0), static_cast<int>(d_bytes), ksteps * kStepK};
+                     h.piece * d_bytes - static_cast<int64_t>(c0) * 4 - (TWO ? kPart * 2 : 0), static_cast<int>(d_bytes), depth};
   HeadAcc<BN> acc = {};
-  multiply<BN, true, true, true, true>(p, q, TWO ? 2 * ksteps : ksteps, TWO, -(kPart * 2), lds, acc);
+  Contract<BN, true, true, true, false, true>(p, q, (TWO ? 2 : 1) * depth / kStep, TWO, -(kPart * 2), lds, acc);
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
   const int up = info.ec + info.ex - 29;
   const bool vec = h.cols % 4 == 0;
@@ -908,7 +955,7 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->grad = grad;
   s->npad = up_to(n, 256);
   s->vp = up_to(t.rows, kTileM);
-  s->hp = up_to(t.cols, kStepK);
+  s->hp = up_to(t.cols, kStep);
   s->widen = s->hp != t.cols;
   // pieces of equal size, of at most the tokens asked for
   const int64_t most = std::min(s->npad, piece ? piece : kPieceTokens);
@@ -918,7 +965,7 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->sums = grad && packed_dt == RS_BF16 && s->n_pieces > 1;
   const int64_t k = std::max<int64_t>(top, 1), dx_m = (t.cols + kTileM - 1) / kTileM;
   for (int64_t tt = 1; tt <= (std::min(s->piece, n) + s->tile_n - 1) / s->tile_n; ++tt)
-    s->dx_groups = std::max(s->dx_groups, dx_m * tt * dx_splits(static_cast<int>(dx_m * tt), static_cast<int>(s->vp / kStepK)));
+    s->dx_groups = std::max(s->dx_groups, dx_m * tt * dx_splits(static_cast<int>(dx_m * tt), static_cast<int>(s->vp / kStep)));
   int64_t at = 0;
   auto room = [&](int64_t bytes) {
     const int64_t here = at;
@@ -981,14 +1028,14 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     const int piece = static_cast<int>(i);
     const int64_t tokens = std::min(s.piece, s.n - i * s.piece);
     const int64_t n_tiles = (tokens + BN - 1) / BN, m_tiles = s.vp / kTileM;
-    const dim3 tiles(static_cast<unsigned>(up_to(m_tiles * n_tiles, 8))), threads(kProductThreads);
+    const dim3 tiles(static_cast<unsigned>(up_to(m_tiles * n_tiles, 8))), threads(HeadTile<BN>::kThreads);
     if (grad) hipLaunchKernelGGL((head_logits_kernel<BN, true>), tiles, threads, 0, q, h, piece, c);
     else hipLaunchKernelGGL((head_logits_kernel<BN, false>), tiles, threads, 0, q, h, piece, c);
     hipLaunchKernelGGL(head_loss_kernel, dim3(static_cast<unsigned>((tokens + kLossTokens - 1) / kLossTokens)), dim3(kThreads), 0, q, h,
                        piece, static_cast<int>(s.vp / (32 * HeadTile<BN>::NI)), f, a.loss);
     if (!grad) continue;
     const bool two = a.packed_dt == RS_F32;
-    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStepK)), static_cast<unsigned>((s.vp + kDeltaCols - 1) / kDeltaCols));
+    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStep)), static_cast<unsigned>((s.vp + kDeltaCols - 1) / kDeltaCols));
     if (two) hipLaunchKernelGGL(head_delta_kernel<true>, delta, dim3(kThreads), 0, q, h, piece);
     else hipLaunchKernelGGL(head_delta_kernel<false>, delta, dim3(kThreads), 0, q, h, piece);
     const int64_t dx_m = (s.cols + kTileM - 1) / kTileM;
@@ -1000,12 +1047,13 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     const int64_t start = a.tensor;
     float* sums = reinterpret_cast<float*>(static_cast<char*>(a.work) + s.acc);
     const float* in = i ? (s.sums ? sums : static_cast<const float*>(a.packed) + start) : a.prev ? a.prev + start : nullptr;
+    const dim3 wide(HeadTile<256>::kThreads);
     if (two)
-      hipLaunchKernelGGL((head_dw_kernel<true, false>), dw, threads, 0, q, h, piece, sigma, in, static_cast<void*>(static_cast<float*>(a.packed) + start));
+      hipLaunchKernelGGL((head_dw_kernel<true, false>), dw, wide, 0, q, h, piece, sigma, in, static_cast<void*>(static_cast<float*>(a.packed) + start));
     else if (s.sums && i + 1 < s.n_pieces)
-      hipLaunchKernelGGL((head_dw_kernel<false, false>), dw, threads, 0, q, h, piece, sigma, in, static_cast<void*>(sums));
+      hipLaunchKernelGGL((head_dw_kernel<false, false>), dw, wide, 0, q, h, piece, sigma, in, static_cast<void*>(sums));
     else
-      hipLaunchKernelGGL((head_dw_kernel<false, true>), dw, threads, 0, q, h, piece, sigma, in,
+      hipLaunchKernelGGL((head_dw_kernel<false, true>), dw, wide, 0, q, h, piece, sigma, in,
                          static_cast<void*>(static_cast<uint16_t*>(a.packed) + start));
   }
 }
