@@ -41,7 +41,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kTileM = 256;          // rows of an output tile: its contiguous dimension in memory
 constexpr int kStep = 64;            // of the contraction, per stage; what it is padded to
-constexpr int kPart = 128;           // columns of d whose fp16 parts lie beside each other
+constexpr int kPart = 64;            // columns of d whose fp16 parts lie beside each other
 constexpr float kLog2e = 1.44269504088896341f;
 
 // ------------------------------------------------------------------ products
@@ -51,7 +51,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 // (ds_read_b64_tr_b16), so the table and d are used as they lie in memory.
 template <int BN>
 struct HeadTile {
-  static constexpr int kWaves = 8, kThreads = kWaves * kWave;
+  static constexpr int kWaves = BN == 256 ? 4 : 8, kThreads = kWaves * kWave;
   static constexpr int WR = BN == 256 ? 2 : 4;              // wave rows
   static constexpr int WC = kWaves / WR;
   static constexpr int NI = kTileM / 32 / WR, NJ = BN / 32 / WC;
@@ -60,13 +60,15 @@ struct HeadTile {
 };
 
 // One operand's tile: from `base` on, `left` bytes may be read. Plain: `rows`
-// rows exist (those past them repeat the last), and the contraction is padded.
+// rows exist (those past them repeat the last), a stage lies `step` bytes behind
+// the one ahead of it, and the contraction is padded.
 // TR: `rows` values of k exist, at least one (those past them repeat the last:
 // the other operand holds zeros there). PARTS: see Fetch.
 struct Operand {
   const char* base;
   int64_t left;
   int pitch, rows;
+  int64_t step;
 };
 
 // Memory to LDS, 16 bytes per lane and load. Plain: 128-byte rows, piece c of
@@ -87,7 +89,7 @@ struct Fetch {
   __device__ __forceinline__ int row(int t) const { return (t * WAVES + wave) * (kWave / kRowLanes) + lane / kRowLanes; }
   __device__ __forceinline__ int piece(int r) const {
     const int c = (lane % kRowLanes) ^ (TR ? 4 * (r % 4) : r / 2 % 8);
-    return PARTS ? c / 16 * 512 + c % 16 * 16 : c * 16;
+    return PARTS ? c / 8 * 256 + c % 8 * 16 : c * 16;
   }
   __device__ __forceinline__ void init(const Operand& o, int wave_, int lane_) {
     wave = wave_;
@@ -104,7 +106,7 @@ struct Fetch {
   __device__ __forceinline__ void load(const Operand& o, int k, int64_t more, lds_char* dst) const {
     if constexpr (FIRST < LAST) {
       const int first = RAGGED ? min(k * kStep, o.rows - 1) : k * kStep;
-      const int64_t at = more + (TR ? static_cast<int64_t>(first) * o.pitch : static_cast<int64_t>(k) * (kStep * 2));
+      const int64_t at = more + (TR ? static_cast<int64_t>(first) * o.pitch : k * o.step);
       const int64_t left = o.left - at;
       const __amdgpu_buffer_rsrc_t rsrc =
           __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(o.base + at), 0,
@@ -349,10 +351,10 @@ struct Head {
   float *pent, *a, *lse;  // by place
   int32_t* pidx;          // top rows of npad
   float *pq, *picked;     // the same: q and the logit there
-  char *xb, *xh;          // by place: x in bf16 and scaled in fp16, hp columns
+  char *xb, *xh;          // by place: x in bf16, 64 columns of all tokens beside each other, and scaled in fp16, 256 columns
   float2* stat;           // of one piece: per 32 * NI rows of the table, `piece` maxima and sums
-  float* logits;          // of one piece: piece x vp, then the fp16 parts of d
-  uint16_t* d;            // of one piece: bf16
+  float* logits;          // of one piece: 256 columns of all its tokens beside each other; then the fp16 parts of d
+  uint16_t* d;            // of one piece: bf16, 64 columns of all its tokens beside each other
   char* slabs;
 };
 
@@ -548,10 +550,9 @@ __global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uin
       h.a[p] = a;
     }
   }
-  uint16_t* xb = reinterpret_cast<uint16_t*>(h.xb) + static_cast<int64_t>(p) * h.hp;
-  _Float16* xh = reinterpret_cast<_Float16*>(h.xh) + static_cast<int64_t>(p) * h.hp;
   const bool vec = h.cols % 8 == 0;
-  for (int c = threadIdx.x * 8; c < h.hp; c += kThreads * 8) {
+  const int wide = GRAD ? (h.cols + kTileM - 1) / kTileM * kTileM : h.hp;
+  for (int c = threadIdx.x * 8; c < wide; c += kThreads * 8) {
     float v[8] = {};
     u32x4 raw = {};
     if (live && vec) {
@@ -562,13 +563,14 @@ __global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uin
       for (int e = 0; e < 8; ++e) e16[e] = c + e < h.cols ? x[t * h.cols + c + e] : 0u;
       raw = u32x4{e16[0] | e16[1] << 16, e16[2] | e16[3] << 16, e16[4] | e16[5] << 16, e16[6] | e16[7] << 16};
     }
-    *reinterpret_cast<u32x4*>(xb + c) = raw;
+    if (c < h.hp)
+      *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(h.xb) + (static_cast<int64_t>(c / kStep) * h.npad + p) * kStep + c % kStep) = raw;
     if constexpr (GRAD) {
       In<true>::widen(raw, v);
       h8 y;
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = a == 0.0f ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(ldexpf(v[e], shift));
-      *reinterpret_cast<h8*>(xh + c) = y;
+      *reinterpret_cast<h8*>(reinterpret_cast<_Float16*>(h.xh) + (static_cast<int64_t>(c / kTileM) * h.npad + p) * kTileM + c % kTileM) = y;
     }
   }
 }
@@ -605,10 +607,10 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Hea
   if (o < 0) return;
   const TileAt at = tile_at(o, n_tiles, m_tiles, false);
   const int v0 = at.m * kTileM, p0 = piece * h.piece + at.n * BN;
-  const int64_t row_bytes = static_cast<int64_t>(h.hp) * 2;
-  const int64_t from = static_cast<int64_t>(v0) * h.pitch;
-  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - v0};
-  const Operand q = {h.xb + p0 * row_bytes, BN * row_bytes, static_cast<int>(row_bytes), BN};
+  const int64_t from = static_cast<int64_t>(v0) * h.pitch, x_from = static_cast<int64_t>(p0) * (kStep * 2);
+  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - v0, kStep * 2};
+  const int64_t x_step = static_cast<int64_t>(h.npad) * (kStep * 2);
+  const Operand q = {h.xb + x_from, h.hp / kStep * x_step - x_from, kStep * 2, BN, x_step};
   HeadAcc<BN> acc = {};
   Contract<BN, false, false, false, false, false>(p, q, h.hp / kStep, false, 0, lds, acc);
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave, half = lane / 32;
@@ -661,7 +663,7 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Hea
     }
     if constexpr (STORE) {
       if (live) {
-        float* out = h.logits + static_cast<int64_t>(place) * h.vp + first + half * 4;
+        float* out = h.logits + (static_cast<int64_t>(at.m) * h.piece + place) * kTileM + (first - v0) + half * 4;
 #pragma unroll
         for (int i = 0; i < T::NI; ++i)
 #pragma unroll
@@ -724,36 +726,35 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
 
 // ------------------------------------------------------------------ gradients
 
-// d = p - q of one token and kDeltaCols columns: bf16 for dx, and times the
-// token's share of the gradient, scaled, in fp16 parts for dW, where the logits
-// lay: 128 logits give way to 128 values of each part, and those that a wave
-// overwrites are its own, read before.
-constexpr int kDeltaCols = 8192;
+// d = p - q of kDeltaTokens tokens and kDeltaCols columns: bf16 for dx, and
+// times the token's share of the gradient, scaled, in fp16 parts for dW, where
+// the logits lay: 64 logits give way to 64 values of each part, and those that a
+// wave overwrites are its own, read before.
+constexpr int kDeltaTokens = 16, kDeltaCols = 512;
 template <bool TWO>
 __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece) {
-  __shared__ int row[kMaxTop];
-  __shared__ float share[kMaxTop];
-  const int count = h.pieces[piece].count, place = blockIdx.x;
-  if (place >= (count + kStep - 1) / kStep * kStep) return;
-  const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
-  const bool live = place < count;
-  const float a = live ? h.a[mine] : 0.0f, z = live ? h.lse[mine] : 0.0f;
-  const bool zero = a == 0.0f;
-  const float g = ldexpf(a, 15 - h.info->ec);
-  float* logits = h.logits + static_cast<int64_t>(place) * h.vp;
-  uint16_t* d16 = h.d + static_cast<int64_t>(place) * h.vp;
-  const int k = max(h.top, 1), c0 = blockIdx.y * kDeltaCols, c1 = min(c0 + kDeltaCols, h.vp);
-  const int slot = threadIdx.x;
-  if (live && slot < k) {
-    row[slot] = h.pidx[static_cast<int64_t>(slot) * h.npad + mine];
-    share[slot] = h.pq[static_cast<int64_t>(slot) * h.npad + mine];
-  }
-  auto part = [&](int c) { return reinterpret_cast<_Float16*>(logits) + c / kPart * (2 * kPart) + c % kPart; };
-  for (int c = c0 + slot * 8; c < c1; c += kThreads * 8) {
+  const int count = h.pieces[piece].count, places = (count + kStep - 1) / kStep * kStep;
+  const int t0 = blockIdx.x * kDeltaTokens, c0 = blockIdx.y * kDeltaCols;
+  if (t0 >= places) return;
+  const int64_t first = static_cast<int64_t>(piece) * h.piece;
+  const int up = 15 - h.info->ec;
+  auto part = [&](int place, int c) {
+    return reinterpret_cast<_Float16*>(h.logits + (static_cast<int64_t>(c / kTileM) * h.piece + place) * kTileM + c % kTileM / kPart * kPart) + c % kPart;
+  };
+  auto d16 = [&](int place, int c) { return h.d + (static_cast<int64_t>(c / kStep) * h.piece + place) * kStep + c % kStep; };
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int u = wave; u < kDeltaTokens / 8 * (kDeltaCols / kPart); u += kThreads / kWave) {   // 8 tokens by 64 columns
+    const int place = t0 + u % (kDeltaTokens / 8) * 8 + lane / 8, c = c0 + u / (kDeltaTokens / 8) * kPart + lane % 8 * 8;
+    if (c >= h.vp) continue;
+    const bool live = place < count;
+    const float a = live ? h.a[first + place] : 0.0f;
     u32x4 out = {};
     h8 hi = {}, lo = {};
-    if (!zero) {
-      const f32x4 l0 = *reinterpret_cast<const f32x4*>(logits + c), l1 = *reinterpret_cast<const f32x4*>(logits + c + 4);
+    if (a != 0.0f) {
+      const float z = h.lse[first + place], g = ldexpf(a, up);
+      const f32x4* l = reinterpret_cast<const f32x4*>(h.logits + (static_cast<int64_t>(c / kTileM) * h.piece + place) * kTileM + c % kTileM);
+      const f32x4 l0 = l[0], l1 = l[1];
       uint32_t b[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -764,26 +765,34 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
       }
       out = u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16};
     }
-    *reinterpret_cast<u32x4*>(d16 + c) = out;
-    *reinterpret_cast<h8*>(part(c)) = hi;
-    if constexpr (TWO) *reinterpret_cast<h8*>(part(c) + kPart) = lo;
+    *reinterpret_cast<u32x4*>(d16(place, c)) = out;
+    *reinterpret_cast<h8*>(part(place, c)) = hi;
+    if constexpr (TWO) *reinterpret_cast<h8*>(part(place, c) + kPart) = lo;
   }
-  if (zero) return;
   __syncthreads();   // the targets' columns again, with their share; the first of equal rows has all of it
-  if (slot >= k) return;
-  const int c = row[slot];
-  if (c < c0 || c >= c1) return;
-  float q = 0.0f;
-  for (int s = 0; s < k; ++s) {
-    if (row[s] != c) continue;
-    if (s < slot) return;
-    q += share[s];
+  const int k = max(h.top, 1);
+  for (int i = threadIdx.x; i < k * kDeltaTokens; i += kThreads) {
+    const int place = t0 + i % kDeltaTokens, slot = i / kDeltaTokens;
+    if (place >= count) continue;
+    const int64_t mine = first + place;
+    auto at = [&](int s) { return static_cast<int64_t>(s) * h.npad + mine; };
+    const int c = h.pidx[at(slot)];
+    const float a = h.a[mine];
+    if (c < c0 || c >= c0 + kDeltaCols || a == 0.0f) continue;
+    float q = 0.0f;
+    bool mine_first = true;
+    for (int s = 0; s < k; ++s) {
+      if (h.pidx[at(s)] != c) continue;
+      mine_first &= s >= slot;
+      q += h.pq[at(s)];
+    }
+    if (!mine_first) continue;
+    const float p = exp_of(h.picked[at(slot)] - h.lse[mine]) - q, y = p * ldexpf(a, up);
+    *d16(place, c) = static_cast<uint16_t>(bf16_rne(p));
+    const _Float16 hi = static_cast<_Float16>(y);
+    *part(place, c) = hi;
+    if constexpr (TWO) part(place, c)[kPart] = static_cast<_Float16>(y - static_cast<float>(hi));
   }
-  const float p = exp_of(h.picked[static_cast<int64_t>(slot) * h.npad + mine] - z) - q, y = p * g;
-  d16[c] = static_cast<uint16_t>(bf16_rne(p));
-  const _Float16 hi = static_cast<_Float16>(y);
-  *part(c) = hi;
-  if constexpr (TWO) part(c)[kPart] = static_cast<_Float16>(y - static_cast<float>(hi));
 }
 
 // dx of a piece: 256 columns by BN tokens, one part of the contraction over the
@@ -804,10 +813,9 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_kernel(Head h,
   // stages behind the table's last row repeat it; d is zero there
   const int row = min(k0 * kStep, h.rows - 1);
   const int64_t from = static_cast<int64_t>(row) * h.pitch + at.m * (kTileM * 2);
-  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - row};
-  const int64_t row_bytes = static_cast<int64_t>(h.vp) * 2;
-  const Operand q = {reinterpret_cast<const char*>(h.d) + at.n * BN * row_bytes + k0 * (kStep * 2), BN * row_bytes - k0 * (kStep * 2),
-                     static_cast<int>(row_bytes), BN};
+  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - row, 0};
+  const int64_t d_step = static_cast<int64_t>(h.piece) * (kStep * 2), d_from = k0 * d_step + at.n * (BN * kStep * 2);
+  const Operand q = {reinterpret_cast<const char*>(h.d) + d_from, ksteps * d_step - d_from, kStep * 2, BN, d_step};
   HeadAcc<BN> acc = {};
   Contract<BN, false, true, false, true, false>(p, q, k1 - k0, false, 0, lds, acc);
   char* out = h.slabs + static_cast<int64_t>(o) * (kTileM * BN * 4) + fresh_thread() * 16;
@@ -869,52 +877,83 @@ __global__ __launch_bounds__(HeadTile<256>::kThreads) void head_dw_kernel(Head h
   const HeadInfo info = *h.info;
   const int count = h.pieces[piece].count, depth = (count + kStep - 1) / kStep * kStep;
   if (count == 0 && in == out) return;   // nothing to add
-  const int64_t row_bytes = static_cast<int64_t>(h.hp) * 2, d_bytes = static_cast<int64_t>(h.vp) * 4;
-  const int64_t from = static_cast<int64_t>(piece) * h.piece * row_bytes + at.m * (kTileM * 2);
+  constexpr int kRow = kTileM * 2, kRowD = BN * 4, kLow = TWO ? kPart * 2 : 0;
+  const int64_t x_from = (static_cast<int64_t>(at.m) * h.npad + static_cast<int64_t>(piece) * h.piece) * kRow;
+  const int64_t d_from = static_cast<int64_t>(at.n) * h.piece * kRowD + kLow;
   const int c0 = at.n * BN;
-  const Operand p = {h.xh + from, h.npad * row_bytes - from, static_cast<int>(row_bytes), depth};
-  const Operand q = {reinterpret_cast<const char*>(h.logits) + static_cast<int64_t>(c0) * 4 + (TWO ? kPart * 2 : 0),
-                     h.piece * d_bytes - static_cast<int64_t>(c0) * 4 - (TWO ? kPart * 2 : 0), static_cast<int>(d_bytes), depth};
+  const Operand p = {h.xh + x_from, static_cast<int64_t>(m_tiles) * h.npad * kRow - x_from, kRow, depth, 0};
+  const Operand q = {reinterpret_cast<const char*>(h.logits) + d_from, static_cast<int64_t>(n_tiles) * h.piece * kRowD - d_from, kRowD, depth, 0};
   HeadAcc<BN> acc = {};
-  Contract<BN, true, true, true, false, true>(p, q, (TWO ? 2 : 1) * depth / kStep, TWO, -(kPart * 2), lds, acc);
+  Contract<BN, true, true, true, false, true>(p, q, (TWO ? 2 : 1) * depth / kStep, TWO, -kLow, lds, acc);
+  // Half of the table's rows at a time go through LDS, 1 KiB each, so that whole
+  // rows are read and written: piece c of row r at place c ^ (r % 32).
+  constexpr int kPassCols = T::NJ / 2, kRows = BN / 2;
+  static_assert(kRows * kTileM * 4 <= T::kLds, "half a tile");
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
-  const int up = info.ec + info.ex - 29;
-  const bool vec = h.cols % 4 == 0;
+  const int up = info.ec + info.ex - 29, width = min(h.cols - at.m * kTileM, kTileM);
+  auto finish = [&](float x, float before) {
+    const float y = __builtin_ldexpf(x, up) * sigma + 0.0f;   // never -0.0
+    return in ? before + y : y;
+  };
 #pragma unroll
-  for (int j = 0; j < T::NJ; ++j) {
-    const int v = c0 + (wave % T::WC * T::NJ + j) * 32 + lane % 32;
-    if (v >= h.rows) continue;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) barrier();
 #pragma unroll
-    for (int i = 0; i < T::NI; ++i)
+    for (int jj = 0; jj < kPassCols; ++jj)
 #pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int c = at.m * kTileM + (wave / T::WC * T::NI + i) * 32 + e * 2 + lane / 32 * 4;
-        if (c >= h.cols) continue;
-        const int64_t to = static_cast<int64_t>(v) * h.cols + c;
-        float y[4];
+      for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) y[t] = __builtin_ldexpf(acc.v[i][j][e + t], up) * sigma + 0.0f;   // never -0.0
-        if (vec) {
-          if (in) {
-            const f32x4 before = *reinterpret_cast<const f32x4*>(in + to);
+        for (int e = 0; e < 16; e += 4) {
+          const f32x16& x = acc.v[i][pass * kPassCols + jj];
+          const int r = (wave % T::WC * kPassCols + jj) * 32 + lane % 32;
+          const int c = (wave / T::WC * T::NI + i) * 8 + e / 2 + lane / 32;
+          *reinterpret_cast<f32x4*>(lds + r * (kTileM * 4) + (c ^ r % 32) * 16) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+        }
+    wait<63, true>();
+    barrier();
+    constexpr int kAhead = 8;
+    static_assert(kRows / T::kWaves % kAhead == 0, "whole batches");
+#pragma unroll 1
+    for (int r0 = wave * (kRows / T::kWaves); r0 < (wave + 1) * (kRows / T::kWaves); r0 += kAhead) {
+      const int j0 = r0 / 32, first = c0 + (j0 / kPassCols * T::NJ + pass * kPassCols + j0 % kPassCols) * 32 + r0 % 32;
+      const int64_t to = static_cast<int64_t>(first) * h.cols + at.m * kTileM;
+      if (h.cols % 4 == 0) {
+        const int c = lane * 4;
+        f32x4 before[kAhead], x[kAhead];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) y[t] = before[t] + y[t];
-          }
+        for (int u = 0; u < kAhead; ++u) {
+          before[u] = f32x4{};
+          if (in && c < width && first + u < h.rows) before[u] = *reinterpret_cast<const f32x4*>(in + to + static_cast<int64_t>(u) * h.cols + c);
+          x[u] = *reinterpret_cast<const f32x4*>(lds + (r0 + u) * (kTileM * 4) + (lane ^ (r0 + u) % 32) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (c >= width || first + u >= h.rows) continue;
+          f32x4 y;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) y[t] = finish(x[u][t], before[u][t]);
+          const int64_t at_row = to + static_cast<int64_t>(u) * h.cols + c;
           if constexpr (OUT16)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + to) =
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at_row) =
                 u32x2{bf16_rne(y[0]) | bf16_rne(y[1]) << 16, bf16_rne(y[2]) | bf16_rne(y[3]) << 16};
           else
-            *reinterpret_cast<f32x4*>(static_cast<float*>(out) + to) = f32x4{y[0], y[1], y[2], y[3]};
-        } else {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at_row) = y;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            if (c + t >= h.cols) continue;
-            if (in) y[t] = in[to + t] + y[t];
-            if constexpr (OUT16) static_cast<uint16_t*>(out)[to + t] = static_cast<uint16_t>(bf16_rne(y[t]));
-            else static_cast<float*>(out)[to + t] = y[t];
+            const int c = t * kWave + lane;
+            if (c >= width || first + u >= h.rows) continue;
+            const float x = *reinterpret_cast<const float*>(lds + (r0 + u) * (kTileM * 4) + (c / 4 ^ (r0 + u) % 32) * 16 + c % 4 * 4);
+            const int64_t at_row = to + static_cast<int64_t>(u) * h.cols + c;
+            const float y = finish(x, in ? in[at_row] : 0.0f);
+            if constexpr (OUT16) static_cast<uint16_t*>(out)[at_row] = static_cast<uint16_t>(bf16_rne(y));
+            else static_cast<float*>(out)[at_row] = y;
           }
-        }
       }
+    }
   }
 }
 
@@ -989,7 +1028,7 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->xb = room(s->npad * s->hp * 2);
   s->stat = room(s->piece * (s->vp / 64) * 8);
   s->table = room(s->widen ? s->rows * s->hp * 2 : 0);
-  s->xh = room(grad ? s->npad * s->hp * 2 : 0);
+  s->xh = room(grad ? s->npad * up_to(s->cols, kTileM) * 2 : 0);
   s->logits = room(grad ? s->piece * s->vp * 4 : 0);
   s->d = room(grad ? s->piece * s->vp * 2 : 0);
   s->slabs = room(grad ? s->dx_groups * kTileM * s->tile_n * 4 : 0);
@@ -1035,7 +1074,7 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
                        piece, static_cast<int>(s.vp / (32 * HeadTile<BN>::NI)), f, a.loss);
     if (!grad) continue;
     const bool two = a.packed_dt == RS_F32;
-    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStep)), static_cast<unsigned>((s.vp + kDeltaCols - 1) / kDeltaCols));
+    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStep) / kDeltaTokens), static_cast<unsigned>((s.vp + kDeltaCols - 1) / kDeltaCols));
     if (two) hipLaunchKernelGGL(head_delta_kernel<true>, delta, dim3(kThreads), 0, q, h, piece);
     else hipLaunchKernelGGL(head_delta_kernel<false>, delta, dim3(kThreads), 0, q, h, piece);
     const int64_t dx_m = (s.cols + kTileM - 1) / kTileM;
