@@ -42,22 +42,30 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr int kTileM = 256;          // rows of an output tile: its contiguous dimension in memory
 constexpr int kStep = 64;            // of the contraction, per stage; what it is padded to
 constexpr int kPart = 64;            // columns of d whose fp16 parts lie beside each other
-constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
+// Two values rounded to nearest-even bf16 by one instruction.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, b2));
+}
 
 // ------------------------------------------------------------------ products
 
 // C[m, n] = sum_k P[m, k] Q[n, k] on one 256 x BN tile, 32 x 32 accumulators. Either operand may lie with k contiguous (plain) or with its
 // other index contiguous (TR): a TR operand is read out of LDS transposed
 // (ds_read_b64_tr_b16), so the table and d are used as they lie in memory.
-template <int BN>
+template <int BN, int WAVES = BN == 256 ? 4 : 8>
 struct HeadTile {
-  static constexpr int kWaves = BN == 256 ? 4 : 8, kThreads = kWaves * kWave;
+  static constexpr int kN = BN, kWaves = WAVES, kThreads = kWaves * kWave;
   static constexpr int WR = BN == 256 ? 2 : 4;              // wave rows
   static constexpr int WC = kWaves / WR;
   static constexpr int NI = kTileM / 32 / WR, NJ = BN / 32 / WC;
   static constexpr int kStages = BN == 256 ? 2 : BN == 128 ? 3 : 4, kStagesQ = BN == 256 ? 3 : kStages;
   static constexpr int kLds = (kStages * kTileM + kStagesQ * BN) * kStep * 2;
 };
+using DwTile = HeadTile<256, 8>;
 
 // One operand's tile: from `base` on, `left` bytes may be read. Plain: `rows`
 // rows exist (those past them repeat the last), a stage lies `step` bytes behind
@@ -91,9 +99,7 @@ struct Fetch {
     const int c = (lane % kRowLanes) ^ (TR ? 4 * (r % 4) : r / 2 % 8);
     return PARTS ? c / 8 * 256 + c % 8 * 16 : c * 16;
   }
-  __device__ __forceinline__ void init(const Operand& o, int wave_, int lane_) {
-    wave = wave_;
-    lane = lane_;
+  __device__ __forceinline__ void init(const Operand& o) {
 #pragma unroll
     for (int t = 0; t < kLoads; ++t) {
       const int r = row(t);
@@ -161,26 +167,26 @@ struct Fragments {
   }
 };
 
-template <int BN>
+template <class T>
 struct HeadAcc {
-  f32x16 v[HeadTile<BN>::NI][HeadTile<BN>::NJ];
+  f32x16 v[T::NI][T::NJ];
 };
 
 // The contraction, in `ksteps` stages. With `two`, after the first half of them
 // P starts over and Q starts over at its other part, `second` bytes further on.
-//   One stage: three sixteen-column multiplications, each while the next
-// fragment is read; then, with every wave done reading this stage and the next
-// one arrived, the fourth under the first reads of the next stage. From there
+//   One stage: sixteen-column multiplications, each while the next fragment is
+// read; then, with every wave done reading this stage and the next one arrived,
+// the last of them under the first reads of the next stage. From there
 // on, spread over a whole stage, the places that this stage leaves are loaded
 // again, P's for kStages stages later and behind them Q's for kStagesQ later.
 // A load into LDS holds its wave up while others are on their way, so loads in
 // one burst stop the multiplications: 8 of them after each turn took 4096 x
 // 131072 x 4096 from 2.85 (loads left out) to 3.33 ms.
-template <int BN, bool F16, bool PT, bool QT, bool RAGGED, bool PARTS>
+template <class T, bool F16, bool PT, bool QT, bool RAGGED, bool PARTS>
 struct Contract {
-using T = HeadTile<BN>;
 using FP = Fetch<kTileM, PT, RAGGED, false, T::kWaves>;
-using FQ = Fetch<BN, QT, false, PARTS, T::kWaves>;
+using FQ = Fetch<T::kN, QT, false, PARTS, T::kWaves>;
+static constexpr int kParts = kStep / 16;   // multiplications of a stage, and parts of its loads
 static constexpr int SP = T::kStages, SQ = T::kStagesQ, U = SP == SQ ? SP : SP * SQ;
 static constexpr int LP = FP::kLoads, LQ = FQ::kLoads, kLoads = LP + LQ;
 static constexpr int kReads = T::NI * (PT ? 2 : 1) + T::NJ * (QT ? 2 : 1), kMuls = T::NI * T::NJ;
@@ -193,9 +199,8 @@ lds_char* base;
 FP fp;
 FQ fq;
 Fragments<kTileM, PT, T::NI> rp;
-Fragments<BN, QT, T::NJ> rq;
+Fragments<T::kN, QT, T::NJ> rq;
 u32x4 fa[2][T::NI], fb[2][T::NJ];
-HeadAcc<BN>& c;
 
 template <int FIRST, int LAST>
 __device__ __forceinline__ void load_p(int s, int place) {
@@ -205,10 +210,10 @@ template <int FIRST, int LAST>
 __device__ __forceinline__ void load_q(int s, int place) {
   fq.template load<FIRST, LAST>(q, s < turn ? s : s - turn, s < turn ? 0 : second, base + SP * FP::kBytes + place * FQ::kBytes);
 }
-// Quarter Q4 of what is loaded into the places of stage s.
-template <int Q4>
-__device__ __forceinline__ void load_quarter(int s, int pp, int qp, bool whole) {
-  constexpr int a = kLoads * Q4 / 4, b = kLoads * (Q4 + 1) / 4;
+// Part PART of what is loaded into the places of stage s.
+template <int PART>
+__device__ __forceinline__ void load_part(int s, int pp, int qp, bool whole) {
+  constexpr int a = kLoads * PART / kParts, b = kLoads * (PART + 1) / kParts;
   if (whole || s + SP < ksteps) load_p<(a < LP ? a : LP), (b < LP ? b : LP)>(s + SP, pp);
   if (whole || s + SQ < ksteps) load_q<(a > LP ? a - LP : 0), (b > LP ? b - LP : 0)>(s + SQ, qp);
 }
@@ -218,7 +223,7 @@ __device__ __forceinline__ void fetch(int pp, int qp, int kk, int to) {
 #pragma unroll
   for (int i = 0; i < T::NI; ++i) fa[to][i] = rp.read(i, kk, pp);
 }
-__device__ __forceinline__ void mma(int from) {
+__device__ __forceinline__ void mma(HeadAcc<T>& c, int from) {
 #pragma unroll
   for (int i = 0; i < T::NI; ++i)
 #pragma unroll
@@ -246,56 +251,76 @@ __device__ static __forceinline__ void interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 template <int KK>
-__device__ __forceinline__ void sixteen(int s, int pp, int qp, int before_p, int before_q, bool whole) {
+__device__ __forceinline__ void sixteen(HeadAcc<T>& c, int s, int pp, int qp, int before_p, int before_q, bool whole) {
   fetch(pp, qp, KK + 1, (KK + 1) & 1);
-  if (whole || s > 0) load_quarter<KK + 1>(s - 1, before_p, before_q, whole);
-  mma(KK & 1);
-  interleave<kLoads * (KK + 2) / 4 - kLoads * (KK + 1) / 4>();
+  if (whole || s > 0) load_part<KK + 1>(s - 1, before_p, before_q, whole);
+  mma(c, KK & 1);
+  interleave<kLoads * (KK + 2) / kParts - kLoads * (KK + 1) / kParts>();
 }
 // Stage s, in places pp and qp; before_p, before_q: those of stage s - 1.
 // whole: everything that a stage loads exists, and stages ahead of this one.
-__device__ __forceinline__ void step(int s, int pp, int qp, int next_p, int next_q, int before_p, int before_q, bool whole) {
-  sixteen<0>(s, pp, qp, before_p, before_q, whole);
-  sixteen<1>(s, pp, qp, before_p, before_q, whole);
-  sixteen<2>(s, pp, qp, before_p, before_q, whole);
+__device__ __forceinline__ void step(HeadAcc<T>& c, int s, int pp, int qp, int next_p, int next_q, int before_p, int before_q, bool whole) {
+  sixteen<0>(c, s, pp, qp, before_p, before_q, whole);
+  sixteen<1>(c, s, pp, qp, before_p, before_q, whole);
+  sixteen<2>(c, s, pp, qp, before_p, before_q, whole);
   // newer than the next stage's loads: SP - 2 turns' and Q's of one stage more
   if (whole || s + SQ <= ksteps) wait<(SP - 2) * kLoads + (SQ - SP) * LQ, true>();
   else wait<0, true>();
   barrier();
   if (whole || s + 1 < ksteps) fetch(next_p, next_q, 0, 0);
-  load_quarter<0>(s, pp, qp, whole);
-  mma(1);
-  interleave<kLoads / 4>();
+  load_part<0>(s, pp, qp, whole);
+  mma(c, 1);
+  interleave<kLoads / kParts>();
 }
 
-__device__ __forceinline__ Contract(const Operand& p_, const Operand& q_, int ksteps_, bool two, int64_t second_, char* lds, HeadAcc<BN>& c_)
-    : p(p_), q(q_), ksteps(ksteps_), turn(two ? ksteps_ / 2 : ksteps_), second(second_), base((lds_char*)lds), c(c_) {
+__device__ __forceinline__ explicit Contract(char* lds) : base((lds_char*)lds) {
   const int tid = fresh_thread(), lane = tid % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  fp.init(p, wave, lane);
-  fq.init(q, wave, lane);
-  rp.init(lds, wave / T::WC * T::NI, lane);
-  rq.init(lds + SP * FP::kBytes, wave % T::WC * T::NJ, lane);
-  if (ksteps == 0) return;
+  fp.wave = fq.wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  fp.lane = fq.lane = lane;
+  rp.init(lds, fp.wave / T::WC * T::NI, lane);
+  rq.init(lds + SP * FP::kBytes, fp.wave % T::WC * T::NJ, lane);
+}
+
+// The first stages' loads of a tile. Every wave has left the loop of run for
+// the tile ahead of it, which is done with LDS then, so a tile's loads can be
+// on their way while the one ahead of it is stored.
+__device__ __forceinline__ void begin(const Operand& p_, const Operand& q_, int ksteps_, bool two, int64_t second_) {
+  p = p_;
+  q = q_;
+  ksteps = ksteps_;
+  turn = two ? ksteps / 2 : ksteps;
+  second = second_;
+  fp.init(p);
+  fq.init(q);
 #pragma unroll
   for (int s = 0; s < SQ; ++s) {
     if (s < SP && s < ksteps) load_p<0, LP>(s, s);
     if (s < ksteps) load_q<0, LQ>(s, s);
   }
-  if (ksteps >= SQ) wait<(SP - 1) * kLoads + (SQ - SP) * LQ, false>();
+}
+
+// c <- the contraction. ahead: what has been loaded or stored since begin is
+// counted as well, so all of it has to arrive.
+__device__ __forceinline__ void run(HeadAcc<T>& c, bool ahead) {
+#pragma unroll
+  for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j) c.v[i][j] = f32x16{};
+  if (ksteps == 0) return;
+  if (!ahead && ksteps >= SQ) wait<(SP - 1) * kLoads + (SQ - SP) * LQ, false>();
   else wait<0, false>();
   barrier();
   fetch(0, 0, 0, 0);
   int s = 0;
   if (ksteps > 2 * U) {   // the first has no stage ahead of it
-    step(0, 0, 0, 1 % SP, 1 % SQ, 0, 0, false);
+    step(c, 0, 0, 0, 1 % SP, 1 % SQ, 0, 0, false);
     for (s = 1; s + U - 1 + SQ < ksteps; s += U) {
 #pragma unroll
       for (int u = 1; u <= U; ++u)
-        step(s + u - 1, u % SP, u % SQ, (u + 1) % SP, (u + 1) % SQ, (u - 1) % SP, (u - 1) % SQ, true);
+        step(c, s + u - 1, u % SP, u % SQ, (u + 1) % SP, (u + 1) % SQ, (u - 1) % SP, (u - 1) % SQ, true);
     }
   }
-  for (; s < ksteps; ++s) step(s, s % SP, s % SQ, (s + 1) % SP, (s + 1) % SQ, (s + SP - 1) % SP, (s + SQ - 1) % SQ, false);
+  for (; s < ksteps; ++s) step(c, s, s % SP, s % SQ, (s + 1) % SP, (s + 1) % SQ, (s + SP - 1) % SP, (s + SQ - 1) % SQ, false);
 }
 };
 
@@ -313,13 +338,17 @@ __device__ __forceinline__ TileAt tile_at(int o, int across, int along, bool m_a
   return m_across ? TileAt{a, b} : TileAt{b, a};
 }
 
-// Work item of this workgroup out of n: workgroup b runs on XCD b % 8, and each
-// XCD takes a contiguous eighth. -1: none.
-__device__ __forceinline__ int xcd_item(int n) {
-  const int per = (n + 7) / 8, slot = static_cast<int>(blockIdx.x) / 8;
-  const int o = static_cast<int>(blockIdx.x) % 8 * per + slot;
-  return slot < per && o < n ? o : -1;
-}
+// The work items of this workgroup out of n: workgroup b runs on XCD b % 8, and
+// each XCD takes a contiguous eighth, its workgroups in turn.
+struct Items {
+  int now, end, stride;
+  __device__ __forceinline__ explicit Items(int n) {
+    const int per = (n + 7) / 8, xcd = static_cast<int>(blockIdx.x) % 8;
+    now = xcd * per + static_cast<int>(blockIdx.x) / 8;
+    end = min((xcd + 1) * per, n);
+    stride = static_cast<int>(gridDim.x) / 8;
+  }
+};
 
 // ------------------------------------------------------------------ call
 
@@ -345,12 +374,12 @@ struct Head {
   HeadPiece* pieces;
   uint32_t* keep;         // by token: has a target
   float *xmax, *ent;      // by token: largest finite |x|, sum q log q
-  int32_t* idx;           // by token, top each: row of the table or -1
+  int32_t* idx;           // by token, top each, ascending: row of the table, kNone behind them
   float* q;
   int32_t* kept;          // by place: the token
-  float *pent, *a, *lse;  // by place
-  int32_t* pidx;          // top rows of npad
-  float *pq, *picked;     // the same: q and the logit there
+  float *pent, *a, *lse;  // by place; lse in powers of two
+  int32_t* pidx;          // by place, top each: the same
+  float *pq, *picked;     // q and the logit there
   char *xb, *xh;          // by place: x in bf16, 64 columns of all tokens beside each other, and scaled in fp16, 256 columns
   float2* stat;           // of one piece: per 32 * NI rows of the table, `piece` maxima and sums
   float* logits;          // of one piece: 256 columns of all its tokens beside each other; then the fp16 parts of d
@@ -361,9 +390,10 @@ struct Head {
 // ------------------------------------------------------------------ targets
 
 constexpr int kMaxTop = 256;
+constexpr int kNone = 0x7fffffff;   // behind every row of the table
 
-// One token a wave: its rows of the table and their share q, whether it has
-// any, and the largest finite |x| (GRAD). A token without a target gets its
+// One token a wave: its rows of the table in ascending order and their share q,
+// whether it has any, and the largest finite |x| (GRAD). A token without a target gets its
 // loss (and dx) of zero here.
 template <bool GRAD>
 __global__ __launch_bounds__(kThreads) void head_targets_kernel(Head h, const void* ids, bool wide, const void* teacher,
@@ -379,7 +409,7 @@ __global__ __launch_bounds__(kThreads) void head_targets_kernel(Head h, const vo
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int s = i * kWave + lane;
-    row[i] = -1;
+    row[i] = kNone;
     z[i] = -INFINITY;
     if (s < k) {
       const int64_t at = t * k + s;
@@ -393,28 +423,37 @@ __global__ __launch_bounds__(kThreads) void head_targets_kernel(Head h, const vo
   }
   bool some = false;   // a teacher's logit of -inf is no target, one of NaN is
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) some |= row[i] >= 0 && !(z[i] == -INFINITY);
+  for (int i = 0; i < kSlots; ++i) some |= row[i] != kNone && !(z[i] == -INFINITY);
 #pragma unroll
   for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
   some = __any(some);
   float sum = 0.0f, ent = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
-    z[i] = row[i] >= 0 && some ? expf((z[i] - top) / temperature) : 0.0f;
+    z[i] = row[i] != kNone && some ? expf((z[i] - top) / temperature) : 0.0f;
     sum += z[i];
   }
 #pragma unroll
   for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
-    const int s = i * kWave + lane;
     z[i] = some ? z[i] / sum : 0.0f;
     if (!(z[i] == 0.0f)) ent += z[i] * logf(z[i]);
-    if (s < k) {
-      h.idx[t * k + s] = row[i];
-      h.q[t * k + s] = z[i];
-    }
   }
+  int rank[kSlots] = {};   // by row, equal ones by place
+#pragma unroll
+  for (int r = 0; r < kSlots; ++r)
+    for (int l = 0; l < kWave && r * kWave + l < k; ++l) {
+      const int other = __builtin_amdgcn_readlane(row[r], l);
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) rank[i] += other < row[i] || (other == row[i] && r * kWave + l < i * kWave + lane);
+    }
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (i * kWave + lane < k) {
+      h.idx[t * k + rank[i]] = row[i];
+      h.q[t * k + rank[i]] = z[i];
+    }
 #pragma unroll
   for (int o = kWave / 2; o > 0; o >>= 1) ent += __shfl_xor(ent, o, kWave);
   float most = 0.0f;
@@ -542,8 +581,8 @@ __global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uin
   if (live) {
     const int k = max(h.top, 1);
     for (int s = threadIdx.x; s < k; s += kThreads) {
-      h.pidx[static_cast<int64_t>(s) * h.npad + p] = h.idx[t * k + s];
-      h.pq[static_cast<int64_t>(s) * h.npad + p] = h.q[t * k + s];
+      h.pidx[static_cast<int64_t>(p) * k + s] = h.idx[t * k + s];
+      h.pq[static_cast<int64_t>(p) * k + s] = h.q[t * k + s];
     }
     if (threadIdx.x == 0) {
       h.pent[p] = h.ent[t];
@@ -591,79 +630,86 @@ __global__ __launch_bounds__(kThreads) void head_widen_kernel(const uint16_t* ta
 
 // ------------------------------------------------------------------ logits
 
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// Exponentials are powers of two: 2^(l log2(e) - z), with maxima, log-sums and
+// z in powers of two, so that the product is not rounded by itself.
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// One tile of the logits of a piece, 256 rows of the table by BN tokens: the
-// largest and the sum of exponentials over the wave's rows for each token, the
-// logits at its targets, and (STORE) the logits themselves, -inf behind the
-// table's end. A lane holds one token's logits, so the sums are its own and
-// the other half wave's.
-template <int BN, bool STORE>
-__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Head h, int piece, float factor) {
-  using T = HeadTile<BN>;
-  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
-  const int count = h.pieces[piece].count, m_tiles = h.vp / kTileM, n_tiles = (count + BN - 1) / BN;
-  const int o = xcd_item(m_tiles * n_tiles);
-  if (o < 0) return;
-  const TileAt at = tile_at(o, n_tiles, m_tiles, false);
-  const int v0 = at.m * kTileM, p0 = piece * h.piece + at.n * BN;
-  const int64_t from = static_cast<int64_t>(v0) * h.pitch, x_from = static_cast<int64_t>(p0) * (kStep * 2);
-  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - v0, kStep * 2};
-  const int64_t x_step = static_cast<int64_t>(h.npad) * (kStep * 2);
-  const Operand q = {h.xb + x_from, h.hp / kStep * x_step - x_from, kStep * 2, BN, x_step};
-  HeadAcc<BN> acc = {};
-  Contract<BN, false, false, false, false, false>(p, q, h.hp / kStep, false, 0, lds, acc);
+// What is kept of one tile of the logits: for each token the largest and the
+// sum of exponentials over the wave's rows, the logits at its targets, and
+// (STORE) the logits themselves, -inf behind the table's end. A lane holds one
+// token's logits, so the sums are its own and the other half wave's.
+template <class T, bool STORE>
+__device__ __forceinline__ void keep_logits(const Head& h, int piece, int count, const TileAt& at, float factor, HeadAcc<T>& acc) {
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave, half = lane / 32;
-  const int first = v0 + wave / T::WC * T::NI * 32;   // the wave's first row of the table
+  const int row = wave / T::WC * T::NI * 32, first = at.m * kTileM + row;   // the wave's first row, in the tile and of the table
   const int k = max(h.top, 1);
+  const bool inside = first + T::NI * 32 <= h.rows;
+  // each token's first target that is no row ahead of the wave's
+  int slot[T::NJ], to[T::NJ];
 #pragma unroll
   for (int j = 0; j < T::NJ; ++j) {
-    const int place = at.n * BN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;   // in the piece
+    slot[j] = 0;
+    to[j] = at.n * T::kN + (wave % T::WC * T::NJ + j) * 32 + lane % 32 < count ? k : 0;
+  }
+  for (int left = k; left > 0; left >>= 1) {
+    int row_at[T::NJ];
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j) {
+      const int64_t mine = static_cast<int64_t>(piece) * h.piece + at.n * T::kN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;
+      row_at[j] = slot[j] < to[j] ? h.pidx[mine * k + (slot[j] + to[j]) / 2] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j) {
+      const int mid = (slot[j] + to[j]) / 2;
+      if (slot[j] < to[j] && row_at[j] < first) slot[j] = mid + 1;
+      else to[j] = mid;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < T::NJ; ++j) {
+    const int place = at.n * T::kN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;   // in the piece
     const bool live = place < count;
     const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc.v[i][j][e] *= factor;
+    if (!inside) {
+#pragma unroll
+      for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (first + i * 32 + e / 4 * 8 + half * 4 + e % 4 >= h.rows) acc.v[i][j][e] = -INFINITY;
+    }
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int v = first + i * 32 + e / 4 * 8 + half * 4 + e % 4;
-        const float l = v < h.rows ? acc.v[i][j][e] * factor : -INFINITY;
-        acc.v[i][j][e] = l;
-        top = fmaxf(top, l);
-      }
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc.v[i][j][e]);
+    top = fmaxf(top, __shfl_xor(top, 32, kWave)) * kLog2e;
     const float base = top == -INFINITY ? 0.0f : top;   // only -inf and NaN: the sum says which
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum += exp_of(acc.v[i][j][e] - base);
+      for (int e = 0; e < 16; ++e) sum += exp2_of(__builtin_fmaf(acc.v[i][j][e], kLog2e, -base));
     sum += __shfl_xor(sum, 32, kWave);
     if (live && half == 0) h.stat[static_cast<int64_t>(first / (32 * T::NI)) * h.piece + place] = float2{top, sum};
-    if (live) {
-      constexpr int kAhead = 8;   // targets looked at together: their loads do not wait for each other
-      for (int s0 = 0; s0 < k; s0 += kAhead) {
-        int r[kAhead];
+    if (live)
+      for (int t = slot[j]; t < k; ++t) {
+        const int hit = h.pidx[mine * k + t] - first;
+        if (hit >= T::NI * 32) break;
+        if (hit / 4 % 2 != half) continue;
+        float l = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) r[u] = s0 + u < k ? h.pidx[static_cast<int64_t>(s0 + u) * h.npad + mine] - first : -1;
-#pragma unroll 1
-        for (int u = 0; u < kAhead; ++u) {   // one body for all: hits are rare
-          int mine_r = -1;
+        for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-          for (int w = 0; w < kAhead; ++w) mine_r = u == w ? r[w] : mine_r;
-          if (mine_r < 0 || mine_r >= T::NI * 32 || mine_r / 4 % 2 != half) continue;
-          float l = 0.0f;
-#pragma unroll
-          for (int i = 0; i < T::NI; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) l = mine_r == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
-          h.picked[static_cast<int64_t>(s0 + u) * h.npad + mine] = l;
-        }
+          for (int e = 0; e < 16; ++e) l = hit == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
+        h.picked[mine * k + t] = l;
       }
-    }
     if constexpr (STORE) {
       if (live) {
-        float* out = h.logits + (static_cast<int64_t>(at.m) * h.piece + place) * kTileM + (first - v0) + half * 4;
+        float* out = h.logits + (static_cast<int64_t>(at.m) * h.piece + place) * kTileM + row + half * 4;
 #pragma unroll
         for (int i = 0; i < T::NI; ++i)
 #pragma unroll
@@ -672,6 +718,36 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Hea
                 f32x4{acc.v[i][j][e], acc.v[i][j][e + 1], acc.v[i][j][e + 2], acc.v[i][j][e + 3]};
       }
     }
+  }
+}
+
+// Tiles of the logits of a piece, 256 rows of the table by BN tokens.
+template <int BN, bool STORE>
+__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Head h, int piece, float factor) {
+  using T = HeadTile<BN>;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const int count = h.pieces[piece].count, m_tiles = h.vp / kTileM, n_tiles = (count + BN - 1) / BN;
+  Items items(m_tiles * n_tiles);
+  if (items.now >= items.end) return;
+  const int64_t x_step = static_cast<int64_t>(h.npad) * (kStep * 2);
+  Contract<T, false, false, false, false, false> product(lds);
+  auto begin = [&](const TileAt& at) {
+    const int64_t from = static_cast<int64_t>(at.m * kTileM) * h.pitch;
+    const int64_t x_from = (static_cast<int64_t>(piece) * h.piece + at.n * BN) * (kStep * 2);
+    product.begin({h.table + from, h.table_bytes - from, h.pitch, h.rows - at.m * kTileM, kStep * 2},
+                  {h.xb + x_from, h.hp / kStep * x_step - x_from, kStep * 2, BN, x_step}, h.hp / kStep, false, 0);
+  };
+  TileAt at = tile_at(items.now, n_tiles, m_tiles, false);
+  begin(at);
+  for (bool ahead = false;; ahead = true) {
+    HeadAcc<T> acc;
+    product.run(acc, ahead);
+    const TileAt done = at;
+    items.now += items.stride;
+    const bool more = items.now < items.end;
+    if (more) begin(at = tile_at(items.now, n_tiles, m_tiles, false));
+    keep_logits<T, STORE>(h, piece, count, done, factor, acc);
+    if (!more) return;
   }
 }
 
@@ -688,7 +764,7 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
   auto add = [&](float t, float s) {
     const float both = fmaxf(top, t), base = both == -INFINITY ? 0.0f : both;
     broken |= !(s >= 0.0f);
-    sum = sum * exp_of(top - base) + s * exp_of(t - base);
+    sum = sum * exp2_of(top - base) + s * exp2_of(t - base);
     top = both;
   };
   if (live)
@@ -703,17 +779,17 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
     top = -INFINITY;
     sum = 0.0f;
     for (int i = 0; i < 32; ++i) add(tops[tok][i], sums[tok][i]);
-    tops[tok][32] = h.lse[mine] = broken ? NAN : top + logf(sum);
+    tops[tok][32] = h.lse[mine] = broken ? NAN : top + log2f(sum);
   }
   __syncthreads();
-  const float z = tops[tok][32];
+  const float z = tops[tok][32] * kLn2;
   float l = 0.0f;
   const int k = max(h.top, 1);
   if (live)
     for (int s = part; s < k; s += 32) {
-      const int64_t at = static_cast<int64_t>(s) * h.npad + mine;
+      const int64_t at = mine * k + s;
       const float q = h.pq[at];
-      if (h.pidx[at] >= 0 && !(q == 0.0f)) l += q * (z - h.picked[at]);
+      if (h.pidx[at] != kNone && !(q == 0.0f)) l += q * (z - h.picked[at]);
     }
   __syncthreads();
   sums[tok][part] = l;
@@ -755,15 +831,15 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
       const float z = h.lse[first + place], g = ldexpf(a, up);
       const f32x4* l = reinterpret_cast<const f32x4*>(h.logits + (static_cast<int64_t>(c / kTileM) * h.piece + place) * kTileM + c % kTileM);
       const f32x4 l0 = l[0], l1 = l[1];
-      uint32_t b[8];
+      float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float p = exp_of((e < 4 ? l0[e] : l1[e - 4]) - z), y = p * g;
-        b[e] = bf16_rne(p);
+        p[e] = exp2_of(__builtin_fmaf(e < 4 ? l0[e] : l1[e - 4], kLog2e, -z));
+        const float y = p[e] * g;
         hi[e] = static_cast<_Float16>(y);
         lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
       }
-      out = u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16};
+      out = u32x4{bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(p[4], p[5]), bf16_pair(p[6], p[7])};
     }
     *reinterpret_cast<u32x4*>(d16(place, c)) = out;
     *reinterpret_cast<h8*>(part(place, c)) = hi;
@@ -772,22 +848,15 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
   __syncthreads();   // the targets' columns again, with their share; the first of equal rows has all of it
   const int k = max(h.top, 1);
   for (int i = threadIdx.x; i < k * kDeltaTokens; i += kThreads) {
-    const int place = t0 + i % kDeltaTokens, slot = i / kDeltaTokens;
+    const int place = t0 + i / k, slot = i % k;
     if (place >= count) continue;
-    const int64_t mine = first + place;
-    auto at = [&](int s) { return static_cast<int64_t>(s) * h.npad + mine; };
-    const int c = h.pidx[at(slot)];
+    const int64_t mine = first + place, at = mine * k;
+    const int c = h.pidx[at + slot];
     const float a = h.a[mine];
-    if (c < c0 || c >= c0 + kDeltaCols || a == 0.0f) continue;
+    if (c < c0 || c >= c0 + kDeltaCols || a == 0.0f || (slot && h.pidx[at + slot - 1] == c)) continue;
     float q = 0.0f;
-    bool mine_first = true;
-    for (int s = 0; s < k; ++s) {
-      if (h.pidx[at(s)] != c) continue;
-      mine_first &= s >= slot;
-      q += h.pq[at(s)];
-    }
-    if (!mine_first) continue;
-    const float p = exp_of(h.picked[at(slot)] - h.lse[mine]) - q, y = p * ldexpf(a, up);
+    for (int s = slot; s < k && h.pidx[at + s] == c; ++s) q += h.pq[at + s];
+    const float p = exp2_of(__builtin_fmaf(h.picked[at + slot], kLog2e, -h.lse[mine])) - q, y = p * ldexpf(a, up);
     *d16(place, c) = static_cast<uint16_t>(bf16_rne(p));
     const _Float16 hi = static_cast<_Float16>(y);
     *part(place, c) = hi;
@@ -803,8 +872,9 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_kernel(Head h,
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   const HeadPiece info = h.pieces[piece];
   const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = (info.count + BN - 1) / BN, tiles = m_tiles * n_tiles;
-  const int o = xcd_item(tiles * info.splits);
-  if (o < 0) return;
+  const Items items(tiles * info.splits);
+  const int o = items.now;
+  if (o >= items.end) return;
   const int split = o / tiles;
   const TileAt at = tile_at(o - split * tiles, m_tiles, n_tiles, true);
   const int ksteps = h.vp / kStep;
@@ -813,11 +883,12 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_kernel(Head h,
   // stages behind the table's last row repeat it; d is zero there
   const int row = min(k0 * kStep, h.rows - 1);
   const int64_t from = static_cast<int64_t>(row) * h.pitch + at.m * (kTileM * 2);
-  const Operand p = {h.table + from, h.table_bytes - from, h.pitch, h.rows - row, 0};
   const int64_t d_step = static_cast<int64_t>(h.piece) * (kStep * 2), d_from = k0 * d_step + at.n * (BN * kStep * 2);
-  const Operand q = {reinterpret_cast<const char*>(h.d) + d_from, ksteps * d_step - d_from, kStep * 2, BN, d_step};
-  HeadAcc<BN> acc = {};
-  Contract<BN, false, true, false, true, false>(p, q, k1 - k0, false, 0, lds, acc);
+  HeadAcc<T> acc;
+  Contract<T, false, true, false, true, false> product(lds);
+  product.begin({h.table + from, h.table_bytes - from, h.pitch, h.rows - row, 0},
+                {reinterpret_cast<const char*>(h.d) + d_from, ksteps * d_step - d_from, kStep * 2, BN, d_step}, k1 - k0, false, 0);
+  product.run(acc, false);
   char* out = h.slabs + static_cast<int64_t>(o) * (kTileM * BN * 4) + fresh_thread() * 16;
 #pragma unroll
   for (int i = 0; i < T::NI; ++i)
@@ -864,96 +935,135 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_sum_kernel(Hea
   }
 }
 
-// dW of a piece, 256 columns by 256 rows of the table: out <- [in +] sigma * sum.
-template <bool TWO, bool OUT16>
-__global__ __launch_bounds__(HeadTile<256>::kThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
-  constexpr int BN = 256;
-  using T = HeadTile<BN>;
-  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
-  const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = h.vp / BN;
-  const int o = xcd_item(m_tiles * n_tiles);
-  if (o < 0) return;
-  const TileAt at = tile_at(o, m_tiles, n_tiles, true);
-  const HeadInfo info = *h.info;
-  const int count = h.pieces[piece].count, depth = (count + kStep - 1) / kStep * kStep;
-  if (count == 0 && in == out) return;   // nothing to add
-  constexpr int kRow = kTileM * 2, kRowD = BN * 4, kLow = TWO ? kPart * 2 : 0;
-  const int64_t x_from = (static_cast<int64_t>(at.m) * h.npad + static_cast<int64_t>(piece) * h.piece) * kRow;
-  const int64_t d_from = static_cast<int64_t>(at.n) * h.piece * kRowD + kLow;
-  const int c0 = at.n * BN;
-  const Operand p = {h.xh + x_from, static_cast<int64_t>(m_tiles) * h.npad * kRow - x_from, kRow, depth, 0};
-  const Operand q = {reinterpret_cast<const char*>(h.logits) + d_from, static_cast<int64_t>(n_tiles) * h.piece * kRowD - d_from, kRowD, depth, 0};
-  HeadAcc<BN> acc = {};
-  Contract<BN, true, true, true, false, true>(p, q, (TWO ? 2 : 1) * depth / kStep, TWO, -kLow, lds, acc);
-  // Half of the table's rows at a time go through LDS, 1 KiB each, so that whole
-  // rows are read and written: piece c of row r at place c ^ (r % 32).
-  constexpr int kPassCols = T::NJ / 2, kRows = BN / 2;
+// How a value of dW is finished: out <- [in +] sigma * 2^up * x. The factor is
+// two, either of which fp32 holds; adding 0 leaves no -0.0.
+template <bool OUT16>
+struct Finish {
+  const float* in;
+  void* out;
+  float f0, f1;
+
+  __device__ __forceinline__ float value(float x, float before) const { return __builtin_fmaf(x * f0, f1, before + 0.0f); }
+  __device__ __forceinline__ void one(int64_t at, float x) const {
+    const float y = value(x, in ? in[at] : 0.0f);
+    if constexpr (OUT16) static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(bf16_rne(y));
+    else static_cast<float*>(out)[at] = y;
+  }
+  __device__ __forceinline__ f32x4 before(int64_t at) const { return in ? *reinterpret_cast<const f32x4*>(in + at) : f32x4{}; }
+  __device__ __forceinline__ void four(int64_t at, const f32x4& x, const f32x4& b) const {
+    const f32x4 y = {value(x[0], b[0]), value(x[1], b[1]), value(x[2], b[2]), value(x[3], b[3])};
+    if constexpr (OUT16) *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+    else *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = y;
+  }
+};
+
+// A tile of dW where rows are 16-byte aligned (fp32): every lane has four
+// neighbours of a row, and four stores of a wave fill 128 bytes of 32 rows.
+template <bool OUT16>
+__device__ __forceinline__ void keep_dw(const Head& h, const TileAt& at, const Finish<OUT16>& f, const HeadAcc<DwTile>& acc) {
+  using T = DwTile;
+  const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
+#pragma unroll
+  for (int j = 0; j < T::NJ; ++j) {
+    const int v = at.n * T::kN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;
+    if (v >= h.rows) continue;
+    const int c = at.m * kTileM + wave / T::WC * T::NI * 32 + lane / 32 * 4;
+    const int64_t to = static_cast<int64_t>(v) * h.cols + c;
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i) {
+      f32x4 b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = c + i * 32 + e * 8 < h.cols ? f.before(to + i * 32 + e * 8) : f32x4{};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x16& x = acc.v[i][j];
+        if (c + i * 32 + e * 8 < h.cols) f.four(to + i * 32 + e * 8, f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]}, b[e]);
+      }
+    }
+  }
+}
+
+// The same for rows of any alignment: half of the tile's rows at a time go
+// through LDS, 1 KiB each, and a wave reads and writes whole rows. Piece c of row
+// r lies at place c ^ (r % 32). Single elements out of the registers took 405 us
+// for 32001 x 1001 and 517 tokens, this way 187.
+template <bool OUT16>
+__device__ __forceinline__ void keep_dw_odd(const Head& h, const TileAt& at, const Finish<OUT16>& f, const HeadAcc<DwTile>& acc, char* lds) {
+  using T = DwTile;
+  constexpr int kHalf = T::NJ / 2, kRows = T::kN / 2;
   static_assert(kRows * kTileM * 4 <= T::kLds, "half a tile");
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave;
-  const int up = info.ec + info.ex - 29, width = min(h.cols - at.m * kTileM, kTileM);
-  auto finish = [&](float x, float before) {
-    const float y = __builtin_ldexpf(x, up) * sigma + 0.0f;   // never -0.0
-    return in ? before + y : y;
-  };
+  const int width = min(h.cols - at.m * kTileM, kTileM);
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     if (pass) barrier();
 #pragma unroll
-    for (int jj = 0; jj < kPassCols; ++jj)
+    for (int jj = 0; jj < kHalf; ++jj)
 #pragma unroll
       for (int i = 0; i < T::NI; ++i)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const f32x16& x = acc.v[i][pass * kPassCols + jj];
-          const int r = (wave % T::WC * kPassCols + jj) * 32 + lane % 32;
+          const f32x16& x = acc.v[i][pass * kHalf + jj];
+          const int r = (wave % T::WC * kHalf + jj) * 32 + lane % 32;
           const int c = (wave / T::WC * T::NI + i) * 8 + e / 2 + lane / 32;
           *reinterpret_cast<f32x4*>(lds + r * (kTileM * 4) + (c ^ r % 32) * 16) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
         }
     wait<63, true>();
     barrier();
-    constexpr int kAhead = 8;
-    static_assert(kRows / T::kWaves % kAhead == 0, "whole batches");
-#pragma unroll 1
-    for (int r0 = wave * (kRows / T::kWaves); r0 < (wave + 1) * (kRows / T::kWaves); r0 += kAhead) {
-      const int j0 = r0 / 32, first = c0 + (j0 / kPassCols * T::NJ + pass * kPassCols + j0 % kPassCols) * 32 + r0 % 32;
-      const int64_t to = static_cast<int64_t>(first) * h.cols + at.m * kTileM;
-      if (h.cols % 4 == 0) {
-        const int c = lane * 4;
-        f32x4 before[kAhead], x[kAhead];
+    for (int r = wave * (kRows / T::kWaves); r < (wave + 1) * (kRows / T::kWaves); ++r) {
+      const int v = at.n * T::kN + (r / 32 / kHalf * T::NJ + pass * kHalf + r / 32 % kHalf) * 32 + r % 32;
+      if (v >= h.rows) continue;
+      const int64_t to = static_cast<int64_t>(v) * h.cols + at.m * kTileM;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          before[u] = f32x4{};
-          if (in && c < width && first + u < h.rows) before[u] = *reinterpret_cast<const f32x4*>(in + to + static_cast<int64_t>(u) * h.cols + c);
-          x[u] = *reinterpret_cast<const f32x4*>(lds + (r0 + u) * (kTileM * 4) + (lane ^ (r0 + u) % 32) * 16);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (c >= width || first + u >= h.rows) continue;
-          f32x4 y;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) y[t] = finish(x[u][t], before[u][t]);
-          const int64_t at_row = to + static_cast<int64_t>(u) * h.cols + c;
-          if constexpr (OUT16)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at_row) =
-                u32x2{bf16_rne(y[0]) | bf16_rne(y[1]) << 16, bf16_rne(y[2]) | bf16_rne(y[3]) << 16};
-          else
-            *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at_row) = y;
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int c = t * kWave + lane;
-            if (c >= width || first + u >= h.rows) continue;
-            const float x = *reinterpret_cast<const float*>(lds + (r0 + u) * (kTileM * 4) + (c / 4 ^ (r0 + u) % 32) * 16 + c % 4 * 4);
-            const int64_t at_row = to + static_cast<int64_t>(u) * h.cols + c;
-            const float y = finish(x, in ? in[at_row] : 0.0f);
-            if constexpr (OUT16) static_cast<uint16_t*>(out)[at_row] = static_cast<uint16_t>(bf16_rne(y));
-            else static_cast<float*>(out)[at_row] = y;
-          }
+      for (int t = 0; t < 4; ++t) {
+        const int c = t * kWave + lane;
+        if (c < width) f.one(to + c, *reinterpret_cast<const float*>(lds + r * (kTileM * 4) + (c / 4 ^ r % 32) * 16 + c % 4 * 4));
       }
     }
+  }
+  barrier();
+}
+
+// Tiles of dW of a piece, 256 columns by 256 rows of the table.
+template <bool TWO, bool OUT16>
+__global__ __launch_bounds__(DwTile::kThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
+  using T = DwTile;
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  const HeadInfo info = *h.info;
+  const int count = h.pieces[piece].count, depth = (count + kStep - 1) / kStep * kStep;
+  if (count == 0 && in == out) return;   // nothing to add
+  const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = h.vp / T::kN;
+  Items items(m_tiles * n_tiles);
+  if (items.now >= items.end) return;
+  const int up = info.ec + info.ex - 29;
+  const Finish<OUT16> finish = {in, out, __builtin_ldexpf(1.0f, up / 2), __builtin_ldexpf(sigma, up - up / 2)};
+  constexpr int kRow = kTileM * 2, kRowD = T::kN * 4, kLow = TWO ? kPart * 2 : 0;
+  Contract<T, true, true, true, false, true> product(lds);
+  auto begin = [&](const TileAt& at) {
+    const int64_t x_from = (static_cast<int64_t>(at.m) * h.npad + static_cast<int64_t>(piece) * h.piece) * kRow;
+    const int64_t d_from = static_cast<int64_t>(at.n) * h.piece * kRowD + kLow;
+    product.begin({h.xh + x_from, static_cast<int64_t>(m_tiles) * h.npad * kRow - x_from, kRow, depth, 0},
+                  {reinterpret_cast<const char*>(h.logits) + d_from, static_cast<int64_t>(n_tiles) * h.piece * kRowD - d_from, kRowD, depth, 0},
+                  (TWO ? 2 : 1) * depth / kStep, TWO, -kLow);
+  };
+  const bool odd = h.cols % 4 != 0;
+  TileAt at = tile_at(items.now, m_tiles, n_tiles, true);
+  begin(at);
+  for (bool ahead = false;; ahead = true) {
+    HeadAcc<T> acc;
+    product.run(acc, ahead);
+    const TileAt done = at;
+    items.now += items.stride;
+    const bool more = items.now < items.end;
+    if (more) at = tile_at(items.now, m_tiles, n_tiles, true);
+    if (odd) {
+      keep_dw_odd(h, done, finish, acc, lds);
+      if (more) begin(at);
+    } else {
+      if (more) begin(at);
+      keep_dw(h, done, finish, acc);
+    }
+    if (!more) return;
   }
 }
 
@@ -963,6 +1073,7 @@ constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxRows = int64_t(1) <
 constexpr int64_t kHeadMaxElems = int64_t(1) << 33;
 constexpr int64_t kPieceTokens = 4096;   // tokens of a piece, unless the call says another number
 constexpr int64_t kPieceMax = 65536;
+constexpr int64_t kCus = 256;   // workgroups of a product: one a CU, each with tile after tile
 
 int64_t up_to(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
@@ -1067,7 +1178,7 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     const int piece = static_cast<int>(i);
     const int64_t tokens = std::min(s.piece, s.n - i * s.piece);
     const int64_t n_tiles = (tokens + BN - 1) / BN, m_tiles = s.vp / kTileM;
-    const dim3 tiles(static_cast<unsigned>(up_to(m_tiles * n_tiles, 8))), threads(HeadTile<BN>::kThreads);
+    const dim3 tiles(static_cast<unsigned>(std::min<int64_t>(up_to(m_tiles * n_tiles, 8), kCus))), threads(HeadTile<BN>::kThreads);
     if (grad) hipLaunchKernelGGL((head_logits_kernel<BN, true>), tiles, threads, 0, q, h, piece, c);
     else hipLaunchKernelGGL((head_logits_kernel<BN, false>), tiles, threads, 0, q, h, piece, c);
     hipLaunchKernelGGL(head_loss_kernel, dim3(static_cast<unsigned>((tokens + kLossTokens - 1) / kLossTokens)), dim3(kThreads), 0, q, h,
@@ -1082,11 +1193,11 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     hipLaunchKernelGGL(head_dx_sum_kernel<BN>, dim3(static_cast<unsigned>(dx_m * n_tiles * HeadTile<BN>::NI * HeadTile<BN>::NJ * 4)),
                        threads, 0, q, h, piece, static_cast<uint16_t*>(a.dx));
     // dW: into the packed buffer, or with more than one piece into fp32 sums that the last piece rounds
-    const dim3 dw(static_cast<unsigned>(up_to(dx_m * (s.vp / 256), 8)));
+    const dim3 dw(static_cast<unsigned>(std::min<int64_t>(up_to(dx_m * (s.vp / DwTile::kN), 8), kCus)));
     const int64_t start = a.tensor;
     float* sums = reinterpret_cast<float*>(static_cast<char*>(a.work) + s.acc);
     const float* in = i ? (s.sums ? sums : static_cast<const float*>(a.packed) + start) : a.prev ? a.prev + start : nullptr;
-    const dim3 wide(HeadTile<256>::kThreads);
+    const dim3 wide(DwTile::kThreads);
     if (two)
       hipLaunchKernelGGL((head_dw_kernel<true, false>), dw, wide, 0, q, h, piece, sigma, in, static_cast<void*>(static_cast<float*>(a.packed) + start));
     else if (s.sums && i + 1 < s.n_pieces)
