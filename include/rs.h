@@ -472,7 +472,7 @@ int rs_layer_norm_workspace(const rs_plan* plan, int64_t weight, int64_t n_rows,
  * device, n_tokens x cols bf16, row-major. targets: device, n_tokens signed
  * integers of id_bytes (4 or 8) bytes, aligned to their size. scale: finite.
  * loss: device, n_tokens fp32. piece: tokens worked on at a time, a multiple of
- * 256 up to 65536, or 0 for up to 4096; it bounds the workspace, and results
+ * 256 up to 65536, or 0 for up to 8192; it bounds the workspace, and results
  * may differ in the last bits with it. work: device memory of rs_head_workspace
  * bytes, contents not kept between calls; calls that may overlap need a
  * workspace each. All but targets 16-byte aligned; outputs and workspace

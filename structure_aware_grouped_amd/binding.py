@@ -557,7 +557,7 @@ def rs_head_workspace(plan: Plan, tensor: int, n_tokens: int, top: int = 0, pack
     """Workspace (uint8, on the plan's device) for the head's calls with n_tokens tokens: for the
     losses, or with packed (the packed buffer, or its dtype) for the gradients too. top: logits of
     the teacher per token, 0 for labels. piece: tokens whose logits are held at a time (a multiple
-    of 256; 0: up to 4096), the same as in the call. Calls that may overlap need a workspace each."""
+    of 256; 0: up to 8192), the same as in the call. Calls that may overlap need a workspace each."""
     dt = packed.dtype if isinstance(packed, torch.Tensor) else packed
     if dt not in (None,) + _FLOATS:
         raise ValueError("packed: fp32 or bf16")

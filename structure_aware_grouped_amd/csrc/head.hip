@@ -44,13 +44,6 @@ constexpr int kStep = 64;            // of the contraction, per stage; what it i
 constexpr int kPart = 64;            // columns of d whose fp16 parts lie beside each other
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
-// Two values rounded to nearest-even bf16 by one instruction.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, b2));
-}
-
 // ------------------------------------------------------------------ products
 
 // C[m, n] = sum_k P[m, k] Q[n, k] on one 256 x BN tile, 32 x 32 accumulators. Either operand may lie with k contiguous (plain) or with its
@@ -1071,7 +1064,7 @@ __global__ __launch_bounds__(DwTile::kThreads) void head_dw_kernel(Head h, int p
 
 constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxRows = int64_t(1) << 21, kHeadMaxCols = int64_t(1) << 16;
 constexpr int64_t kHeadMaxElems = int64_t(1) << 33;
-constexpr int64_t kPieceTokens = 4096;   // tokens of a piece, unless the call says another number
+constexpr int64_t kPieceTokens = 8192;   // tokens of a piece, unless the call says another number
 constexpr int64_t kPieceMax = 65536;
 constexpr int64_t kCus = 256;   // workgroups of a product: one a CU, each with tile after tile
 

@@ -20,6 +20,7 @@
 // every G-th row and adds up its rows' share of dw and db in registers (fp32);
 // a second launch adds the G shares in their order, without atomics.
 #include "host_common.h"
+#include "mfma.h"
 
 namespace rs {
 namespace {
@@ -27,7 +28,13 @@ namespace {
 // 8 * VPT values of a row per thread, as loaded. VEC: vectors of 8 neighbours
 // (every row 16-byte aligned), vector k of thread t is number k * NT + t;
 // else value 8 * k + e of thread t is column (8 * k + e) * NT + t.
-template <bool B16, bool VEC, int VPT>
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) {
+  if constexpr (STREAM) return ldg(p);
+  else return *p;
+}
+
+template <bool B16, bool VEC, int VPT, bool STREAM = false>
 struct Row {
   u32x4 v[VPT][B16 && VEC ? 1 : 2];
 
@@ -38,11 +45,11 @@ struct Row {
         const int c = (k * nt + static_cast<int>(threadIdx.x)) * 8;
         if (c < cols) {
           if constexpr (B16) {
-            v[k][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at + c);
+            v[k][0] = load16<STREAM>(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at + c));
           } else {
             const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + at + c);
-            v[k][0] = q[0];
-            v[k][1] = q[1];
+            v[k][0] = load16<STREAM>(q);
+            v[k][1] = load16<STREAM>(q + 1);
           }
         } else {
           v[k][0] = u32x4{};
@@ -56,6 +63,13 @@ struct Row {
         }
       }
     }
+  }
+  // Keeps the compiler from keeping the widened values across a loop.
+  __device__ __forceinline__ void hide() {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+      for (u32x4& x : v[k]) asm volatile("" : "+v"(x));
   }
   __device__ __forceinline__ void widen(int k, float (&x)[8]) const {
     if constexpr (B16 && VEC) {
@@ -73,21 +87,16 @@ __device__ __forceinline__ bool in_row(int k, int e, int cols, int nt) {
   return VEC ? (k * nt + static_cast<int>(threadIdx.x)) * 8 < cols : (k * 8 + e) * nt + static_cast<int>(threadIdx.x) < cols;
 }
 
-template <bool B16, bool VEC>
+template <bool B16, bool VEC, int POLICY = 0>
 __device__ __forceinline__ void store8(void* p, int64_t at, int k, const float (&x)[8], int cols, int nt) {
   if constexpr (VEC) {
     const int c = (k * nt + static_cast<int>(threadIdx.x)) * 8;
     if (c >= cols) return;
     if constexpr (B16) {
-      uint32_t b[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = bf16_rne(x[e]);
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at + c) =
-          u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16};
+      sts_at<POLICY>(static_cast<uint16_t*>(p) + at, c * 2, u32x4{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])});
     } else {
-      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at + c);
-      o[0] = f32x4{x[0], x[1], x[2], x[3]};
-      o[1] = f32x4{x[4], x[5], x[6], x[7]};
+      sts_at<POLICY>(static_cast<float*>(p) + at, c * 4, f32x4{x[0], x[1], x[2], x[3]});
+      sts_at<POLICY>(static_cast<float*>(p) + at, c * 4 + 16, f32x4{x[4], x[5], x[6], x[7]});
     }
   } else {
 #pragma unroll
@@ -103,26 +112,24 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int k, const float (
 // Sums over the workgroup, N of them at once, the same bits in every thread.
 // `red` alternates between two halves from call to call: whoever writes one
 // half has passed the barrier behind the reads of it.
-constexpr int kMaxWaves = 16;
+constexpr int kNormThreads = 512, kGradThreads = 1024, kMaxWaves = 16;
+static_assert(kGradThreads <= kMaxWaves * kWave, "a row of lanes holds one value of each wave");
 template <int N>
 __device__ __forceinline__ void group_sum(float (&s)[N], float* red, int& half, int nt) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) s[i] += __shfl_xor(s[i], o, kWave);
+  for (int i = 0; i < N; ++i) s[i] = wave_sum(s[i]);
   if (nt == kWave) return;
   float* mine = red + half * (2 * kMaxWaves);
   half ^= 1;
-  const int tid = static_cast<int>(threadIdx.x);
-  if (tid % kWave == 0)
+  const int lane = static_cast<int>(threadIdx.x) % kWave, wave = static_cast<int>(threadIdx.x) / kWave;
+  if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) mine[i * kMaxWaves + tid / kWave] = s[i];
-  __syncthreads();
+    for (int i = 0; i < N; ++i) mine[i * kMaxWaves + wave] = s[i];
+  wait<63, true>();
+  barrier();
+  const int slot = lane % kMaxWaves;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    s[i] = 0.0f;
-    for (int w = 0; w < nt / kWave; ++w) s[i] += mine[i * kMaxWaves + w];
-  }
+  for (int i = 0; i < N; ++i) s[i] = from_lane(row_sum_last(slot < nt / kWave ? mine[i * kMaxWaves + slot] : 0.0f), kMaxWaves - 1);
 }
 
 // One of the parameters, the same columns as a Row's; zeros where there is none.
@@ -146,8 +153,8 @@ __device__ __forceinline__ void load_param(const void* p, bool b16, float (&w)[V
 }
 
 // Deviations from the mean and the reciprocal deviation of the row.
-template <bool B16, bool VEC, int VPT>
-__device__ __forceinline__ float standardize(const Row<B16, VEC, VPT>& row, float (&h)[VPT][8], int cols, float eps, bool center,
+template <bool B16, bool VEC, int VPT, bool STREAM>
+__device__ __forceinline__ float standardize(const Row<B16, VEC, VPT, STREAM>& row, float (&h)[VPT][8], int cols, float eps, bool center,
                                              float* red, int& half, int nt) {
   float s[1] = {0.0f};
 #pragma unroll
@@ -189,16 +196,16 @@ struct NormCall {
 };
 
 template <bool IN16, bool OUT16, bool VEC, int VPT>
-__global__ __launch_bounds__(1024) void norm_kernel(NormCall c, const void* x, void* y) {
-  __shared__ float red[4 * kMaxWaves];
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(NormCall c, const void* x, void* y) {
+  __shared__ __attribute__((aligned(16))) float red[4 * kMaxWaves];
   const int nt = static_cast<int>(blockDim.x);
   int half = 0;
   float w[VPT][8], b[VPT][8];
   load_param<VEC, VPT>(c.weight, c.param16, w, c.cols, nt);
   load_param<VEC, VPT>(c.bias, c.param16, b, c.cols, nt);
+  Row<IN16, VEC, VPT> row;
+  row.load(x, blockIdx.x * static_cast<int64_t>(c.cols), c.cols, nt);
   for (int64_t r = blockIdx.x; r < c.n; r += gridDim.x) {
-    Row<IN16, VEC, VPT> row;
-    row.load(x, r * c.cols, c.cols, nt);
     float h[VPT][8];
     standardize(row, h, c.cols, c.eps, c.center, red, half, nt);
 #pragma unroll
@@ -210,37 +217,41 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormCall c, const void* x, v
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[k][e] *= w[k][e];
       }
-      store8<OUT16, VEC>(y, r * c.cols, k, h[k], c.cols, nt);
+      store8<OUT16, VEC, kStoreNtSc1>(y, r * c.cols, k, h[k], c.cols, nt);
     }
+    if (r + gridDim.x < c.n) row.load(x, (r + gridDim.x) * c.cols, c.cols, nt);
   }
 }
 
 // dx of every G-th row, and the workgroup's share of dw and db.
-template <bool IN16, bool DY16, bool VEC, int VPT>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(NormCall c, const void* x, const void* dy, void* dx, float* part) {
-  __shared__ float red[4 * kMaxWaves];
+template <bool IN16, bool DY16, bool P16, bool VEC, int VPT>
+__global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(NormCall c, const void* x, const void* dy, void* dx, float* part) {
+  __shared__ __attribute__((aligned(16))) float red[4 * kMaxWaves];
   const int nt = static_cast<int>(blockDim.x);
   const float width = static_cast<float>(c.cols);
   int half = 0;
-  float w[VPT][8], dw[VPT][8] = {}, db[VPT][8] = {};
-  load_param<VEC, VPT>(c.weight, c.param16, w, c.cols, nt);
+  float dw[VPT][8] = {}, db[VPT][8] = {};
+  Row<P16, VEC, VPT> weight;
+  weight.load(c.weight, 0, c.cols, nt);
+  Row<IN16, VEC, VPT, true> row;
+  Row<DY16, VEC, VPT, true> up;
+  row.load(x, blockIdx.x * static_cast<int64_t>(c.cols), c.cols, nt);
+  up.load(dy, blockIdx.x * static_cast<int64_t>(c.cols), c.cols, nt);
   for (int64_t r = blockIdx.x; r < c.n; r += gridDim.x) {
-    Row<IN16, VEC, VPT> row;
-    Row<DY16, VEC, VPT> up;
-    row.load(x, r * c.cols, c.cols, nt);
-    up.load(dy, r * c.cols, c.cols, nt);
+    weight.hide();
     float h[VPT][8];
     const float inv = standardize(row, h, c.cols, c.eps, c.center, red, half, nt);
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      float d[8];
+      float d[8], w[8];
       up.widen(k, d);
+      weight.widen(k, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dw[k][e] = __builtin_fmaf(d[e], h[k][e], dw[k][e]);
         db[k][e] += d[e];
-        const float g = d[e] * w[k][e];
+        const float g = d[e] * w[e];
         s[0] = __builtin_fmaf(g, h[k][e], s[0]);
         s[1] += g;
       }
@@ -249,11 +260,16 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormCall c, const void*
     const float along = s[0] / width, mean = c.center ? s[1] / width : 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      float d[8];
+      float d[8], w[8];
       up.widen(k, d);
+      weight.widen(k, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = (d[e] * w[k][e] - mean - h[k][e] * along) * inv;
+      for (int e = 0; e < 8; ++e) d[e] = (d[e] * w[e] - mean - h[k][e] * along) * inv;
       store8<IN16, VEC>(dx, r * c.cols, k, d, c.cols, nt);
+    }
+    if (r + gridDim.x < c.n) {
+      row.load(x, (r + gridDim.x) * c.cols, c.cols, nt);
+      up.load(dy, (r + gridDim.x) * c.cols, c.cols, nt);
     }
   }
   float* mine = part + static_cast<int64_t>(blockIdx.x) * 2 * c.cols;
@@ -307,16 +323,26 @@ struct NormShape {
   unsigned grid;
 };
 
-// Vectors of 8 per thread and threads per row.
-NormShape norm_shape(int64_t n, int64_t cols, int64_t per_cu) {
+// The launch of a pass: threads per row, vectors of 8 per thread, and workgroups,
+// per_cu threads' worth of them on each of the 256 CUs. 16384 rows of 8192 bf16
+// columns: forwards 512 threads with two vectors each and 8192 threads a CU take
+// 82 us (4096: 84, 2048: 96; 256 threads with four 84; 1024 with one 110);
+// backwards 512 with two and 1024 a CU 161 (1024 with one 216, 256 with four 210;
+// 1536 a CU 218), where more workgroups mean more shares to add up.
+NormShape norm_shape(int64_t n, int64_t cols, int vmost, int most, int64_t per_cu) {
   NormShape s{kWave, 1, 0};
-  while (s.threads < 1024 && s.threads * 8 < cols) s.threads *= 2;
-  if (s.threads * 8 < cols) s.vpt = 2;
+  while (s.vpt < vmost && s.threads * 8 * s.vpt < cols) s.vpt *= 2;
+  while (s.threads < 512 && s.threads * 8 * s.vpt < cols) s.threads *= 2;
+  while (s.vpt < 2 && s.threads * 8 * s.vpt < cols) s.vpt *= 2;
+  while (s.threads < most && s.threads * 8 * s.vpt < cols) s.threads *= 2;
+  while (s.threads * 8 * s.vpt < cols) s.vpt *= 2;
   s.grid = static_cast<unsigned>(std::min<int64_t>(n, 256 * std::max<int64_t>(1, per_cu / s.threads)));
   return s;
 }
+NormShape forward_shape(int64_t n, int64_t cols) { return norm_shape(n, cols, 2, kNormThreads, 8192); }
+NormShape grad_shape(int64_t n, int64_t cols) { return norm_shape(n, cols, 1, kGradThreads, 1024); }
 
-int64_t grad_work(int64_t n, int64_t cols) { return int64_t(norm_shape(n, cols, 1024).grid) * 2 * cols * 4; }
+int64_t grad_work(int64_t n, int64_t cols) { return int64_t(grad_shape(n, cols).grid) * 2 * cols * 4; }
 
 int check_norm(const rs_plan* p, int64_t weight, int64_t bias, int64_t n, const char* who) {
   if (weight < 0 || weight >= p->n || bias < -1 || bias >= p->n || bias == weight)
@@ -335,7 +361,8 @@ template <typename F>
 void by_types(bool a16, bool b16, bool vec, int vpt, F f) {
   auto width = [&](auto a, auto b, auto v) {
     if (vpt == 1) f(a, b, v, std::integral_constant<int, 1>{});
-    else f(a, b, v, std::integral_constant<int, 2>{});
+    else if (vpt == 2) f(a, b, v, std::integral_constant<int, 2>{});
+    else f(a, b, v, std::integral_constant<int, 4>{});
   };
   auto aligned = [&](auto a, auto b) {
     if (vec) width(a, b, std::true_type{});
@@ -376,7 +403,7 @@ extern "C" int rs_layer_norm(rs_plan* p, int64_t weight, int64_t bias, const voi
     return fail(RS_EALIGN, std::string(who) + ": buffers must be 16-byte aligned");
   if (n_rows == 0) return RS_OK;
   const NormCall c = norm_call(p, weight, bias, gathered, dt, n_rows, eps, center);
-  const NormShape s = norm_shape(n_rows, c.cols, 2048);
+  const NormShape s = forward_shape(n_rows, c.cols);
   by_types(x_dt == RS_BF16, y_dt == RS_BF16, c.cols % 8 == 0, s.vpt, [&](auto in, auto out, auto vec, auto vpt) {
     hipLaunchKernelGGL((norm_kernel<in.value, out.value, vec.value, vpt.value>), dim3(s.grid),
                        dim3(static_cast<unsigned>(s.threads)), 0, static_cast<hipStream_t>(stream), c, x, y);
@@ -420,12 +447,16 @@ extern "C" int rs_layer_norm_grad(rs_plan* p, int64_t weight, int64_t bias, cons
   if (work_bytes < need)
     return fail(RS_EINVAL, std::string(who) + ": workspace of " + std::to_string(work_bytes) + " bytes, " + std::to_string(need) +
                                " needed");
-  const NormShape s = norm_shape(n_rows, c.cols, 1024);
+  const NormShape s = grad_shape(n_rows, c.cols);
   hipStream_t q = static_cast<hipStream_t>(stream);
   if (n_rows)
     by_types(x_dt == RS_BF16, dy_dt == RS_BF16, c.cols % 8 == 0, s.vpt, [&](auto in, auto up, auto vec, auto vpt) {
-      hipLaunchKernelGGL((norm_grad_kernel<in.value, up.value, vec.value, vpt.value>), dim3(s.grid),
-                         dim3(static_cast<unsigned>(s.threads)), 0, q, c, x, dy, dx, static_cast<float*>(work));
+      constexpr int kVpt = vpt.value > 2 ? 2 : vpt.value;   // norm_shape gives no more
+      const dim3 grid(s.grid), threads(static_cast<unsigned>(s.threads));
+      if (c.param16)
+        hipLaunchKernelGGL((norm_grad_kernel<in.value, up.value, true, vec.value, kVpt>), grid, threads, 0, q, c, x, dy, dx, static_cast<float*>(work));
+      else
+        hipLaunchKernelGGL((norm_grad_kernel<in.value, up.value, false, vec.value, kVpt>), grid, threads, 0, q, c, x, dy, dx, static_cast<float*>(work));
     });
   auto out = [&](int64_t t) -> NormOut {
     if (t < 0) return {nullptr, nullptr};
