@@ -533,9 +533,9 @@ int rs_distill_grad(rs_plan* plan, int64_t tensor, const void* gathered, const v
 /* Bytes of workspace for the four calls on this tensor: n_tokens, piece and
  * top (0 for labels) as in the call; grad 1 for the gradients (a workspace that
  * also serves the losses), packed_dt the packed buffer's type. About
- * 4 n cols + 8 n top for the tokens; rows * cols * 2 more where cols is no
- * multiple of 64; for gradients piece * rows * 6, at most 256 MiB for parts of
- * dx, and rows * cols * 4 more for a bf16 packed buffer and more than one piece.
+ * 4 n cols + 16 n top for the tokens; rows * cols * 2 more where cols is no
+ * multiple of 64; piece * rows * 4 where rows < 256 top, piece * rows * 6 for
+ * gradients, for these piece * cols * 4 or at most 256 MiB for parts of dx, and rows * cols * 4 more for a bf16 packed buffer and more than one piece.
  * Errors: RS_EINVAL, RS_EDTYPE, RS_ERANGE. */
 int rs_head_workspace(const rs_plan* plan, int64_t tensor, int64_t n_tokens, int64_t top, int32_t grad, int32_t packed_dt,
                       int64_t piece, int64_t* bytes);

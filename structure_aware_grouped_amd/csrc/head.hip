@@ -375,7 +375,7 @@ struct Head {
   float *pq, *picked;     // q and the logit there
   char *xb, *xh;          // by place: x in bf16, 64 columns of all tokens beside each other, and scaled in fp16, 256 columns
   float2* stat;           // of one piece: per 32 * NI rows of the table, `piece` maxima and sums
-  float* logits;          // of one piece: 256 columns of all its tokens beside each other; then the fp16 parts of d
+  float* logits;          // of one piece: see logit_at; then the fp16 parts of d, 256 columns of all its tokens beside each other
   uint16_t* d;            // of one piece: bf16, 64 columns of all its tokens beside each other
   char* slabs;
 };
@@ -607,7 +607,8 @@ __global__ __launch_bounds__(kThreads) void head_gather_kernel(Head h, const uin
   }
 }
 
-// The table with its rows padded, where their width is no multiple of kStep.
+// The table with its rows padded, where their width is no multiple of kStep. Bound
+// by memory: 76552 x 4184 in 235 us, 5.5 TB/s (two bytes a lane: 400).
 __global__ __launch_bounds__(kThreads) void head_widen_kernel(const uint16_t* table, int rows, int cols, int hp, uint16_t* out) {
   const int per = hp / 8;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -615,10 +616,16 @@ __global__ __launch_bounds__(kThreads) void head_widen_kernel(const uint16_t* ta
   const int64_t r = u / per;
   const int c = static_cast<int>(u - r * per) * 8;
   const uint16_t* from = table + r * cols + c;
-  uint32_t v[8];
+  u32x4 v = {};
+  if (c + 8 <= cols) {
+    __builtin_memcpy(&v, from, 16);   // one load, aligned or not
+  } else {
+    uint32_t e16[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? from[e] : 0u;
-  *reinterpret_cast<u32x4*>(out + r * hp + c) = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+    for (int e = 0; e < 8; ++e) e16[e] = c + e < cols ? from[e] : 0u;
+    v = u32x4{e16[0] | e16[1] << 16, e16[2] | e16[3] << 16, e16[4] | e16[5] << 16, e16[6] | e16[7] << 16};
+  }
+  *reinterpret_cast<u32x4*>(out + r * hp + c) = v;
 }
 
 // ------------------------------------------------------------------ logits
@@ -627,17 +634,26 @@ __global__ __launch_bounds__(kThreads) void head_widen_kernel(const uint16_t* ta
 // z in powers of two, so that the product is not rounded by itself.
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Where the logit of row c (rows c to c | 3) and a place of the piece lies:
+// blocks of 256 rows by 32 tokens, in them the order of the accumulators, so that
+// a wave stores 1 KB at once (4096 tokens by 131072 rows of 4096: 3.70 ms; token
+// after token, 32 bytes at once, 3.85).
+__device__ __forceinline__ float* logit_at(const Head& h, int c, int place) {
+  const int block = place / 32 * 32, row = c % kTileM;
+  return h.logits + (static_cast<int64_t>(c / kTileM) * h.piece + block) * kTileM + row / 8 * 256 + (row / 4 % 2 * 32 + place - block) * 4 + row % 4;
+}
+
 // What is kept of one tile of the logits: for each token the largest and the
-// sum of exponentials over the wave's rows, the logits at its targets, and
-// (STORE) the logits themselves, -inf behind the table's end. A lane holds one
-// token's logits, so the sums are its own and the other half wave's.
+// sum of exponentials over the wave's rows, and the logits themselves, -inf
+// behind the table's end (STORE), or those at its targets, which are sorted. A lane
+// holds one token's logits, so the sums are its own and the other half wave's.
 template <class T, bool STORE>
 __device__ __forceinline__ void keep_logits(const Head& h, int piece, int count, const TileAt& at, float factor, HeadAcc<T>& acc) {
   const int tid = fresh_thread(), lane = tid % kWave, wave = tid / kWave, half = lane / 32;
   const int row = wave / T::WC * T::NI * 32, first = at.m * kTileM + row;   // the wave's first row, in the tile and of the table
-  const int k = max(h.top, 1);
   const bool inside = first + T::NI * 32 <= h.rows;
   // each token's first target that is no row ahead of the wave's
+  const int k = STORE ? 0 : max(h.top, 1);
   int slot[T::NJ], to[T::NJ];
 #pragma unroll
   for (int j = 0; j < T::NJ; ++j) {
@@ -662,7 +678,6 @@ __device__ __forceinline__ void keep_logits(const Head& h, int piece, int count,
   for (int j = 0; j < T::NJ; ++j) {
     const int place = at.n * T::kN + (wave % T::WC * T::NJ + j) * 32 + lane % 32;   // in the piece
     const bool live = place < count;
-    const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
 #pragma unroll
     for (int i = 0; i < T::NI; ++i)
 #pragma unroll
@@ -688,29 +703,33 @@ __device__ __forceinline__ void keep_logits(const Head& h, int piece, int count,
       for (int e = 0; e < 16; ++e) sum += exp2_of(__builtin_fmaf(acc.v[i][j][e], kLog2e, -base));
     sum += __shfl_xor(sum, 32, kWave);
     if (live && half == 0) h.stat[static_cast<int64_t>(first / (32 * T::NI)) * h.piece + place] = float2{top, sum};
-    if (live)
-      for (int t = slot[j]; t < k; ++t) {
-        const int hit = h.pidx[mine * k + t] - first;
-        if (hit >= T::NI * 32) break;
-        if (hit / 4 % 2 != half) continue;
-        float l = 0.0f;
+    if constexpr (!STORE) {
+      const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
+      if (live)
+        for (int t = slot[j]; t < k; ++t) {
+          const int hit = h.pidx[mine * k + t] - first;
+          if (hit >= T::NI * 32) break;
+          if (hit / 4 % 2 != half) continue;
+          float l = 0.0f;
 #pragma unroll
-        for (int i = 0; i < T::NI; ++i)
+          for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) l = hit == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
-        h.picked[mine * k + t] = l;
-      }
+            for (int e = 0; e < 16; ++e) l = hit == i * 32 + e / 4 * 8 + half * 4 + e % 4 ? acc.v[i][j][e] : l;
+          h.picked[mine * k + t] = l;
+        }
+    }
     if constexpr (STORE) {
       if (live) {
-        float* out = h.logits + (static_cast<int64_t>(at.m) * h.piece + place) * kTileM + row + half * 4;
+        float* out = logit_at(h, first + half * 4, place);
 #pragma unroll
         for (int i = 0; i < T::NI; ++i)
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<f32x4*>(out + i * 32 + e * 2) =
+            *reinterpret_cast<f32x4*>(out + i * 1024 + e * 64) =
                 f32x4{acc.v[i][j][e], acc.v[i][j][e + 1], acc.v[i][j][e + 2], acc.v[i][j][e + 3]};
       }
     }
+    if constexpr (STORE) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -744,12 +763,16 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Hea
   }
 }
 
-// Log-sum-exp and loss of kLossTokens tokens, 32 threads each.
-constexpr int kLossTokens = kThreads / 32;
+// Log-sum-exp and loss of TOKENS tokens, and (STORED) the logits at their targets
+// out of the stored ones. A token's numbers lie a piece apart, so eight
+// neighbours share what a load brings; few tokens take a workgroup each (48 with
+// 2048 numbers: 32 us with eight, 7 with one).
+template <int TOKENS, bool STORED>
 __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, int stats, float factor, float* loss) {
-  __shared__ float tops[kLossTokens][33], sums[kLossTokens][33];
-  const int tok = threadIdx.x % kLossTokens, part = threadIdx.x / kLossTokens;
-  const int place = blockIdx.x * kLossTokens + tok, count = h.pieces[piece].count;
+  constexpr int kParts = kThreads / TOKENS;
+  __shared__ float tops[TOKENS][kParts + 1], sums[TOKENS][kParts + 1];
+  const int tok = threadIdx.x % TOKENS, part = threadIdx.x / TOKENS;
+  const int place = blockIdx.x * TOKENS + tok, count = h.pieces[piece].count;
   const bool live = place < count;
   const int64_t mine = static_cast<int64_t>(piece) * h.piece + place;
   float top = -INFINITY, sum = 0.0f;
@@ -761,49 +784,56 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
     top = both;
   };
   if (live)
-    for (int i = part; i < stats; i += 32) {
+#pragma unroll 4
+    for (int i = part; i < stats; i += kParts) {
       const float2 s = h.stat[static_cast<int64_t>(i) * h.piece + place];
       add(s.x, s.y);
     }
-  tops[tok][part] = top;
-  sums[tok][part] = broken ? NAN : sum;
-  __syncthreads();
-  if (part == 0 && live) {
-    top = -INFINITY;
-    sum = 0.0f;
-    for (int i = 0; i < 32; ++i) add(tops[tok][i], sums[tok][i]);
-    tops[tok][32] = h.lse[mine] = broken ? NAN : top + log2f(sum);
+  for (int width = kParts; width > 1; width /= 2) {   // the upper half joins the lower one
+    __syncthreads();
+    if (part >= width / 2 && part < width) {
+      tops[tok][part] = top;
+      sums[tok][part] = broken ? NAN : sum;
+    }
+    __syncthreads();
+    if (part < width / 2) add(tops[tok][part + width / 2], sums[tok][part + width / 2]);
   }
+  if (part == 0) tops[tok][kParts] = broken ? NAN : top + log2f(sum);
   __syncthreads();
-  const float z = tops[tok][32] * kLn2;
+  const float z = tops[tok][kParts] * kLn2;
   float l = 0.0f;
   const int k = max(h.top, 1);
   if (live)
-    for (int s = part; s < k; s += 32) {
+    for (int s = part; s < k; s += kParts) {
       const int64_t at = mine * k + s;
+      const int c = h.pidx[at];
+      if (c == kNone) continue;
+      float y;
+      if constexpr (STORED) h.picked[at] = y = *logit_at(h, c, place);
+      else y = h.picked[at];
       const float q = h.pq[at];
-      if (h.pidx[at] != kNone && !(q == 0.0f)) l += q * (z - h.picked[at]);
+      if (!(q == 0.0f)) l += q * (z - y);
     }
-  __syncthreads();
   sums[tok][part] = l;
   __syncthreads();
   if (part || !live) return;
   l = 0.0f;
-  for (int i = 0; i < min(k, 32); ++i) l += sums[tok][i];
+  for (int i = 0; i < min(k, kParts); ++i) l += sums[tok][i];
+  h.lse[mine] = tops[tok][kParts];
   loss[h.kept[mine]] = factor * (h.pent[mine] + l);
 }
 
 // ------------------------------------------------------------------ gradients
 
-// d = p - q of kDeltaTokens tokens and kDeltaCols columns: bf16 for dx, and
-// times the token's share of the gradient, scaled, in fp16 parts for dW, where
-// the logits lay: 64 logits give way to 64 values of each part, and those that a
-// wave overwrites are its own, read before.
-constexpr int kDeltaTokens = 16, kDeltaCols = 512;
+// d = p - q of a block of 32 tokens and 256 columns: bf16 for dx, and times the
+// token's share of the gradient, scaled, in fp16 parts for dW, where the logits
+// lay, in rows of 256 columns a token: 64 logits give way to 64 values of each
+// part. The whole block is read ahead of the first write.
+constexpr int kDeltaTokens = 32;
 template <bool TWO>
 __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece) {
   const int count = h.pieces[piece].count, places = (count + kStep - 1) / kStep * kStep;
-  const int t0 = blockIdx.x * kDeltaTokens, c0 = blockIdx.y * kDeltaCols;
+  const int t0 = blockIdx.x * kDeltaTokens, c0 = blockIdx.y * kTileM;
   if (t0 >= places) return;
   const int64_t first = static_cast<int64_t>(piece) * h.piece;
   const int up = 15 - h.info->ec;
@@ -811,23 +841,30 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
     return reinterpret_cast<_Float16*>(h.logits + (static_cast<int64_t>(c / kTileM) * h.piece + place) * kTileM + c % kTileM / kPart * kPart) + c % kPart;
   };
   auto d16 = [&](int place, int c) { return h.d + (static_cast<int64_t>(c / kStep) * h.piece + place) * kStep + c % kStep; };
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  constexpr int kUnits = kDeltaTokens * kTileM / 8 / kThreads;   // of 8 columns, 64 columns of 8 tokens a wave
+  static_assert(kDeltaTokens == kThreads / kWave * 8 && kUnits == kTileM / kPart, "a wave has its tokens");
+  const int lane = threadIdx.x % kWave, place = t0 + threadIdx.x / 8, c1 = c0 + lane % 8 * 8;
+  const float a = place < count ? h.a[first + place] : 0.0f;
+  const float z = a != 0.0f ? h.lse[first + place] : 0.0f, g = ldexpf(a, up);
+  f32x4 l[kUnits][2] = {};
+  if (a != 0.0f) {
 #pragma unroll
-  for (int u = wave; u < kDeltaTokens / 8 * (kDeltaCols / kPart); u += kThreads / kWave) {   // 8 tokens by 64 columns
-    const int place = t0 + u % (kDeltaTokens / 8) * 8 + lane / 8, c = c0 + u / (kDeltaTokens / 8) * kPart + lane % 8 * 8;
-    if (c >= h.vp) continue;
-    const bool live = place < count;
-    const float a = live ? h.a[first + place] : 0.0f;
+    for (int u = 0; u < kUnits; ++u) {
+      l[u][0] = *reinterpret_cast<const f32x4*>(logit_at(h, c1 + u * kPart, place));
+      l[u][1] = *reinterpret_cast<const f32x4*>(logit_at(h, c1 + u * kPart + 4, place));
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int c = c1 + u * kPart;
     u32x4 out = {};
     h8 hi = {}, lo = {};
     if (a != 0.0f) {
-      const float z = h.lse[first + place], g = ldexpf(a, up);
-      const f32x4* l = reinterpret_cast<const f32x4*>(h.logits + (static_cast<int64_t>(c / kTileM) * h.piece + place) * kTileM + c % kTileM);
-      const f32x4 l0 = l[0], l1 = l[1];
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[e] = exp2_of(__builtin_fmaf(e < 4 ? l0[e] : l1[e - 4], kLog2e, -z));
+        p[e] = exp2_of(__builtin_fmaf(l[u][e / 4][e % 4], kLog2e, -z));
         const float y = p[e] * g;
         hi[e] = static_cast<_Float16>(y);
         lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
@@ -841,19 +878,19 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
   __syncthreads();   // the targets' columns again, with their share; the first of equal rows has all of it
   const int k = max(h.top, 1);
   for (int i = threadIdx.x; i < k * kDeltaTokens; i += kThreads) {
-    const int place = t0 + i / k, slot = i % k;
-    if (place >= count) continue;
-    const int64_t mine = first + place, at = mine * k;
+    const int to = t0 + i / k, slot = i % k;
+    if (to >= count) continue;
+    const int64_t mine = first + to, at = mine * k;
     const int c = h.pidx[at + slot];
     const float a = h.a[mine];
-    if (c < c0 || c >= c0 + kDeltaCols || a == 0.0f || (slot && h.pidx[at + slot - 1] == c)) continue;
+    if (c < c0 || c >= c0 + kTileM || a == 0.0f || (slot && h.pidx[at + slot - 1] == c)) continue;
     float q = 0.0f;
     for (int s = slot; s < k && h.pidx[at + s] == c; ++s) q += h.pq[at + s];
     const float p = exp2_of(__builtin_fmaf(h.picked[at + slot], kLog2e, -h.lse[mine])) - q, y = p * ldexpf(a, up);
-    *d16(place, c) = static_cast<uint16_t>(bf16_rne(p));
+    *d16(to, c) = static_cast<uint16_t>(bf16_rne(p));
     const _Float16 hi = static_cast<_Float16>(y);
-    *part(place, c) = hi;
-    if constexpr (TWO) part(place, c)[kPart] = static_cast<_Float16>(y - static_cast<float>(hi));
+    *part(to, c) = hi;
+    if constexpr (TWO) part(to, c)[kPart] = static_cast<_Float16>(y - static_cast<float>(hi));
   }
 }
 
@@ -1066,6 +1103,7 @@ constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxRows = int64_t(1) <
 constexpr int64_t kHeadMaxElems = int64_t(1) << 33;
 constexpr int64_t kPieceTokens = 8192;   // tokens of a piece, unless the call says another number
 constexpr int64_t kPieceMax = 65536;
+constexpr int64_t kFewTokens = 512;
 constexpr int64_t kCus = 256;   // workgroups of a product: one a CU, each with tile after tile
 
 int64_t up_to(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -1075,7 +1113,7 @@ struct HeadShape {
   int64_t n = 0, npad = 0, rows = 0, cols = 0, vp = 0, hp = 0, top = 0, piece = 0, n_pieces = 0;
   int tile_n = 256;            // tokens of a tile
   int64_t dx_groups = 0;       // workgroups of the dx product
-  bool grad = false, widen = false, sums = false;   // sums: dW adds up in the workspace
+  bool grad = false, widen = false, stored = false, sums = false;   // sums: dW adds up in the workspace
   int64_t info, pieces, keep, xmax, ent, idx, q, kept, pent, a, lse, pidx, pq, picked, xb, xh, stat, logits, d, slabs, table, acc;
   int64_t bytes = 0;
 };
@@ -1105,6 +1143,10 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->n_pieces = most ? (s->npad + most - 1) / most : 0;
   s->piece = s->n_pieces ? up_to((s->npad + s->n_pieces - 1) / s->n_pieces, 256) : 256;
   s->tile_n = n <= 64 ? 64 : n <= 128 ? 128 : 256;
+  // the logits at the targets: out of the stored logits where these are stored
+  // anyway, or where a wave's rows would hold several of a token's targets; else
+  // out of the registers
+  s->stored = grad || t.rows < 256 * top;
   s->sums = grad && packed_dt == RS_BF16 && s->n_pieces > 1;
   const int64_t k = std::max<int64_t>(top, 1), dx_m = (t.cols + kTileM - 1) / kTileM;
   for (int64_t tt = 1; tt <= (std::min(s->piece, n) + s->tile_n - 1) / s->tile_n; ++tt)
@@ -1133,7 +1175,7 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->stat = room(s->piece * (s->vp / 64) * 8);
   s->table = room(s->widen ? s->rows * s->hp * 2 : 0);
   s->xh = room(grad ? s->npad * up_to(s->cols, kTileM) * 2 : 0);
-  s->logits = room(grad ? s->piece * s->vp * 4 : 0);
+  s->logits = room(s->stored ? s->piece * s->vp * 4 : 0);
   s->d = room(grad ? s->piece * s->vp * 2 : 0);
   s->slabs = room(grad ? s->dx_groups * kTileM * s->tile_n * 4 : 0);
   s->acc = room(s->sums ? s->rows * s->cols * 4 : 0);
@@ -1172,13 +1214,21 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     const int64_t tokens = std::min(s.piece, s.n - i * s.piece);
     const int64_t n_tiles = (tokens + BN - 1) / BN, m_tiles = s.vp / kTileM;
     const dim3 tiles(static_cast<unsigned>(std::min<int64_t>(up_to(m_tiles * n_tiles, 8), kCus))), threads(HeadTile<BN>::kThreads);
-    if (grad) hipLaunchKernelGGL((head_logits_kernel<BN, true>), tiles, threads, 0, q, h, piece, c);
+    if (s.stored) hipLaunchKernelGGL((head_logits_kernel<BN, true>), tiles, threads, 0, q, h, piece, c);
     else hipLaunchKernelGGL((head_logits_kernel<BN, false>), tiles, threads, 0, q, h, piece, c);
-    hipLaunchKernelGGL(head_loss_kernel, dim3(static_cast<unsigned>((tokens + kLossTokens - 1) / kLossTokens)), dim3(kThreads), 0, q, h,
-                       piece, static_cast<int>(s.vp / (32 * HeadTile<BN>::NI)), f, a.loss);
+    const int stats = static_cast<int>(s.vp / (32 * HeadTile<BN>::NI));
+    const dim3 few(static_cast<unsigned>(tokens)), many(static_cast<unsigned>((tokens + 7) / 8));
+    if (tokens <= kFewTokens && s.stored)
+      hipLaunchKernelGGL((head_loss_kernel<1, true>), few, dim3(kThreads), 0, q, h, piece, stats, f, a.loss);
+    else if (tokens <= kFewTokens)
+      hipLaunchKernelGGL((head_loss_kernel<1, false>), few, dim3(kThreads), 0, q, h, piece, stats, f, a.loss);
+    else if (s.stored)
+      hipLaunchKernelGGL((head_loss_kernel<8, true>), many, dim3(kThreads), 0, q, h, piece, stats, f, a.loss);
+    else
+      hipLaunchKernelGGL((head_loss_kernel<8, false>), many, dim3(kThreads), 0, q, h, piece, stats, f, a.loss);
     if (!grad) continue;
     const bool two = a.packed_dt == RS_F32;
-    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStep) / kDeltaTokens), static_cast<unsigned>((s.vp + kDeltaCols - 1) / kDeltaCols));
+    const dim3 delta(static_cast<unsigned>(up_to(tokens, kStep) / kDeltaTokens), static_cast<unsigned>(s.vp / kTileM));
     if (two) hipLaunchKernelGGL(head_delta_kernel<true>, delta, dim3(kThreads), 0, q, h, piece);
     else hipLaunchKernelGGL(head_delta_kernel<false>, delta, dim3(kThreads), 0, q, h, piece);
     const int64_t dx_m = (s.cols + kTileM - 1) / kTileM;
