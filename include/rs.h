@@ -492,9 +492,10 @@ int rs_head_loss(rs_plan* plan, int64_t tensor, const void* gathered, const void
  * on W's interval, sigma = grad_scale (RS_SCALE_GIVEN) or fl32(grad_scale / V)
  * (RS_SCALE_INV_V). A token without a target gets a dx of +0.0 and adds nothing,
  * and neither does one of weight 0, whatever its x holds. p - e_y is computed in
- * fp32; for dx it is rounded to bf16, for the table's gradient to fp16 (a bf16
- * packed buffer) or to 22 bits (fp32), below a few 2^-24 of the largest
- * a_t it loses bits, as x does below 2^-28 of the largest |x|. Sums are fp32.
+ * fp32; for dx it is rounded to bf16. For the table's gradient a_t (p - e_y) is
+ * rounded to 11 bits (a bf16 packed buffer) or 22 (fp32), or to within 2^-38 of
+ * the largest |a_t| where that is more, and x to within 2^-38 of the largest |x|
+ * (its bf16 values are exact down to 2^-28 of it). Sums are fp32.
  * W's interval is written whole (with n_tokens = 0 too; with prev = packed and
  * no targets it is left alone); other positions are left alone.
  * weights: device, n_tokens fp32, or NULL. dx: device, n_tokens x cols bf16.
@@ -530,12 +531,13 @@ int rs_distill_grad(rs_plan* plan, int64_t tensor, const void* gathered, const v
                     int32_t packed_dt, int32_t scale_mode, float grad_scale, int64_t piece, void* work, int64_t work_bytes,
                     void* stream);
 
-/* Bytes of workspace for the four calls on this tensor: n_tokens, piece and
- * top (0 for labels) as in the call; grad 1 for the gradients (a workspace that
+/* Bytes of workspace for the four calls on this tensor with n_tokens tokens, or
+ * fewer: piece and top (0 for labels) as in the call; grad 1 for the gradients (a workspace that
  * also serves the losses), packed_dt the packed buffer's type. About
  * 4 n cols + 16 n top for the tokens; rows * cols * 2 more where cols is no
  * multiple of 64; piece * rows * 4 where rows < 256 top, piece * rows * 6 for
- * gradients, for these piece * cols * 4 or at most 256 MiB for parts of dx, and rows * cols * 4 more for a bf16 packed buffer and more than one piece.
+ * gradients; for these too piece * cols * 4 or at most 256 MiB for parts of dx,
+ * and rows * cols * 4 for a bf16 packed buffer and more than one piece.
  * Errors: RS_EINVAL, RS_EDTYPE, RS_ERANGE. */
 int rs_head_workspace(const rs_plan* plan, int64_t tensor, int64_t n_tokens, int64_t top, int32_t grad, int32_t packed_dt,
                       int64_t piece, int64_t* bytes);

@@ -554,7 +554,7 @@ def rs_layer_norm_grad(plan: Plan, weight: int, gathered: torch.Tensor, x: torch
 # ---------------------------------------------------------------- the vocabulary head
 
 def rs_head_workspace(plan: Plan, tensor: int, n_tokens: int, top: int = 0, packed=None, piece: int = 0) -> torch.Tensor:
-    """Workspace (uint8, on the plan's device) for the head's calls with n_tokens tokens: for the
+    """Workspace (uint8, on the plan's device) for the head's calls with n_tokens tokens, or fewer: for the
     losses, or with packed (the packed buffer, or its dtype) for the gradients too. top: logits of
     the teacher per token, 0 for labels. piece: tokens whose logits are held at a time (a multiple
     of 256; 0: up to 8192), the same as in the call. Calls that may overlap need a workspace each."""

@@ -825,6 +825,14 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
 
 // ------------------------------------------------------------------ gradients
 
+// A product that is split: both parts must be of one value, where the compiler
+// otherwise multiplies a second time with a single rounding to fp16, which ends on
+// the other side of a tie now and then.
+__device__ __forceinline__ float one_value(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
 // d = p - q of a block of 32 tokens and 256 columns: bf16 for dx, and times the
 // token's share of the gradient, scaled, in fp16 parts for dW, where the logits
 // lay, in rows of 256 columns a token: 64 logits give way to 64 values of each
@@ -865,7 +873,7 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         p[e] = exp2_of(__builtin_fmaf(l[u][e / 4][e % 4], kLog2e, -z));
-        const float y = p[e] * g;
+        const float y = one_value(p[e] * g);
         hi[e] = static_cast<_Float16>(y);
         lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
       }
@@ -886,7 +894,7 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
     if (c < c0 || c >= c0 + kTileM || a == 0.0f || (slot && h.pidx[at + slot - 1] == c)) continue;
     float q = 0.0f;
     for (int s = slot; s < k && h.pidx[at + s] == c; ++s) q += h.pq[at + s];
-    const float p = exp2_of(__builtin_fmaf(h.picked[at + slot], kLog2e, -h.lse[mine])) - q, y = p * ldexpf(a, up);
+    const float p = exp2_of(__builtin_fmaf(h.picked[at + slot], kLog2e, -h.lse[mine])) - q, y = one_value(p * ldexpf(a, up));
     *d16(to, c) = static_cast<uint16_t>(bf16_rne(p));
     const _Float16 hi = static_cast<_Float16>(y);
     *part(to, c) = hi;
@@ -1138,7 +1146,8 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->vp = up_to(t.rows, kTileM);
   s->hp = up_to(t.cols, kStep);
   s->widen = s->hp != t.cols;
-  // pieces of equal size, of at most the tokens asked for
+  // pieces of equal size, of at most the tokens asked for; the workspace has room
+  // for these, so that one for more tokens serves fewer
   const int64_t most = std::min(s->npad, piece ? piece : kPieceTokens);
   s->n_pieces = most ? (s->npad + most - 1) / most : 0;
   s->piece = s->n_pieces ? up_to((s->npad + s->n_pieces - 1) / s->n_pieces, 256) : 256;
@@ -1149,7 +1158,7 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->stored = grad || t.rows < 256 * top;
   s->sums = grad && packed_dt == RS_BF16 && s->n_pieces > 1;
   const int64_t k = std::max<int64_t>(top, 1), dx_m = (t.cols + kTileM - 1) / kTileM;
-  for (int64_t tt = 1; tt <= (std::min(s->piece, n) + s->tile_n - 1) / s->tile_n; ++tt)
+  for (int64_t tt = 1; tt <= (std::min(most, n) + s->tile_n - 1) / s->tile_n; ++tt)
     s->dx_groups = std::max(s->dx_groups, dx_m * tt * dx_splits(static_cast<int>(dx_m * tt), static_cast<int>(s->vp / kStep)));
   int64_t at = 0;
   auto room = [&](int64_t bytes) {
@@ -1172,11 +1181,11 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->pq = room(s->npad * k * 4);
   s->picked = room(s->npad * k * 4);
   s->xb = room(s->npad * s->hp * 2);
-  s->stat = room(s->piece * (s->vp / 64) * 8);
+  s->stat = room(most * (s->vp / 64) * 8);
   s->table = room(s->widen ? s->rows * s->hp * 2 : 0);
   s->xh = room(grad ? s->npad * up_to(s->cols, kTileM) * 2 : 0);
-  s->logits = room(s->stored ? s->piece * s->vp * 4 : 0);
-  s->d = room(grad ? s->piece * s->vp * 2 : 0);
+  s->logits = room(s->stored ? most * s->vp * 4 : 0);
+  s->d = room(grad ? most * s->vp * 2 : 0);
   s->slabs = room(grad ? s->dx_groups * kTileM * s->tile_n * 4 : 0);
   s->acc = room(s->sums ? s->rows * s->cols * 4 : 0);
   s->bytes = n ? at : 0;
