@@ -49,7 +49,7 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // C[m, n] = sum_k P[m, k] Q[n, k] on one 256 x BN tile, 32 x 32 accumulators. Either operand may lie with k contiguous (plain) or with its
 // other index contiguous (TR): a TR operand is read out of LDS transposed
 // (ds_read_b64_tr_b16), so the table and d are used as they lie in memory.
-template <int BN, int WAVES = BN == 256 ? 4 : 8>
+template <int BN, int WAVES = 8>
 struct HeadTile {
   static constexpr int kN = BN, kWaves = WAVES, kThreads = kWaves * kWave;
   static constexpr int WR = BN == 256 ? 2 : 4;              // wave rows
@@ -58,7 +58,16 @@ struct HeadTile {
   static constexpr int kStages = BN == 256 ? 2 : BN == 128 ? 3 : 4, kStagesQ = BN == 256 ? 3 : kStages;
   static constexpr int kLds = (kStages * kTileM + kStagesQ * BN) * kStep * 2;
 };
-using DwTile = HeadTile<256, 8>;
+// dx has four waves, which read less out of LDS for as many multiplications
+// (2048 x 131072 x 2048: 0.85 ms, with eight 0.91); dW eight (4096 x 131072 x 4096
+// with both parts: 6.9 ms, with four 8.0). The logits have eight, of which one
+// multiplies while the other keeps its results, up to kShortCols columns, and four
+// above (2048 tokens by 131072 rows of 256, 1024, 2048: 200, 549, 1060 us with eight,
+// 270, 600, 1120 with four; 4096 tokens, 4096 columns: 3.86 ms and 3.74).
+constexpr int64_t kShortCols = 2048;
+template <int BN>
+using DxTile = HeadTile<BN, BN == 256 ? 4 : 8>;
+using DwTile = HeadTile<256>;
 
 // One operand's tile: from `base` on, `left` bytes may be read. Plain: `rows`
 // rows exist (those past them repeat the last), a stage lies `step` bytes behind
@@ -173,8 +182,9 @@ struct HeadAcc {
 // on, spread over a whole stage, the places that this stage leaves are loaded
 // again, P's for kStages stages later and behind them Q's for kStagesQ later.
 // A load into LDS holds its wave up while others are on their way, so loads in
-// one burst stop the multiplications: 8 of them after each turn took 4096 x
-// 131072 x 4096 from 2.85 (loads left out) to 3.33 ms.
+// one burst stop the multiplications: in one, dx of 4096 x 131072 x 4096 took
+// 3.84 ms, spread it takes 3.0 to 3.2 (1370 to 1460 TFLOP/s, the matrix cores busy
+// for 73 to 75% of it at 1.55 to 1.75 GHz; a library product of the size 2.8).
 template <class T, bool F16, bool PT, bool QT, bool RAGGED, bool PARTS>
 struct Contract {
 using FP = Fetch<kTileM, PT, RAGGED, false, T::kWaves>;
@@ -729,14 +739,17 @@ __device__ __forceinline__ void keep_logits(const Head& h, int piece, int count,
                 f32x4{acc.v[i][j][e], acc.v[i][j][e + 1], acc.v[i][j][e + 2], acc.v[i][j][e + 3]};
       }
     }
-    if constexpr (STORE) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Tiles of the logits of a piece, 256 rows of the table by BN tokens.
-template <int BN, bool STORE>
-__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Head h, int piece, float factor) {
-  using T = HeadTile<BN>;
+// Tiles of the logits of a piece, 256 rows of the table by BN tokens; one
+// workgroup a CU, which takes tile after tile and loads the next one while it keeps
+// this one. Bound by the matrix cores: 4096 x 131072 x 4096 in 3.73 ms with the
+// logits stored and 3.65 without, 1180 and 1205 TFLOP/s; by memory for up to
+// 64 tokens (48 x 131072 x 4096: 178 us, 6.0 TB/s of the table).
+template <class T, bool STORE>
+__global__ __launch_bounds__(T::kThreads) void head_logits_kernel(Head h, int piece, float factor) {
+  constexpr int BN = T::kN;
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   const int count = h.pieces[piece].count, m_tiles = h.vp / kTileM, n_tiles = (count + BN - 1) / BN;
   Items items(m_tiles * n_tiles);
@@ -765,8 +778,8 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_logits_kernel(Hea
 
 // Log-sum-exp and loss of TOKENS tokens, and (STORED) the logits at their targets
 // out of the stored ones. A token's numbers lie a piece apart, so eight
-// neighbours share what a load brings; few tokens take a workgroup each (48 with
-// 2048 numbers: 32 us with eight, 7 with one).
+// neighbours share what a load brings; few tokens take a workgroup each. Bound by
+// latency: 15 us for 4096 tokens with 1024 numbers each (34 MB).
 template <int TOKENS, bool STORED>
 __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, int stats, float factor, float* loss) {
   constexpr int kParts = kThreads / TOKENS;
@@ -833,6 +846,7 @@ __device__ __forceinline__ float one_value(float x) {
   return x;
 }
 
+// Bound by memory: 4096 tokens by 131072 rows in 0.85 ms, 5.1 TB/s.
 // d = p - q of a block of 32 tokens and 256 columns: bf16 for dx, and times the
 // token's share of the gradient, scaled, in fp16 parts for dW, where the logits
 // lay, in rows of 256 columns a token: 64 logits give way to 64 values of each
@@ -903,10 +917,12 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
 }
 
 // dx of a piece: 256 columns by BN tokens, one part of the contraction over the
-// table's rows. Sums go to the part's slab, in the registers' order.
+// table's rows (see dx_splits). Sums go to the part's slab, in the registers'
+// order. Bound by the matrix cores: 4096 x 131072 x 4096 in 3.0 to 3.2 ms; by
+// memory for few tokens (48 x 131072 x 1024: 48 us, 5.9 TB/s).
 template <int BN>
-__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_kernel(Head h, int piece) {
-  using T = HeadTile<BN>;
+__global__ __launch_bounds__(DxTile<BN>::kThreads) void head_dx_kernel(Head h, int piece) {
+  using T = DxTile<BN>;
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   const HeadPiece info = h.pieces[piece];
   const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = (info.count + BN - 1) / BN, tiles = m_tiles * n_tiles;
@@ -941,8 +957,8 @@ __global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_kernel(Head h,
 // dx of one 32-column block of a tile for each of its waves: the parts added in
 // their order, times a, rounded to bf16, to the tokens' own rows.
 template <int BN>
-__global__ __launch_bounds__(HeadTile<BN>::kThreads) void head_dx_sum_kernel(Head h, int piece, uint16_t* dx) {
-  using T = HeadTile<BN>;
+__global__ __launch_bounds__(DxTile<BN>::kThreads) void head_dx_sum_kernel(Head h, int piece, uint16_t* dx) {
+  using T = DxTile<BN>;
   constexpr int kBlocks = T::NI * T::NJ * 4;
   const HeadPiece info = h.pieces[piece];
   const int m_tiles = (h.cols + kTileM - 1) / kTileM, n_tiles = (info.count + BN - 1) / BN, tiles = m_tiles * n_tiles;
@@ -1023,8 +1039,10 @@ __device__ __forceinline__ void keep_dw(const Head& h, const TileAt& at, const F
 
 // The same for rows of any alignment: half of the tile's rows at a time go
 // through LDS, 1 KiB each, and a wave reads and writes whole rows. Piece c of row
-// r lies at place c ^ (r % 32). Single elements out of the registers took 405 us
-// for 32001 x 1001 and 517 tokens, this way 187.
+// r lies at place c ^ (r % 32). 32001 x 1001 and 517 tokens: 187 us, single
+// elements out of the registers 405. Where rows are aligned it is no faster
+// (131072 x 4096 and 4096 tokens: 7.13 ms against 7.03, 512 tokens 258 us against
+// 250), so these have keep_dw.
 template <bool OUT16>
 __device__ __forceinline__ void keep_dw_odd(const Head& h, const TileAt& at, const Finish<OUT16>& f, const HeadAcc<DwTile>& acc, char* lds) {
   using T = DwTile;
@@ -1062,7 +1080,11 @@ __device__ __forceinline__ void keep_dw_odd(const Head& h, const TileAt& at, con
   barrier();
 }
 
-// Tiles of dW of a piece, 256 columns by 256 rows of the table.
+// Tiles of dW of a piece, 256 columns by 256 rows of the table; one workgroup a
+// CU, with tile after tile (512 tokens, 131072 x 1024: 259 us, one tile a workgroup
+// 285). Bound by the matrix cores: 1250 TFLOP/s with
+// two parts, 1170 with one; for few tokens by the tiles' stores, one CU with one
+// tile at a time.
 template <bool TWO, bool OUT16>
 __global__ __launch_bounds__(DwTile::kThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
   using T = DwTile;
@@ -1109,9 +1131,14 @@ __global__ __launch_bounds__(DwTile::kThreads) void head_dw_kernel(Head h, int p
 
 constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxRows = int64_t(1) << 21, kHeadMaxCols = int64_t(1) << 16;
 constexpr int64_t kHeadMaxElems = int64_t(1) << 33;
-constexpr int64_t kPieceTokens = 8192;   // tokens of a piece, unless the call says another number
+// Tokens of a piece, unless the call says another number (16384 tokens of 131072 x
+// 4096, fp32 gradients: 57.7 ms; 59.6 with 4096, which halves the workspace).
+constexpr int64_t kPieceTokens = 8192;
 constexpr int64_t kPieceMax = 65536;
-constexpr int64_t kFewTokens = 512;
+// Up to here a workgroup takes one token's loss, above it eight (131072 rows: 100
+// tokens 8.7 us with one, 16.0 with eight; 200 7.7 and 11.1; 512 9.9 and 7.8; 1024
+// 15.8 and 8.8).
+constexpr int64_t kFewTokens = 256;
 constexpr int64_t kCus = 256;   // workgroups of a product: one a CU, each with tile after tile
 
 int64_t up_to(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -1151,6 +1178,9 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   const int64_t most = std::min(s->npad, piece ? piece : kPieceTokens);
   s->n_pieces = most ? (s->npad + most - 1) / most : 0;
   s->piece = s->n_pieces ? up_to((s->npad + s->n_pieces - 1) / s->n_pieces, 256) : 256;
+  // tokens of a tile of the logits and dx (131072 x 1024: 48 tokens 82 + 48 us with
+  // 64, 84 + 54 with 128, 104 + 77 with 256; 100 tokens 84 + 59 with 128, 105 + 82
+  // with 256)
   s->tile_n = n <= 64 ? 64 : n <= 128 ? 128 : 256;
   // the logits at the targets: out of the stored logits where these are stored
   // anyway, or where a wave's rows would hold several of a token's targets; else
@@ -1222,9 +1252,15 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     const int piece = static_cast<int>(i);
     const int64_t tokens = std::min(s.piece, s.n - i * s.piece);
     const int64_t n_tiles = (tokens + BN - 1) / BN, m_tiles = s.vp / kTileM;
-    const dim3 tiles(static_cast<unsigned>(std::min<int64_t>(up_to(m_tiles * n_tiles, 8), kCus))), threads(HeadTile<BN>::kThreads);
-    if (s.stored) hipLaunchKernelGGL((head_logits_kernel<BN, true>), tiles, threads, 0, q, h, piece, c);
-    else hipLaunchKernelGGL((head_logits_kernel<BN, false>), tiles, threads, 0, q, h, piece, c);
+    const dim3 tiles(static_cast<unsigned>(std::min<int64_t>(up_to(m_tiles * n_tiles, 8), kCus)));
+    auto logits = [&](auto tile) {
+      using T = decltype(tile);
+      static_assert(T::NI == HeadTile<BN>::NI, "rows of the statistics");
+      if (s.stored) hipLaunchKernelGGL((head_logits_kernel<T, true>), tiles, dim3(T::kThreads), 0, q, h, piece, c);
+      else hipLaunchKernelGGL((head_logits_kernel<T, false>), tiles, dim3(T::kThreads), 0, q, h, piece, c);
+    };
+    if (s.cols <= kShortCols) logits(HeadTile<BN>());
+    else logits(DxTile<BN>());
     const int stats = static_cast<int>(s.vp / (32 * HeadTile<BN>::NI));
     const dim3 few(static_cast<unsigned>(tokens)), many(static_cast<unsigned>((tokens + 7) / 8));
     if (tokens <= kFewTokens && s.stored)
@@ -1241,9 +1277,10 @@ void launch_head(const HeadShape& s, const Head& h, const HeadArgs& a, float sig
     if (two) hipLaunchKernelGGL(head_delta_kernel<true>, delta, dim3(kThreads), 0, q, h, piece);
     else hipLaunchKernelGGL(head_delta_kernel<false>, delta, dim3(kThreads), 0, q, h, piece);
     const int64_t dx_m = (s.cols + kTileM - 1) / kTileM;
-    hipLaunchKernelGGL(head_dx_kernel<BN>, dim3(static_cast<unsigned>(up_to(s.dx_groups, 8))), threads, 0, q, h, piece);
-    hipLaunchKernelGGL(head_dx_sum_kernel<BN>, dim3(static_cast<unsigned>(dx_m * n_tiles * HeadTile<BN>::NI * HeadTile<BN>::NJ * 4)),
-                       threads, 0, q, h, piece, static_cast<uint16_t*>(a.dx));
+    const dim3 dx_threads(DxTile<BN>::kThreads);
+    hipLaunchKernelGGL(head_dx_kernel<BN>, dim3(static_cast<unsigned>(up_to(s.dx_groups, 8))), dx_threads, 0, q, h, piece);
+    hipLaunchKernelGGL(head_dx_sum_kernel<BN>, dim3(static_cast<unsigned>(dx_m * n_tiles * DxTile<BN>::NI * DxTile<BN>::NJ * 4)),
+                       dx_threads, 0, q, h, piece, static_cast<uint16_t*>(a.dx));
     // dW: into the packed buffer, or with more than one piece into fp32 sums that the last piece rounds
     const dim3 dw(static_cast<unsigned>(std::min<int64_t>(up_to(dx_m * (s.vp / DwTile::kN), 8), kCus)));
     const int64_t start = a.tensor;

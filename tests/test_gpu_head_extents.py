@@ -187,3 +187,16 @@ def test_both_parts_of_d_are_of_one_value(gpu_lib):
     got = packed[:rows * cols].view(rows, cols).double()
     assert bool(((got - want).abs() <= 2.0 ** -15 * want.abs()).all())
     plan.close()
+
+
+@pytest.mark.parametrize("n,rows,cols,top", [(300, 700, 2049, 0), (257, 300, 2112, 0), (300, 520, 2304, 7), (1, 300, 2112, 0), (70, 300, 2100, 3)])
+def test_long_rows(gpu_lib, n, rows, cols, top):
+    import structure_aware_grouped_amd as rs
+    case = Case(rs, n, rows, cols, top=top)
+    want = case.expect()
+    loss = torch.full((n,), float("nan"), device=DEV)
+    case.loss(rs, loss, case.work(rs))
+    assert (abs(_f64(loss) - want["loss"]) <= want["off_loss"]).all()
+    _check_grad(rs, case, "f32")
+    _check_grad(rs, case, "bf16", mode="other", inv_v=True)
+    case.plan.close()
