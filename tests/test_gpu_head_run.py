@@ -13,6 +13,10 @@ own rounding of p - q is one of 2^-8 for dx and one of 2^-22 for the table. fp32
 sums of at most 600 values add 600 * 2^-23 = 2^-13.8 of the sums of absolute
 values, products of bounds (second order) at most 2^-8 * (1 + 6) of the bounds:
 together under 2^-4 of the bounds and 2^-13 of the sums."""
+import os
+import re
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -160,3 +164,29 @@ def test_a_step_in_a_graph(gpu_lib, top):
     del graph
     m.plan.close()
     ref.plan.close()
+
+
+def test_the_readme_example_of_these_calls_runs(gpu_lib):
+    """And its losses and the table's gradient hold against torch's operations in fp32."""
+    import structure_aware_grouped_amd as rs
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    block = re.search(r"tied to the lookup's \(imports as above\):\n\n((?:    .*\n|\n)+)", text).group(1)
+    env = {"torch": torch, "rs": rs, "TensorSpec": TensorSpec}
+    exec(compile(textwrap.dedent(block), "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    start = env["starts"][0]
+    table = env["gathered"][start:start + 32000 * 4096].view(32000, 4096).double()
+    y, target, at = env["y"].double(), env["targets"], torch.arange(64, device=DEV)
+    got = env["packed"][start:start + 32000 * 4096].view(32000, 4096)
+    total = torch.zeros(32000, 4096, device=DEV, dtype=torch.float64)
+    for t0 in range(0, 2048, 64):
+        l = 2.0 ** -6 * y[t0:t0 + 64] @ table.T
+        # 4096 products of normal values: sums of absolute values of 2^-6 * 4096 * 2 / pi = 41, under 60; 2 * 4098 u of
+        # them is 0.03. Partial sums stay under 10 (deviation 1): 256 additions of two half steps of those are 3.1e-4
+        want = l.logsumexp(1) - l[at, target[t0:t0 + 64]]
+        assert float((env["loss"][t0:t0 + 64].double() - want).abs().max()) <= 2 * 3.1e-4 + 200 * 2.0 ** -24
+        d = l.softmax(1)
+        d[at, target[t0:t0 + 64]] -= 1.0
+        total += 2.0 ** -6 * d.T @ y[t0:t0 + 64]
+    # d is off by at most 2 * 3.1e-4 of p, so the gradient by that of the sums: in the Frobenius norm under 2^-9 of it
+    assert float((got.double() - total).norm() / total.norm()) <= 2.0 ** -9
