@@ -492,7 +492,8 @@ int rs_head_loss(rs_plan* plan, int64_t tensor, const void* gathered, const void
  * on W's interval, sigma = grad_scale (RS_SCALE_GIVEN) or fl32(grad_scale / V)
  * (RS_SCALE_INV_V). A token without a target gets a dx of +0.0 and adds nothing,
  * and neither does one of weight 0, whatever its x holds. p - e_y is computed in
- * fp32; for dx it is rounded to bf16. For the table's gradient a_t (p - e_y) is
+ * fp32; for dx it is rounded to bf16, and what that leaves at the target is added
+ * in fp32. For the table's gradient a_t (p - e_y) is
  * rounded to 11 bits (a bf16 packed buffer) or 22 (fp32), or to within 2^-38 of
  * the largest |a_t| where that is more, and x to within 2^-38 of the largest |x|
  * (its bf16 values are exact down to 2^-28 of it). Sums are fp32.
@@ -536,7 +537,8 @@ int rs_distill_grad(rs_plan* plan, int64_t tensor, const void* gathered, const v
  * also serves the losses), packed_dt the packed buffer's type. About
  * 4 n cols + 16 n top for the tokens; rows * cols * 2 more where cols is no
  * multiple of 64; piece * rows * 4 where rows < 256 top, piece * rows * 6 for
- * gradients; for these too piece * cols * 4 or at most 256 MiB for parts of dx,
+ * gradients; for these too piece * cols * 4, as much again or at most 256 MiB for
+ * parts of dx,
  * and rows * cols * 4 for a bf16 packed buffer and more than one piece.
  * Errors: RS_EINVAL, RS_EDTYPE, RS_ERANGE. */
 int rs_head_workspace(const rs_plan* plan, int64_t tensor, int64_t n_tokens, int64_t top, int32_t grad, int32_t packed_dt,
