@@ -359,7 +359,7 @@ struct Items {
 // What the tokens of a call come to, known on the device only.
 struct HeadInfo {
   int32_t count;     // tokens with a target
-  int32_t ex, ec;    // |x| < 2^ex and |a_t| < 2^ec over them
+  int32_t ex, ec;    // |a_t| < 2^ec over them, |x| < 2^ex over those of a_t that is not 0
   int32_t pad;
 };
 struct HeadPiece {
@@ -541,8 +541,8 @@ __global__ __launch_bounds__(kKeepThreads) void head_keep_kernel(Head h, const f
     base += all;
     if (mine) {
       h.kept[before + __popcll(set & ((1ull << lane) - 1))] = t;
-      most_x = fmaxf(most_x, h.xmax[t]);
       const float a = fabsf((weights ? weights[t] : 1.0f) * factor);
+      if (a != 0.0f) most_x = fmaxf(most_x, h.xmax[t]);   // others have zeros as fp16
       if (a <= FLT_MAX) most_a = fmaxf(most_a, a);
     }
   }
