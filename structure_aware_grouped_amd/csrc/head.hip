@@ -400,7 +400,7 @@ constexpr int kNone = 0x7fffffff;   // behind every row of the table
 
 // One token a wave: its rows of the table in ascending order and their share q,
 // whether it has any, and the largest finite |x| (GRAD). A token without a target gets its
-// loss (and dx) of zero here.
+// loss (and dx) of zero here, and its x is not read.
 template <bool GRAD>
 __global__ __launch_bounds__(kThreads) void head_targets_kernel(Head h, const void* ids, bool wide, const void* teacher,
                                                                 bool teacher16, float temperature, const uint16_t* x, float* loss,
@@ -464,27 +464,27 @@ __global__ __launch_bounds__(kThreads) void head_targets_kernel(Head h, const vo
   for (int o = kWave / 2; o > 0; o >>= 1) ent += __shfl_xor(ent, o, kWave);
   float most = 0.0f;
   if constexpr (GRAD) {
-    const uint16_t* from = x + t * h.cols;
-    if (h.cols % 8 == 0) {
-      for (int c = lane * 8; c < h.cols; c += kWave * 8) {
-        float v[8];
-        In<true>::widen(*reinterpret_cast<const u32x4*>(from + c), v);
+    if (some) {
+      const uint16_t* from = x + t * h.cols;
+      if (h.cols % 8 == 0) {
+        for (int c = lane * 8; c < h.cols; c += kWave * 8) {
+          float v[8];
+          In<true>::widen(*reinterpret_cast<const u32x4*>(from + c), v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = fabsf(v[e]) <= FLT_MAX ? fmaxf(most, fabsf(v[e])) : most;
+          for (int e = 0; e < 8; ++e) most = fabsf(v[e]) <= FLT_MAX ? fmaxf(most, fabsf(v[e])) : most;
+        }
+      } else {
+        for (int c = lane; c < h.cols; c += kWave) {
+          const float v = fabsf(In<true>::elem(from, c));
+          most = v <= FLT_MAX ? fmaxf(most, v) : most;
+        }
       }
+#pragma unroll
+      for (int o = kWave / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, kWave));
+    } else if (h.cols % 8 == 0) {
+      for (int c = lane * 8; c < h.cols; c += kWave * 8) *reinterpret_cast<u32x4*>(dx + t * h.cols + c) = u32x4{};
     } else {
-      for (int c = lane; c < h.cols; c += kWave) {
-        const float v = fabsf(In<true>::elem(from, c));
-        most = v <= FLT_MAX ? fmaxf(most, v) : most;
-      }
-    }
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, kWave));
-    if (!some) {
-      if (h.cols % 8 == 0)
-        for (int c = lane * 8; c < h.cols; c += kWave * 8) *reinterpret_cast<u32x4*>(dx + t * h.cols + c) = u32x4{};
-      else
-        for (int c = lane; c < h.cols; c += kWave) dx[t * h.cols + c] = 0;
+      for (int c = lane; c < h.cols; c += kWave) dx[t * h.cols + c] = 0;
     }
   }
   if (lane == 0) {

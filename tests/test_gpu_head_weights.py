@@ -38,3 +38,25 @@ def test_large_values_in_tokens_of_weight_zero(gpu_lib, top, packed_dt, piece, v
     assert torch.equal(dx, other[1]) and not bool(dx[masked].any())
     assert torch.equal(packed, other[2]) and bool(packed[case.at].any())
     case.plan.close()
+
+
+@pytest.mark.parametrize("top", [0, 6])
+def test_x_of_tokens_without_a_target_is_not_read(gpu_lib, top):
+    """Whatever they hold, a call leaves the same bytes in a workspace that was cleared ahead of it."""
+    import structure_aware_grouped_amd as rs
+    n, rows, cols = 300, 257, 72
+    case = Case(rs, n, rows, cols, top=top, none=0.4)
+    live = torch.from_numpy(case.expect()["live"]).to(DEV)
+    assert 0 < int(live.sum()) < n
+    outs = []
+    for value in (0.0, 2.0 ** 99, float("nan")):
+        case.x[~live] = value
+        packed = torch.zeros(case.total, device=DEV)
+        loss, dx = torch.zeros(n, device=DEV), torch.zeros(n, cols, device=DEV, dtype=torch.bfloat16)
+        work = case.work(rs, packed).zero_()
+        case.grad(rs, loss, dx, packed, work)
+        assert not bool(loss[~live].any()) and not bool(dx[~live].any())
+        outs.append((work, loss, dx, packed))
+    for other in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
+    case.plan.close()
