@@ -381,7 +381,8 @@ struct Head {
   int32_t* idx;           // by token, top each, ascending: row of the table, kNone behind them
   float* q;
   int32_t* kept;          // by place: the token
-  float *pent, *a, *lse;  // by place; lse in powers of two
+  float *pent, *a;        // by place
+  float2* lse;            // by place, in powers of two: the largest logit, log of the sum of exponentials ahead of it
   int32_t* pidx;          // by place, top each: the same
   float *pq, *picked;     // q and the logit there
   char *xb, *xh;          // by place: x in bf16, 64 columns of all tokens beside each other, and scaled in fp16, 256 columns
@@ -780,7 +781,9 @@ __global__ __launch_bounds__(T::kThreads) void head_logits_kernel(Head h, int pi
 }
 
 // Log-sum-exp and loss of TOKENS tokens, and (STORED) the logits at their targets
-// out of the stored ones. A token's numbers lie a piece apart, so eight
+// out of the stored ones. The largest logit and the logarithm stay two numbers, from
+// which a logit's distance is taken first: in one fp32 number a loss of 1e-6 at
+// logits of 100 would be off by 1e-5 (now by 1e-6 at most), and be negative at times. A token's numbers lie a piece apart, so eight
 // neighbours share what a load brings; few tokens take a workgroup each. Bound by
 // latency: 15 us for 4096 tokens with 1024 numbers each (34 MB).
 template <int TOKENS, bool STORED>
@@ -814,9 +817,12 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
     __syncthreads();
     if (part < width / 2) add(tops[tok][part + width / 2], sums[tok][part + width / 2]);
   }
-  if (part == 0) tops[tok][kParts] = broken ? NAN : top + log2f(sum);
+  if (part == 0) {
+    tops[tok][kParts] = top;
+    sums[tok][kParts] = broken ? NAN : log2f(sum);
+  }
   __syncthreads();
-  const float z = tops[tok][kParts] * kLn2;
+  const float2 z = {tops[tok][kParts], sums[tok][kParts]};
   float l = 0.0f;
   const int k = max(h.top, 1);
   if (live)
@@ -828,14 +834,15 @@ __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, 
       if constexpr (STORED) h.picked[at] = y = *logit_at(h, c, place);
       else y = h.picked[at];
       const float q = h.pq[at];
-      if (!(q == 0.0f)) l += q * (z - y);
+      const float far = z.y - __builtin_fmaf(y, kLog2e, -z.x);   // -log2 p, under 0 by rounding alone
+      if (!(q == 0.0f)) l += q * (far < 0.0f ? 0.0f : far * kLn2);
     }
   sums[tok][part] = l;
   __syncthreads();
   if (part || !live) return;
   l = 0.0f;
   for (int i = 0; i < min(k, kParts); ++i) l += sums[tok][i];
-  h.lse[mine] = tops[tok][kParts];
+  h.lse[mine] = z;
   loss[h.kept[mine]] = factor * (h.pent[mine] + l);
 }
 
@@ -870,7 +877,8 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
   static_assert(kDeltaTokens == kThreads / kWave * 8 && kUnits == kTileM / kPart, "a wave has its tokens");
   const int lane = threadIdx.x % kWave, place = t0 + threadIdx.x / 8, c1 = c0 + lane % 8 * 8;
   const float a = place < count ? h.a[first + place] : 0.0f;
-  const float z = a != 0.0f ? h.lse[first + place] : 0.0f, g = ldexpf(a, up);
+  const float2 z = a != 0.0f ? h.lse[first + place] : float2{};
+  const float g = ldexpf(a, up);
   f32x4 l[kUnits][2] = {};
   if (a != 0.0f) {
 #pragma unroll
@@ -889,7 +897,7 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[e] = exp2_of(__builtin_fmaf(l[u][e / 4][e % 4], kLog2e, -z));
+        p[e] = exp2_of(__builtin_fmaf(l[u][e / 4][e % 4], kLog2e, -z.x) - z.y);
         const float y = one_value(p[e] * g);
         hi[e] = static_cast<_Float16>(y);
         lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
@@ -915,7 +923,8 @@ __global__ __launch_bounds__(kThreads) void head_delta_kernel(Head h, int piece)
     }
     float q = 0.0f;
     for (int s = slot; s < k && h.pidx[at + s] == c; ++s) q += h.pq[at + s];
-    const float p = exp2_of(__builtin_fmaf(h.picked[at + slot], kLog2e, -h.lse[mine])) - q, y = one_value(p * ldexpf(a, up));
+    const float2 z = h.lse[mine];
+    const float p = exp2_of(__builtin_fmaf(h.picked[at + slot], kLog2e, -z.x) - z.y) - q, y = one_value(p * ldexpf(a, up));
     const uint32_t rounded = bf16_rne(p);
     *d16(to, c) = static_cast<uint16_t>(rounded);
     h.rest[at + slot] = p - __builtin_bit_cast(float, rounded << 16);
@@ -1245,7 +1254,7 @@ int head_shape(const rs_plan* p, int64_t tensor, int64_t n, int64_t top, bool gr
   s->kept = room(s->npad * 4);
   s->pent = room(s->npad * 4);
   s->a = room(s->npad * 4);
-  s->lse = room(s->npad * 4);
+  s->lse = room(s->npad * 8);
   s->pidx = room(s->npad * k * 4);
   s->pq = room(s->npad * k * 4);
   s->picked = room(s->npad * k * 4);
@@ -1414,7 +1423,7 @@ int run_head(rs_plan* p, HeadArgs a, bool grad, void* stream, const char* who) {
   h.kept = reinterpret_cast<int32_t*>(w + s.kept);
   h.pent = reinterpret_cast<float*>(w + s.pent);
   h.a = reinterpret_cast<float*>(w + s.a);
-  h.lse = reinterpret_cast<float*>(w + s.lse);
+  h.lse = reinterpret_cast<float2*>(w + s.lse);
   h.pidx = reinterpret_cast<int32_t*>(w + s.pidx);
   h.pq = reinterpret_cast<float*>(w + s.pq);
   h.picked = reinterpret_cast<float*>(w + s.picked);
