@@ -518,14 +518,16 @@ int rs_head_grad(rs_plan* plan, int64_t tensor, const void* gathered, const void
  * with both its shares. A teacher's logit of NaN or +inf makes the token's loss
  * NaN. ids: device, n_tokens x top integers of id_bytes; teacher: device,
  * n_tokens x top of teacher_dt (RS_F32 or RS_BF16), 16-byte aligned.
- * temperature: finite, above 0, as is its square. The rest as in rs_head_loss. */
+ * temperature: finite, above 0, as is its square; scale / temperature finite.
+ * The rest as in rs_head_loss. */
 int rs_distill_loss(rs_plan* plan, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* ids,
                     int32_t id_bytes, const void* teacher, int32_t teacher_dt, int64_t top, float temperature, float scale,
                     float* loss, int64_t piece, void* work, int64_t work_bytes, void* stream);
 
 /* The losses of rs_distill_loss and the gradients of their weighted sum as in
  * rs_head_grad, with p = softmax(l / T), q in e_y's place and
- * a_t = w_t * T * scale. The teacher's logits get no gradient. */
+ * a_t = w_t * T * scale, of which T * scale has to be finite. The teacher's logits
+ * get no gradient. */
 int rs_distill_grad(rs_plan* plan, int64_t tensor, const void* gathered, const void* x, int64_t n_tokens, const void* ids,
                     int32_t id_bytes, const void* teacher, int32_t teacher_dt, int64_t top, const float* weights,
                     float temperature, float scale, float* loss, void* dx, const float* prev, void* packed,

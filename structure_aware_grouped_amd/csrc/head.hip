@@ -1373,8 +1373,10 @@ int run_head(rs_plan* p, HeadArgs a, bool grad, void* stream, const char* who) {
   if ((a.teacher_dt != RS_F32 && a.teacher_dt != RS_BF16) || (grad && a.packed_dt != RS_F32 && a.packed_dt != RS_BF16))
     return fail(RS_EDTYPE, std::string(who) + ": fp32 or bf16");
   if (!std::isfinite(a.scale) || !(a.temperature > 0.0f) || !std::isfinite(a.temperature) || !std::isfinite(a.scale / a.temperature) ||
-      !std::isfinite(a.temperature * a.temperature))
-    return fail(RS_EINVAL, std::string(who) + ": scale must be finite, temperature finite and above 0");
+      !std::isfinite(a.temperature * a.temperature) || !(a.temperature * a.temperature > 0.0f))
+    return fail(RS_EINVAL, std::string(who) + ": scale and scale / temperature must be finite, temperature and its square finite and above 0");
+  if (grad && !std::isfinite(a.temperature * a.scale))
+    return fail(RS_EINVAL, std::string(who) + ": temperature * scale must be finite");
   if (grad && a.prev == a.packed && a.packed_dt != RS_F32)
     return fail(RS_EINVAL, std::string(who) + ": prev may be packed only when packed is fp32");
   if (grad && ((a.scale_mode != RS_SCALE_INV_V && a.scale_mode != RS_SCALE_GIVEN) || !std::isfinite(a.grad_scale)))

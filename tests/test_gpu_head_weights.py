@@ -60,3 +60,22 @@ def test_x_of_tokens_without_a_target_is_not_read(gpu_lib, top):
     for other in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
     case.plan.close()
+
+
+def test_temperatures_out_of_range_are_refused(gpu_lib):
+    """A temperature whose square is 0 in fp32, and gradients whose common factor temperature * scale is not finite."""
+    import structure_aware_grouped_amd as rs
+    n = 10
+    case = Case(rs, n, 100, 64, top=4)
+    packed, loss, dx = torch.full((case.total,), 3.0, device=DEV), torch.full((n,), 3.0, device=DEV), torch.full_like(case.x, 3.0)
+    work = case.work(rs, packed)
+    args = (case.plan, 1, case.gathered, case.x, case.ids, case.teacher)
+    for kw in ({"temperature": 1e-23}, {"temperature": 2.0 ** -76, "scale": 2.0 ** -20}):
+        with pytest.raises(rs.RsError):
+            rs.rs_distill_loss(*args, loss, work, **kw)
+        with pytest.raises(rs.RsError):
+            rs.rs_distill_grad(*args, loss, dx, packed, work, **kw)
+    with pytest.raises(rs.RsError):
+        rs.rs_distill_grad(*args, loss, dx, packed, work, temperature=1e18, scale=1e30)
+    assert bool((packed == 3).all()) and bool((loss == 3).all()) and bool((dx == 3).all())
+    case.plan.close()
