@@ -465,8 +465,9 @@ int rs_layer_norm_workspace(const rs_plan* plan, int64_t weight, int64_t n_rows,
  *   l = scale * (W x_t),   loss[t] = log(sum over r of exp(l_r)) - l_y
  * A target outside [0, rows) (e.g. -100) is none: its loss is +0.0, its x is
  * not read, and it costs next to nothing. The logits live in the workspace at
- * most. Products of bf16 values with fp32 sums; everything else is fp32. Sums
- * have a fixed order: the same call gives the same bits. A NaN or an infinity
+ * most. Products of bf16 values with fp32 sums; everything else is fp32, with the
+ * largest logit taken out first, so a loss is never negative. Sums have a fixed
+ * order: the same call gives the same bits. A NaN or an infinity
  * in x_t makes loss[t] NaN (one in W may make all of them NaN).
  * Any block kind but RS_TILEMAJOR. gathered: device, R_mat*S bf16 elements. x:
  * device, n_tokens x cols bf16, row-major. targets: device, n_tokens signed
@@ -492,10 +493,10 @@ int rs_head_loss(rs_plan* plan, int64_t tensor, const void* gathered, const void
  * on W's interval, sigma = grad_scale (RS_SCALE_GIVEN) or fl32(grad_scale / V)
  * (RS_SCALE_INV_V). A token without a target gets a dx of +0.0 and adds nothing,
  * and neither does one of weight 0, whatever its x holds. p - e_y is computed in
- * fp32; for dx it is rounded to bf16, and what that leaves at the target is added
- * in fp32. For the table's gradient a_t (p - e_y) is
- * rounded to 11 bits (a bf16 packed buffer) or 22 (fp32), or to within 2^-38 of
- * the largest |a_t| where that is more, and x to within 2^-38 of the largest |x|
+ * fp32; for dx it is rounded to bf16 (8 bits), and what that leaves at the target is
+ * added in fp32. For the table's gradient a_t (p - e_y) is rounded to 11 bits (a
+ * bf16 packed buffer) or 22 (fp32), or to within 2^-38 of the largest |a_t| where
+ * that is more, and x to within 2^-38 of the largest |x| of a token of weight not 0
  * (its bf16 values are exact down to 2^-28 of it). Sums are fp32.
  * W's interval is written whole (with n_tokens = 0 too; with prev = packed and
  * no targets it is left alone); other positions are left alone.

@@ -16,18 +16,22 @@
 // These are three products; nothing is computed twice. Tokens are taken in
 // pieces: a piece's logits are stored (fp32) with each row's running maximum
 // and sum per 128 columns, become d in place, and are used up by the piece's two
-// gradient products. Tokens without a target take part in none of them: the
+// gradient products. The maximum and the logarithm of the sum stay two numbers:
+// log p is a logit's distance from the first less the second, as exact for logits
+// of 100 as for those of 1. Tokens without a target take part in none of them: the
 // others are brought together first.
 //
 // Number formats. The logits' product takes the bf16 operands as they are, with
 // fp32 sums. d is computed in fp32 and rounded once for each of the two
 // products that read it: to bf16 for dx, whose result is bf16 too and whose
 // other operand is the table as gathered (range of bf16, no copy; what the
-// rounding leaves at the targets is added by itself); to fp16,
-// eight times finer, for dW, with x scaled to fp16 by a power of two. Where the
-// packed buffer is fp32, d has a second fp16 part that holds the rest of the
-// first, and its product comes ahead of the first's: the result is then as
-// near as fp32 products'.
+// rounding leaves at the targets is added by itself in fp32, all other rows keep
+// 8 bits); to fp16, eight times finer, for dW, with x scaled to fp16 by a power of
+// two. Where the packed buffer is fp32, a d has a second fp16 part that holds the
+// rest of the first, and its product comes ahead of the first's: 22 bits, as near
+// as fp32 products' for a d down to 2^-17 of the largest a. One scale serves the
+// whole call, so smaller ones are rounded to within 2^-38 of the largest a
+// (10 bits at 2^-29 of it, 0 below 2^-40), and x to within 2^-38 of the largest x.
 #include "host_common.h"
 #include "mfma.h"
 
@@ -185,7 +189,8 @@ struct HeadAcc {
 // A load into LDS holds its wave up while others are on their way, so loads in
 // one burst stop the multiplications: in one, dx of 4096 x 131072 x 4096 took
 // 3.84 ms, spread it takes 3.0 to 3.2 (1370 to 1460 TFLOP/s, the matrix cores busy
-// for 73 to 75% of it at 1.55 to 1.75 GHz; a library product of the size 2.8).
+// for 83% of it at 1.55 to 1.6 GHz; a library product of the size 2.8). For the
+// logits they are busy 66 to 74%, for dW 75 to 78%, at 1.5 to 1.7 GHz.
 template <class T, bool F16, bool PT, bool QT, bool RAGGED, bool PARTS>
 struct Contract {
 using FP = Fetch<kTileM, PT, RAGGED, false, T::kWaves>;
@@ -781,11 +786,12 @@ __global__ __launch_bounds__(T::kThreads) void head_logits_kernel(Head h, int pi
 }
 
 // Log-sum-exp and loss of TOKENS tokens, and (STORED) the logits at their targets
-// out of the stored ones. The largest logit and the logarithm stay two numbers, from
-// which a logit's distance is taken first: in one fp32 number a loss of 1e-6 at
-// logits of 100 would be off by 1e-5 (now by 1e-6 at most), and be negative at times. A token's numbers lie a piece apart, so eight
-// neighbours share what a load brings; few tokens take a workgroup each. Bound by
-// latency: 15 us for 4096 tokens with 1024 numbers each (34 MB).
+// out of the stored ones. The largest logit and the logarithm stay two numbers, and
+// a logit's distance is taken from the first ahead of the second: added up in one
+// fp32 number, a loss of 1e-6 at logits of 100 is off by up to 9e-6 and negative at
+// times (so by 1e-6 at most, and never). A token's numbers lie a piece apart, so
+// eight neighbours share what a load brings; few tokens take a workgroup each. Bound
+// by latency: 15 us for 4096 tokens with 1024 numbers each (34 MB).
 template <int TOKENS, bool STORED>
 __global__ __launch_bounds__(kThreads) void head_loss_kernel(Head h, int piece, int stats, float factor, float* loss) {
   constexpr int kParts = kThreads / TOKENS;
@@ -1132,7 +1138,9 @@ __device__ __forceinline__ void keep_dw_odd(const Head& h, const TileAt& at, con
 // CU, with tile after tile (512 tokens, 131072 x 1024: 259 us, one tile a workgroup
 // 285). Bound by the matrix cores: 1250 TFLOP/s with
 // two parts, 1170 with one; for few tokens by the tiles' stores, one CU with one
-// tile at a time.
+// tile at a time. The tokens of a piece are not split: a small table has few tiles,
+// whose CUs walk all of them (the whole call on 1000 x 64 with 2048, 8192, 16384
+// tokens, fp32: 134, 354, 698 us).
 template <bool TWO, bool OUT16>
 __global__ __launch_bounds__(DwTile::kThreads) void head_dw_kernel(Head h, int piece, float sigma, const float* in, void* out) {
   using T = DwTile;

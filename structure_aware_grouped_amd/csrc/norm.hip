@@ -195,8 +195,10 @@ struct NormCall {
   bool center;
 };
 
-// y of every G-th row. Bound by memory: 16384 rows of 8192 bf16 in 81 us, 6.6 TB/s,
-// with streaming stores that no barrier waits for.
+// y of every G-th row. Bound by memory: 16384 rows of 8192 bf16 in 80 to 82 us, 6.6
+// TB/s (a call 94), with streaming stores that no barrier waits for. Widths that are
+// no multiple of 8 by their single-element accesses: 4097 bf16 rows of 1001, 5001 and
+// 9001 in 17, 118 and 210 us a call; above 8192 these spill 14 registers.
 template <bool IN16, bool OUT16, bool VEC, int VPT>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormCall c, const void* x, void* y) {
   __shared__ __attribute__((aligned(16))) float red[4 * kMaxWaves];
@@ -227,8 +229,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormCall c, const vo
 
 // dx of every G-th row, and the workgroup's share of dw and db. Bound by the
 // latency of a row's load and two sums, with as many rows in flight as the
-// registers allow: 16384 rows of 8192 bf16 in 160 to 170 us, 5.0 TB/s; rows of odd
-// width by their single-element accesses (4097 x 1001 fp32: 18 us).
+// registers allow: 16384 rows of 8192 bf16 in 152 to 172 us, 4.7 to 5.3 TB/s (a call
+// 166; 138 for the RMS norm, which keeps db and the sum of g all the same); rows of
+// odd width by their single-element accesses (4097 x 1001 fp32: 19 us, and a call
+// 29), above 4096 columns also by what the loop over rows spills, 103 to 137 of its
+// registers: 4097 x 5001 and 9001 fp32 210 and 340 us a call, 1.0 and 1.1 TB/s.
 template <bool IN16, bool DY16, bool P16, bool VEC, int VPT>
 __global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(NormCall c, const void* x, const void* dy, void* dx, float* part) {
   __shared__ __attribute__((aligned(16))) float red[4 * kMaxWaves];
@@ -334,7 +339,9 @@ struct NormShape {
 // columns: forwards 512 threads with two vectors each and 8192 threads a CU take
 // 82 us (4096: 84, 2048: 96; 256 threads with four 84; 1024 with one 110);
 // backwards 512 with two and 1024 a CU 161 (1024 with one 216, 256 with four 210;
-// 1536 a CU 218), where more workgroups mean more shares to add up.
+// 1536 a CU 218), where more workgroups mean more shares to add up. Narrow rows have
+// the most of these, 128 threads a row and 2048 shares for 4097 x 1001: their 16 MB
+// are written and read beside 41 MB of data (65536 x 64 bf16: 52 us a call, 0.5 TB/s).
 NormShape norm_shape(int64_t n, int64_t cols, int vmost, int most, int64_t per_cu) {
   NormShape s{kWave, 1, 0};
   while (s.vpt < vmost && s.threads * 8 * s.vpt < cols) s.vpt *= 2;
